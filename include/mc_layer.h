@@ -462,6 +462,164 @@ int mc_attention_backward_cp(const uint16_t* qkv, const uint16_t* o, const float
                              int32_t head_dim, int32_t cp_parts, void* workspace,
                              size_t workspace_bytes, int* status, void* stream);
 
+/* ---- Rotary positions, interval masks and attention over them.
+ *
+ * Stages beside mc_attention_forward / _backward for tokens that carry
+ * positions and for sequences that are not one causal document: several
+ * documents packed into a sequence, prefixes that see themselves whole,
+ * sliding windows, padding; scores capped by a tanh or biased by the
+ * distance.  The layer runs them through mc_layer_forward_opt /
+ * mc_layer_backward_opt. */
+
+/* Rotary positions.  Pair p of a head turns by the angle
+ * positions[x(p)][t] * inv_freq[p] of token t, x(p) being the pair's axis
+ * (one for text; time, height and width for images and video):
+ *   (u, v) -> (u cos w - v sin w, u sin w + v cos w).
+ * rot_dim (even, <= head_dim) leading dimensions of a head turn, the others
+ * stay.  Pairs are dimensions (p, p + rot_dim / 2), or (2p, 2p + 1) with
+ * MC_ROTARY_ADJACENT_PAIRS.  sections[x] pairs belong to axis x (their sum is
+ * rot_dim / 2): the first sections[0] pairs to axis 0 and so on, or, with
+ * MC_ROTARY_DEAL_AXES, dealt in turn (0, 1, 2, 0, 1, 2, ...), an axis leaving
+ * the round when its section is used up. */
+#define MC_ROTARY_MAX_AXES 4
+#define MC_ROTARY_ADJACENT_PAIRS 1u
+#define MC_ROTARY_DEAL_AXES 2u
+typedef struct mc_rotary_spec {
+  int32_t rot_dim;
+  int32_t axes; /* 1 .. MC_ROTARY_MAX_AXES */
+  int32_t sections[MC_ROTARY_MAX_AXES];
+  uint32_t flags; /* MC_ROTARY_ADJACENT_PAIRS | MC_ROTARY_DEAL_AXES, or 0 */
+} mc_rotary_spec;
+
+/* Turns `heads` heads of head_dim elements at the start of each of `tokens`
+ * rows (row strides ld_in, ld_out >= heads * head_dim, in elements; what lies
+ * behind the heads in a row is neither read nor written): fp32, or bf16 when
+ * is_bf16 != 0, rounded once.  Over the Q and K of a packed Q|K|V row:
+ * heads = 2 H, ld = 3a.  positions: int32 [axes, tokens], any value (angles
+ * are formed in 64 bits); inv_freq: fp32 [rot_dim / 2], finite.  out == in
+ * (with the same stride) turns in place; otherwise they must not overlap.
+ * rot_dim <= 512.  Vectors of 16 bytes are used where rot_dim / 2, head_dim,
+ * the strides and the addresses are multiples of them, else smaller ones. */
+int mc_rotary_forward(const void* in, void* out, int32_t is_bf16, int64_t tokens, int32_t heads,
+                      int32_t head_dim, int64_t ld_in, int64_t ld_out, const int32_t* positions,
+                      const float* inv_freq, const mc_rotary_spec* spec, int* status,
+                      void* stream);
+
+/* The gradient of mc_rotary_forward's input from its output's: the same
+ * pairs turned by the opposite angle. */
+int mc_rotary_backward(const void* dout, void* din, int32_t is_bf16, int64_t tokens,
+                       int32_t heads, int32_t head_dim, int64_t ld_dout, int64_t ld_din,
+                       const int32_t* positions, const float* inv_freq,
+                       const mc_rotary_spec* spec, int* status, void* stream);
+
+/* Interval masks: query i of a sequence sees its keys [key_lo[i], key_hi[i])
+ * (int32 [micro_batch, seq_len], indices within the sequence; an interval
+ * with lo >= hi is empty: such a row gives O = 0, log-sum-exp = -infinity and
+ * no gradients).  `tables` summarises them per block of 128 rows for the
+ * attention kernels (device memory, 16-byte aligned,
+ * mc_attention_mask_table_ints int32, n = micro_batch * ceil(seq_len / 128)):
+ *   n entries {sequence, query block, lo, hi}: the union of the block's
+ *     intervals ({.., 0, 0}: none), then
+ *   n entries {sequence, key block, first, end}: the query blocks whose
+ *     union meets the key block ({.., 0, 0}: none),
+ * each sorted by the length of its range, longest first, ties in order of
+ * sequence and block (more than 4096 entries: unsorted, the query entries
+ * from the last to the first).  A mask is made once per batch and used by
+ * every layer, forward and backward. */
+size_t mc_attention_mask_table_ints(int32_t micro_batch, int32_t seq_len);
+
+/* Intervals and tables of packed documents: document k owns the tokens
+ * [offsets[k], offsets[k + 1]) of the micro_batch * seq_len tokens (int32
+ * [n_docs + 1], ascending; documents of length 0 are fine, one that runs
+ * over the end of a sequence is cut there; tokens before the first and after
+ * the last document see nothing).  A token sees the keys of its own document
+ * up to itself (causal != 0; else all of them), its document's first
+ * prefix[k] tokens whole (prefix: int32 [n_docs], or NULL for none; a
+ * negative one marks padding, whose tokens see nothing), and of those only
+ * keys less than `window` away (0: no limit).  Writes key_lo, key_hi and
+ * `tables`. */
+int mc_attention_mask_documents(const int32_t* offsets, int32_t n_docs, const int32_t* prefix,
+                                int32_t causal, int32_t window, int32_t micro_batch,
+                                int32_t seq_len, int32_t* key_lo, int32_t* key_hi,
+                                int32_t* tables, int* status, void* stream);
+
+/* The tables of the caller's own intervals (bounds outside the sequence are
+ * cut to it).  The attention visits every key block between the lowest and
+ * the highest visible key of a query block. */
+int mc_attention_mask_intervals(int32_t micro_batch, int32_t seq_len, const int32_t* key_lo,
+                                const int32_t* key_hi, int32_t* tables, int* status,
+                                void* stream);
+
+/* What mc_attention_forward_opt / _backward_opt compute beyond plain causal
+ * attention.  With z = q k / sqrt(d):
+ *   softcap > 0:     z <- softcap * tanh(z / softcap)
+ *   slopes != NULL:  z <- z - slopes[head] * |query - key| (fp32 [heads];
+ *                    constants: they get no gradient)
+ * then the softmax over the keys of the query's interval.  causal != 0 states
+ * that no interval reaches past its own query (key_hi[i] <= i + 1), which
+ * halves the backward's workspace; an interval that does is then reported as
+ * MC_ERR_DEVICE_BOUNDS in `status` and the gradients are not valid. */
+typedef struct mc_attention_options {
+  const int32_t* key_lo;
+  const int32_t* key_hi;
+  const int32_t* tables; /* made from key_lo / key_hi for the same shape */
+  const float* slopes;   /* or NULL */
+  float softcap;         /* 0: none */
+  int32_t causal;
+} mc_attention_options;
+
+/* mc_attention_forward over an interval mask: same layouts, types and errors
+ * (lse is -infinity for a row that sees nothing).  MC_ERR_ARGUMENT for a
+ * negative or non-finite softcap.  Values in rows that a query does not see
+ * have no influence as long as they are finite: a NaN or infinity in K or V
+ * can reach the other queries of blocks that hold it. */
+int mc_attention_forward_opt(const uint16_t* qkv, uint16_t* o, float* lse, int32_t micro_batch,
+                             int32_t seq_len, int32_t heads, int32_t head_dim,
+                             const mc_attention_options* options, int* status, void* stream);
+
+/* Bytes of the dS workspace of mc_attention_backward_opt for these options
+ * (only options->causal is read; the pointers in it are not): one 32 KB tile
+ * per pair of 128-row blocks, of the lower triangle when causal.  0 for an
+ * invalid shape. */
+size_t mc_attention_backward_opt_ws_bytes(int32_t micro_batch, int32_t seq_len, int32_t heads,
+                                          int32_t head_dim, const mc_attention_options* options);
+
+/* mc_attention_backward over an interval mask.  With `ds_workspace`
+ * (mc_attention_backward_opt_ws_bytes, 16-byte aligned; too small ->
+ * MC_ERR_WORKSPACE) dQ is formed from dS tiles as in
+ * mc_attention_backward_ws; with NULL the scores are formed a second time. */
+int mc_attention_backward_opt(const uint16_t* qkv, const uint16_t* o, const float* lse,
+                              const uint16_t* dout, uint16_t* dqkv, float* delta,
+                              int32_t micro_batch, int32_t seq_len, int32_t heads,
+                              int32_t head_dim, const mc_attention_options* options,
+                              void* ds_workspace, size_t ds_workspace_bytes, int* status,
+                              void* stream);
+
+/* The layer with positions and / or an interval mask in its attention stage
+ * (either may be NULL; both NULL is mc_layer_forward / _backward, to the
+ * bit): after the QKV projection `rotary` turns Q and K (it sees head_dim =
+ * the layer's, tokens = T), `attention` replaces the causal mask and scores;
+ * in the backward pass dQ and dK are turned back.  The backward call gets the
+ * same two as its forward call.  All shape flags combine with them;
+ * mc_layer_workspace_bytes covers the dS tiles of a causal mask, and
+ * mc_layer_workspace_bytes_opt those of any. */
+typedef struct mc_layer_rotary {
+  mc_rotary_spec spec;
+  const int32_t* positions; /* [axes, T] */
+  const float* inv_freq;    /* [rot_dim / 2] */
+} mc_layer_rotary;
+
+size_t mc_layer_workspace_bytes_opt(const mc_layer_shape* shape,
+                                    const mc_attention_options* attention);
+int mc_layer_forward_opt(const mc_layer_shape* shape, const mc_layer_weights* w,
+                         const mc_layer_rotary* rotary, const mc_attention_options* attention,
+                         const float* x, float* y, void* saved, void* ws, size_t ws_bytes,
+                         void* stream);
+int mc_layer_backward_opt(const mc_layer_shape* shape, const mc_layer_weights* w,
+                          const mc_layer_rotary* rotary, const mc_attention_options* attention,
+                          const float* x, const float* dy, const void* saved, float* dx,
+                          const mc_layer_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -69,6 +69,27 @@ class mc_layer_grads(ctypes.Structure):  # noqa: N801
     _fields_ = [(n, ctypes.c_void_p) for n in PARAM_ORDER]
 
 
+MC_ROTARY_MAX_AXES = 4
+MC_ROTARY_ADJACENT_PAIRS = 1
+MC_ROTARY_DEAL_AXES = 2
+
+
+class mc_rotary_spec(ctypes.Structure):  # noqa: N801
+    _fields_ = [("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * MC_ROTARY_MAX_AXES), ("flags", ctypes.c_uint32)]
+
+
+class mc_attention_options(ctypes.Structure):  # noqa: N801
+    _fields_ = [("key_lo", ctypes.c_void_p), ("key_hi", ctypes.c_void_p),
+                ("tables", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("softcap", ctypes.c_float), ("causal", ctypes.c_int32)]
+
+
+class mc_layer_rotary(ctypes.Structure):  # noqa: N801
+    _fields_ = [("spec", mc_rotary_spec), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -76,6 +97,9 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+
+_OPT = ctypes.POINTER(mc_attention_options)
+_ROT = ctypes.POINTER(mc_layer_rotary)
 
 _SIGNATURES = {
     "mc_layer_check_shape": (_INT, [ctypes.POINTER(mc_layer_shape)]),
@@ -113,6 +137,25 @@ _SIGNATURES = {
     "mc_attention_forward_cp": (_INT, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P]),
     "mc_attention_backward_cp": (_INT, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P,
                                         _SZ, _P, _P]),
+    "mc_rotary_forward": (_INT, [_P, _P, _I32, _I64, _I32, _I32, _I64, _I64, _P, _P,
+                                 ctypes.POINTER(mc_rotary_spec), _P, _P]),
+    "mc_rotary_backward": (_INT, [_P, _P, _I32, _I64, _I32, _I32, _I64, _I64, _P, _P,
+                                  ctypes.POINTER(mc_rotary_spec), _P, _P]),
+    "mc_attention_mask_table_ints": (_SZ, [_I32, _I32]),
+    "mc_attention_mask_documents": (_INT, [_P, _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                           _P]),
+    "mc_attention_mask_intervals": (_INT, [_I32, _I32, _P, _P, _P, _P, _P]),
+    "mc_attention_forward_opt": (_INT, [_P, _P, _P, _I32, _I32, _I32, _I32, _OPT, _P, _P]),
+    "mc_attention_backward_opt_ws_bytes": (_SZ, [_I32, _I32, _I32, _I32, _OPT]),
+    "mc_attention_backward_opt": (_INT, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _OPT, _P,
+                                         _SZ, _P, _P]),
+    "mc_layer_workspace_bytes_opt": (_SZ, [ctypes.POINTER(mc_layer_shape), _OPT]),
+    "mc_layer_forward_opt": (_INT, [ctypes.POINTER(mc_layer_shape),
+                                    ctypes.POINTER(mc_layer_weights), _ROT, _OPT, _P, _P, _P, _P,
+                                    _SZ, _P]),
+    "mc_layer_backward_opt": (_INT, [ctypes.POINTER(mc_layer_shape),
+                                     ctypes.POINTER(mc_layer_weights), _ROT, _OPT, _P, _P, _P, _P,
+                                     ctypes.POINTER(mc_layer_grads), _P, _SZ, _P]),
 }
 
 
@@ -333,6 +376,122 @@ def mc_gemm_fp8(M, N, K, A, lda, a_format, B, ldb, b_format, a_scale_inv, b_scal
                              _ptr(a_scale_inv), _ptr(b_scale_inv), _ptr(out), ldc, epilogue,
                              _ptr(bias), _ptr(aux), ldaux, accumulate, k_parts, _ptr(status),
                              _stream(stream))
+
+
+# ---- rotary positions, interval masks and attention over them
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def make_rotary_spec(rot_dim, sections=None, interleaved_pairs=False, interleaved_axes=False):
+    """`sections`: pairs of each axis (default: one axis).  `interleaved_pairs`:
+    pairs are neighbours (2p, 2p + 1); `interleaved_axes`: axes dealt in turn."""
+    sections = [rot_dim // 2] if sections is None else [int(x) for x in sections]
+    if not 1 <= len(sections) <= MC_ROTARY_MAX_AXES:
+        raise ValueError(f"1 to {MC_ROTARY_MAX_AXES} axes, got {len(sections)}")
+    flags = (MC_ROTARY_ADJACENT_PAIRS if interleaved_pairs else 0) | \
+        (MC_ROTARY_DEAL_AXES if interleaved_axes else 0)
+    return mc_rotary_spec(rot_dim, len(sections), (ctypes.c_int32 * MC_ROTARY_MAX_AXES)(*sections),
+                          flags)
+
+
+def make_layer_rotary(spec, positions, inv_freq):
+    """Keeps a reference to the tensors it points to."""
+    out = mc_layer_rotary(spec, _ptr(positions), _ptr(inv_freq))
+    out.tensors = (positions, inv_freq)
+    return out
+
+
+def make_attention_options(key_lo, key_hi, tables, slopes=None, softcap=0.0, causal=True):
+    """Keeps a reference to the tensors it points to."""
+    out = mc_attention_options(_ptr(key_lo), _ptr(key_hi), _ptr(tables), _ptr(slopes),
+                               float(softcap), 1 if causal else 0)
+    out.tensors = (key_lo, key_hi, tables, slopes)
+    return out
+
+
+def _is_bf16(x):
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"rotary positions take bf16 or fp32, got {x.dtype}")
+    return 1 if x.dtype == torch.bfloat16 else 0
+
+
+def mc_rotary_forward(x, out, tokens, heads, head_dim, ld_in, ld_out, positions, inv_freq, spec,
+                      status=None, stream=None) -> int:
+    """Rotary positions over `heads` heads at the start of each row of x (a
+    bf16 or fp32 tensor; `out` of the same type, or x itself)."""
+    if out.dtype != x.dtype:
+        raise TypeError(f"rotary positions: {x.dtype} in, {out.dtype} out")
+    return lib().mc_rotary_forward(_ptr(x), _ptr(out), _is_bf16(x), tokens, heads, head_dim, ld_in,
+                                   ld_out, _ptr(positions), _ptr(inv_freq), ctypes.byref(spec),
+                                   _ptr(status), _stream(stream))
+
+
+def mc_rotary_backward(dout, din, tokens, heads, head_dim, ld_dout, ld_din, positions, inv_freq,
+                       spec, status=None, stream=None) -> int:
+    if din.dtype != dout.dtype:
+        raise TypeError(f"rotary positions: {dout.dtype} in, {din.dtype} out")
+    return lib().mc_rotary_backward(_ptr(dout), _ptr(din), _is_bf16(dout), tokens, heads, head_dim,
+                                    ld_dout, ld_din, _ptr(positions), _ptr(inv_freq),
+                                    ctypes.byref(spec), _ptr(status), _stream(stream))
+
+
+def mc_attention_mask_table_ints(micro_batch, seq_len) -> int:
+    return lib().mc_attention_mask_table_ints(micro_batch, seq_len)
+
+
+def mc_attention_mask_documents(offsets, n_docs, prefix, causal, window, micro_batch, seq_len,
+                                key_lo, key_hi, tables, status=None, stream=None) -> int:
+    return lib().mc_attention_mask_documents(_ptr(offsets), n_docs, _ptr(prefix), causal, window,
+                                             micro_batch, seq_len, _ptr(key_lo), _ptr(key_hi),
+                                             _ptr(tables), _ptr(status), _stream(stream))
+
+
+def mc_attention_mask_intervals(micro_batch, seq_len, key_lo, key_hi, tables, status=None,
+                                stream=None) -> int:
+    return lib().mc_attention_mask_intervals(micro_batch, seq_len, _ptr(key_lo), _ptr(key_hi),
+                                             _ptr(tables), _ptr(status), _stream(stream))
+
+
+def mc_attention_forward_opt(qkv, o, lse, micro_batch, seq_len, heads, head_dim, options,
+                             status=None, stream=None) -> int:
+    return lib().mc_attention_forward_opt(_ptr(qkv), _ptr(o), _ptr(lse), micro_batch, seq_len,
+                                          heads, head_dim, _ref(options), _ptr(status),
+                                          _stream(stream))
+
+
+def mc_attention_backward_opt_ws_bytes(micro_batch, seq_len, heads, head_dim, options) -> int:
+    return lib().mc_attention_backward_opt_ws_bytes(micro_batch, seq_len, heads, head_dim,
+                                                    _ref(options))
+
+
+def mc_attention_backward_opt(qkv, o, lse, dout, dqkv, delta, micro_batch, seq_len, heads,
+                              head_dim, options, ds_workspace=None, ds_workspace_bytes=0,
+                              status=None, stream=None) -> int:
+    return lib().mc_attention_backward_opt(_ptr(qkv), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dqkv),
+                                           _ptr(delta), micro_batch, seq_len, heads, head_dim,
+                                           _ref(options), _ptr(ds_workspace), ds_workspace_bytes,
+                                           _ptr(status), _stream(stream))
+
+
+def mc_layer_workspace_bytes_opt(shape, attention) -> int:
+    return lib().mc_layer_workspace_bytes_opt(ctypes.byref(shape), _ref(attention))
+
+
+def mc_layer_forward_opt(shape, weights, rotary, attention, x, y, saved, ws, ws_bytes,
+                         stream=None) -> int:
+    return lib().mc_layer_forward_opt(ctypes.byref(shape), ctypes.byref(weights), _ref(rotary),
+                                      _ref(attention), _ptr(x), _ptr(y), _ptr(saved), _ptr(ws),
+                                      ws_bytes, _stream(stream))
+
+
+def mc_layer_backward_opt(shape, weights, rotary, attention, x, dy, saved, dx, grads, ws, ws_bytes,
+                          stream=None) -> int:
+    return lib().mc_layer_backward_opt(ctypes.byref(shape), ctypes.byref(weights), _ref(rotary),
+                                       _ref(attention), _ptr(x), _ptr(dy), _ptr(saved), _ptr(dx),
+                                       ctypes.byref(grads), _ptr(ws), ws_bytes, _stream(stream))
 
 
 def mc_selftest_bounds_check(index, extent, buf, status, stream=None) -> int:

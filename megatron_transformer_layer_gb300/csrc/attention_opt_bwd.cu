@@ -1,0 +1,1026 @@
+// Attention backward over interval masks (sm_103a, tcgen05), scores optionally
+// capped by a tanh and biased by the distance.  With P = exp(z - lse) over the
+// visible keys, delta = rowsum(dO O) and t = tanh of the capped score:
+//   dV = P^T dO,  dP = dO V^T,  dz = P (dP - delta) (1 - t^2),
+//   dQ = dz K / sqrt(d),  dK = dz^T Q / sqrt(d).
+// Masked places get P = 0 by a select, so rows that see nothing (lse =
+// -infinity) give and receive nothing.
+//
+//   dkdv: a 128-key block against the query blocks that see it (the mask's
+//         key table), accumulates dV and dK and, given a workspace, writes
+//         each block pair's dz^T tile as bf16.
+//   dq:   a 128-query block: with the tiles dQ is their product with K
+//         (persistent, bound by the tiles' traffic); without, S and dP are
+//         formed again.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attention_opt.cuh"
+
+namespace mc {
+namespace {
+
+constexpr int kOptBwdThreads = 320;  // producer, MMA, 8 compute warps
+constexpr int64_t kOptTileBytes = 128 * 128 * 2;  // one bf16 dz^T tile (128 keys x 128 queries)
+
+struct OptBwdArgs {
+  uint16_t* dqkv;
+  const float* lse;
+  const float* delta;
+  const int32_t* key_lo;
+  const int32_t* key_hi;
+  const int32_t* tables;  // the query entries; the key entries follow
+  const float* slopes;
+  uint8_t* ds_tiles;
+  float softcap;
+  int b, s, H;
+  int head_major;
+  int causal;  // the tiles are of the lower triangle only
+  int* status;
+};
+
+// Tile (query block, key block) of a (head, batch) in the workspace.
+__device__ __forceinline__ int64_t opt_tile(int causal, int nb, int64_t hb, int qb, int kb) {
+  const int64_t n = nb;
+  return causal ? hb * (n * (n + 1) / 2) + static_cast<int64_t>(qb) * (qb + 1) / 2 + kb
+                : (hb * n + qb) * n + kb;
+}
+
+// ---------------------------------------------------------------- dK, dV
+template <int D>
+struct OptBwdCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTile = 128 * D * 2;
+  // K, V, two (Q_i, dO_i) stages, the dz^T tile staged for its bulk store,
+  // lse / delta [2][128], the queries' key ranges relative to the block
+  // [2][128] (two bytes each), their edge flags [2][4], barriers.  The
+  // dynamic shared memory starts 1024-byte aligned (checked at run time).
+  static constexpr int kUsed = 6 * kTile + static_cast<int>(kOptTileBytes) + 4 * 128 * 4 +
+                               2 * 128 * 2 + 2 * 4 * 4 + 24 * 8;
+  // one CTA per SM: it takes all 512 TMEM columns
+  static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kUsed <= 227 * 1024, "dkdv kernel shared memory");
+};
+
+// TMEM: S^T [0, 128), dP^T [128, 256), dV [256, 256 + D), dK [384, 384 + D).
+// Per query block i:
+//   MMA      S^T_i = K Q_i^T (as soon as the compute warps hold S^T_{i-1} in
+//            registers), then dV += P^T_{i-1} dO_{i-1}, dK += dz^T_{i-1} Q_{i-1},
+//            then (those done) dP^T_i = V dO_i^T.
+//   compute  P^T (and the cap's derivative) from S^T_i while the products
+//            above run, then dz^T from dP^T_i.
+// A compute thread owns one key row and 64 query columns: the 16 queries of
+// group g (dP^T columns [16g, 16g + 16)) leave P at columns [16g, 16g + 8)
+// and dz at [16g + 8, 16g + 16), over columns that the thread itself has read.
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kOptBwdThreads, 1)
+    attn_opt_dkdv_kernel(const __grid_constant__ CUtensorMap tm_qkv,
+                         const __grid_constant__ CUtensorMap tm_do,
+                         const __grid_constant__ OptBwdArgs A) {
+  using C = OptBwdCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  int* status = A.status;
+  if (smem_u32(smem) & 1023u) {  // the 128-byte swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) record_error(status, MC_ERR_DEVICE_BOUNDS, kSiteAttention);
+    return;
+  }
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + C::kTile;
+  uint8_t* sQ[2] = {smem + 2 * C::kTile, smem + 3 * C::kTile};
+  uint8_t* sdO[2] = {smem + 4 * C::kTile, smem + 5 * C::kTile};
+  uint8_t* sDs = smem + 6 * C::kTile;  // dz^T tile image (swizzled), 32 KB
+  float* sL = reinterpret_cast<float*>(sDs + kOptTileBytes);  // [2][128] lse * log2(e)
+  float* sD = sL + 256;                                        // [2][128] delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + 256);
+  uint64_t* r_full = bars + 0;
+  uint64_t* st_full = bars + 1;    // [2]
+  uint64_t* st_empty = bars + 3;   // [2]
+  uint64_t* s_full = bars + 5;     // S^T_i in TMEM
+  uint64_t* s_free = bars + 6;     // compute warps hold S^T_i in registers
+  uint64_t* dp_full = bars + 7;    // dP^T_i in TMEM
+  uint64_t* p_full = bars + 8;     // P^T_i, dz^T_i in TMEM
+  uint64_t* acc_done = bars + 9;   // dV, dK products of block i complete
+  uint64_t* drain = bars + 10;
+  uint64_t* lse_ready = bars + 11;  // [2]
+  uint64_t* ds_full = bars + 13;    // the dz^T tile of block i is in sDs (256 threads)
+  uint64_t* ds_free = bars + 14;    // its bulk store has read sDs
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 24);  // [2][128] first | end << 8
+  int* sF = reinterpret_cast<int*>(sM + 256);             // [2][4] the 32 queries see the whole block
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = A.s, H = A.H, a = A.H * D;
+  const int nb = (s + 127) / 128;
+  if (threadIdx.x == 0) {
+    mbar_init(r_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&st_full[i], 1);
+      mbar_init(&st_empty[i], 1);
+      mbar_init(&lse_ready[i], 256);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 256);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 256);
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(ds_full, 256);
+    mbar_init(ds_free, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_qkv);
+    tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the previous kernel on the stream has completed
+  const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 384;
+
+  int4 entry;  // sequence, key block, first and end of the query blocks that see it
+  int hh;
+  const bool ok_entry = opt_entry(A.tables + 4ll * A.b * nb, A.head_major != 0, A.b, nb, entry, hh,
+                                  status);
+  const int bi = entry.x, kb = entry.y;
+  const int r0 = kb * 128;
+  const int qb0 = max(entry.z, 0);
+  const int count = ok_entry ? max(min(entry.w, nb) - qb0, 0) : 0;
+
+  if (warp == 0) {
+    if (lane == 0 && count > 0) {
+      // -------------------------------------------------------- producer
+      const int cq = hh * D, ck = a + hh * D, cv = 2 * a + hh * D;
+      mbar_arrive_expect_tx(r_full, 2 * C::kTile);
+      for (int c = 0; c < C::kChunks; ++c) {
+        tma_load_3d(sK + c * 16384, &tm_qkv, r_full, ck + c * 64, r0, bi);
+        tma_load_3d(sV + c * 16384, &tm_qkv, r_full, cv + c * 64, r0, bi);
+      }
+      int issued = 0;
+      for (int i = 0; i < count; ++i) {
+        const int st = i & 1;
+        const int row = (qb0 + i) * 128;
+        if (!mbar_wait(&st_empty[st], ((i >> 1) & 1) ^ 1u, status, kSiteAttention)) break;
+        mbar_arrive_expect_tx(&st_full[st], 2 * C::kTile);
+        for (int c = 0; c < C::kChunks; ++c) {
+          tma_load_3d(sQ[st] + c * 16384, &tm_qkv, &st_full[st], cq + c * 64, row, bi);
+          tma_load_3d(sdO[st] + c * 16384, &tm_do, &st_full[st], hh * D + c * 64, row, bi);
+        }
+        ++issued;
+      }
+      pdl_launch();  // every load of this CTA is issued
+      mbar_wait(r_full, 0, status, kSiteAttention, 200000000ull, false);
+      for (int i = issued - 1; i >= 0 && i >= issued - 2; --i)
+        mbar_wait(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention, 200000000ull, false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && count > 0) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+      bool ok = mbar_wait(r_full, 0, status, kSiteAttention);
+      const uint32_t kbase = smem_u32(sK), vbase = smem_u32(sV);
+      for (int i = 0; ok && i <= count; ++i) {
+        const int st = i & 1;
+        if (i < count) {
+          if (!mbar_wait(&st_full[st], (i >> 1) & 1, status, kSiteAttention)) break;
+          // tS was read into registers for block i - 1.
+          if (i > 0 && !mbar_wait(s_free, (i - 1) & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint32_t qb = smem_u32(sQ[st]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_bf16(tS, smem_desc_sw128(kbase + off, 16, 1024), smem_desc_sw128(qb + off, 16, 1024),
+                      kIdescSq, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(s_full);
+        }
+        if (i > 0) {
+          const int pi = i - 1, pst = pi & 1;
+          if (!mbar_wait(p_full, pi & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint32_t qb = smem_u32(sQ[pst]), dob = smem_u32(sdO[pst]);
+#pragma unroll
+          for (int kk = 0; kk < 128 / 16; ++kk) {
+            // 16 queries = group kk: P at 16 kk, dz at 16 kk + 8; B tiles viewed MN-major
+            const uint32_t pcol = static_cast<uint32_t>(kk * 16);
+            const uint32_t acc = (pi > 0 || kk > 0) ? 1u : 0u;
+            umma_bf16_ts(tdV, tdP + pcol, smem_desc_sw128(dob + kk * 2048, 16384, 1024), kIdescAcc,
+                         acc);
+            umma_bf16_ts(tdK, tdP + pcol + 8, smem_desc_sw128(qb + kk * 2048, 16384, 1024),
+                         kIdescAcc, acc);
+          }
+          umma_commit(&st_empty[pst]);
+          umma_commit(acc_done);
+        }
+        if (i < count) {
+          // dP^T_i overwrites the P^T / dz^T that the products above read.
+          if (i > 0 && !mbar_wait(acc_done, (i - 1) & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint32_t dob = smem_u32(sdO[st]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_bf16(tdP, smem_desc_sw128(vbase + off, 16, 1024),
+                      smem_desc_sw128(dob + off, 16, 1024), kIdescSq, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(dp_full);
+        }
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+    }
+  } else {
+    // ---------------------------------------------------------- compute
+    // Two warps per TMEM lane quarter; `half` picks 64 of the 128 query columns.
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const int t = quarter * 32 + lane;  // key row within the block
+    const int r = r0 + t;               // this thread's key
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t my_cols = lane_off + static_cast<uint32_t>(half * 64);
+    const ScoreConst sc =
+        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, A.slopes, hh);
+    const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s;  // of lse and delta
+    const int64_t brow = static_cast<int64_t>(bi) * s;             // of the intervals
+    // What query t of the next block brings, loaded one block ahead (half 0).
+    // Queries past the sequence see the whole block: their Q and dO are zeros.
+    float nl2 = 0.f, nd = 0.f;
+    int nrange = 128 << 8;
+    auto load_query = [&](int qn) {
+      nl2 = 0.f;
+      nd = 0.f;
+      nrange = 128 << 8;
+      if (qn < s) {
+        nl2 = A.lse[hrow + qn] * kOptLog2e;
+        nd = A.delta[hrow + qn];
+        const int first = min(max(A.key_lo[brow + qn] - r0, 0), 128);
+        const int end = min(max(min(A.key_hi[brow + qn], s) - r0, 0), 128);
+        nrange = first | (end << 8);
+      }
+    };
+    if (half == 0 && count > 0) load_query(qb0 * 128 + t);
+    bool ok = true;
+    for (int i = 0; i < count; ++i) {
+      const int c0 = (qb0 + i) * 128;  // first query of this block
+      const float* l2 = sL + (i & 1) * 128 + half * 64;
+      const float* dl = sD + (i & 1) * 128 + half * 64;
+      if (half == 0) {
+        sL[(i & 1) * 128 + t] = nl2;
+        sD[(i & 1) * 128 + t] = nd;
+        sM[(i & 1) * 128 + t] = static_cast<uint16_t>(nrange);
+        const bool whole = __all_sync(0xffffffffu, nrange == (128 << 8));
+        if (lane == 0) sF[(i & 1) * 4 + quarter] = whole ? 1 : 0;
+        load_query(c0 + 128 + t);
+      }
+      mbar_arrive(&lse_ready[i & 1]);
+      if (!mbar_wait_warp(&lse_ready[i & 1], (i >> 1) & 1, status, kSiteAttention) ||
+          !mbar_wait_warp(s_full, i & 1, status, kSiteAttention)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float p[64];
+      tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
+      tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(s_free);
+      const bool edge = (sF[(i & 1) * 4 + 2 * half] & sF[(i & 1) * 4 + 2 * half + 1]) == 0;
+      // P (bf16 pairs in pp with a cap, else still in p), and in p what dP -
+      // delta is multiplied by: P, with a cap P (1 - tanh^2).
+      uint32_t pp[CAP ? 32 : 1];
+      const float base = static_cast<float>(c0 + half * 64 - r);
+      const uint16_t* mrow = sM + (i & 1) * 128 + half * 64;
+      auto weights = [&](auto edge_c) {
+        constexpr bool EDGE = decltype(edge_c)::value;
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const float4 lv = *reinterpret_cast<const float4*>(l2 + e);
+          uint32_t mm[2] = {0u, 0u};
+          if constexpr (EDGE) {
+            const uint2 w = *reinterpret_cast<const uint2*>(mrow + e);
+            mm[0] = w.x;
+            mm[1] = w.y;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = e + 2 * h;
+            float2 add = h == 0 ? make_float2(-lv.x, -lv.y) : make_float2(-lv.z, -lv.w);
+            if constexpr (CAP) add = __fadd2_rn(add, make_float2(sc.cap2, sc.cap2));
+            if constexpr (BIAS) {
+              add.x = fmaf(-sc.slope2, fabsf(base + k), add.x);
+              add.y = fmaf(-sc.slope2, fabsf(base + (k + 1)), add.y);
+            }
+            const float2 x = make_float2(p[k], p[k + 1]);
+            float2 y;
+            [[maybe_unused]] float2 rr;
+            if constexpr (CAP) {
+              rr = cap_r(x, sc.mul);
+              y = __ffma2_rn(rr, make_float2(-2.f * sc.cap2, -2.f * sc.cap2), add);
+            } else {
+              y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
+            }
+            float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            if constexpr (EDGE) {
+              const int f0 = mm[h] & 255, e0 = (mm[h] >> 8) & 255;
+              const int f1 = (mm[h] >> 16) & 255, e1 = mm[h] >> 24;
+              const bool v0 = t >= f0 && t < e0, v1 = t >= f1 && t < e1;
+              pv = make_float2(v0 ? pv.x : 0.f, v1 ? pv.y : 0.f);
+              if constexpr (CAP) rr = make_float2(v0 ? rr.x : 0.f, v1 ? rr.y : 0.f);
+            }
+            if constexpr (CAP) {
+              pp[k / 2] = pack_bf16x2(pv.x, pv.y);
+              // 1 - tanh^2 = 4 r (1 - r)
+              const float2 r4 = __fmul2_rn(rr, make_float2(4.f, 4.f));
+              const float2 om = __ffma2_rn(make_float2(-r4.x, -r4.y), rr, r4);
+              pv = __fmul2_rn(pv, om);
+            }
+            p[k] = pv.x;
+            p[k + 1] = pv.y;
+          }
+        }
+      };
+      if (edge)
+        weights(BoolC<true>{});
+      else
+        weights(BoolC<false>{});
+      if (!mbar_wait_warp(dp_full, i & 1, status, kSiteAttention)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // dz^T of this block pair also goes to `ds_tiles` for the dQ product, as
+      // the 128-byte-swizzled shared-memory image of an MN-major A operand:
+      // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit of
+      // queries [8u, 8u + 8) at unit u ^ (t & 7); assembled in sDs, sent as
+      // one bulk store, whose predecessor must have read sDs first.
+      const bool store_ds = A.ds_tiles != nullptr;
+      uint8_t* ds_row = sDs + half * 16384 + t * 128;
+      if (store_ds && i > 0) {
+        if (threadIdx.x == 64) {
+          bulk_wait_read();
+          mbar_arrive(ds_free);
+        }
+        if (!mbar_wait_warp(ds_free, (i - 1) & 1, status, kSiteAttention)) {
+          ok = false;
+          break;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float dv[16];
+        tmem_ld_32x32b_x16(tdP + my_cols + g * 16, dv);
+        uint32_t w[16];  // [P of the 16 queries | dz of the 16 queries]
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 dlv = *reinterpret_cast<const float4*>(dl + g * 16 + e);
+          const float* pq = p + g * 16 + e;
+          const float2 d0 = __fmul2_rn(make_float2(pq[0], pq[1]),
+                                       __fadd2_rn(make_float2(dv[e], dv[e + 1]),
+                                                  make_float2(-dlv.x, -dlv.y)));
+          const float2 d1 = __fmul2_rn(make_float2(pq[2], pq[3]),
+                                       __fadd2_rn(make_float2(dv[e + 2], dv[e + 3]),
+                                                  make_float2(-dlv.z, -dlv.w)));
+          if constexpr (CAP) {
+            w[e / 2] = pp[(g * 16 + e) / 2];
+            w[e / 2 + 1] = pp[(g * 16 + e) / 2 + 1];
+          } else {
+            w[e / 2] = pack_bf16x2(pq[0], pq[1]);
+            w[e / 2 + 1] = pack_bf16x2(pq[2], pq[3]);
+          }
+          w[8 + e / 2] = pack_bf16x2(d0.x, d0.y);
+          w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
+        }
+        if (store_ds) {
+          *reinterpret_cast<uint4*>(ds_row + (((2 * g) ^ (t & 7)) << 4)) =
+              make_uint4(w[8], w[9], w[10], w[11]);
+          *reinterpret_cast<uint4*>(ds_row + (((2 * g + 1) ^ (t & 7)) << 4)) =
+              make_uint4(w[12], w[13], w[14], w[15]);
+        }
+        // over this thread's own dP^T columns, already in registers
+        tmem_st_32x32b_x16(tdP + my_cols + g * 16, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_full);
+      if (store_ds) {
+        fence_proxy_async_smem();  // sDs writes visible to the bulk copy
+        mbar_arrive(ds_full);
+        if (warp == 2) {
+          // one thread stores the assembled tile
+          if (!mbar_wait_warp(ds_full, i & 1, status, kSiteAttention)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            const int qb = qb0 + i;
+            // the workspace of a causal mask has no tile above the diagonal
+            if (check_index(!A.causal || kb <= qb, status, kSiteAttention)) {
+              bulk_store(A.ds_tiles +
+                             opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb, kb) *
+                                 kOptTileBytes,
+                         sDs, static_cast<uint32_t>(kOptTileBytes));
+              bulk_commit();
+            }
+          }
+        }
+      }
+    }
+    // the tile stores must be complete (and done with sDs) before exit
+    if (A.ds_tiles && threadIdx.x == 64) bulk_wait_all();
+    if (count > 0 && ok) ok = mbar_wait_warp(acc_done, (count - 1) & 1, status, kSiteAttention);
+    if (ok && ok_entry) {
+      tc_fence_after();
+      const float scale = rsqrtf(static_cast<float>(D));
+      const int64_t row = (brow + r) * 3 * static_cast<int64_t>(a);
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        // w = 0: dV (V's columns of dqkv), w = 1: dK scaled by 1/sqrt(d)
+        const uint32_t tacc = w == 0 ? tdV : tdK;
+        // (a key block that no query sees gets zeros)
+        const float mul = w == 0 ? 1.f : scale;
+        const int col = (w == 0 ? 2 * a : a) + hh * D;
+#pragma unroll 1
+        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
+          float v[32] = {};
+          if (count > 0) tmem_ld_32x32b_x32(tacc + lane_off + c * 32, v);
+          if (r < s && MC_DCHECK(r >= 0 && col + c * 32 + 32 <= 3 * a, status, kSiteAttention)) {
+            uint4* dst = reinterpret_cast<uint4*>(A.dqkv + row + col + c * 32);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 wv;
+              wv.x = pack_bf16x2(v[8 * k + 0] * mul, v[8 * k + 1] * mul);
+              wv.y = pack_bf16x2(v[8 * k + 2] * mul, v[8 * k + 3] * mul);
+              wv.z = pack_bf16x2(v[8 * k + 4] * mul, v[8 * k + 5] * mul);
+              wv.w = pack_bf16x2(v[8 * k + 6] * mul, v[8 * k + 7] * mul);
+              dst[k] = wv;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- dQ, scores formed again
+template <int D>
+struct OptDqCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTile = 128 * D * 2;
+  // Q, dO, three K stages, two V stages, barriers, alignment slack
+  static constexpr int kUsed = 7 * kTile + 24 * 8 + 1024;
+  static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kUsed <= 227 * 1024, "dq kernel shared memory");
+};
+
+// TMEM: S [0, 128), dP [128, 256), dQ [256, 256 + D), dz (bf16) [384, 448).
+// The compute warps read S_j and dP_j into registers and release them at once
+// (s_free), so S_{j+1} and dP_{j+1} run while dz_j is formed; dQ += dz_j K_j
+// follows when dz_j is in TMEM (ds_full), and its completion (ds_free) lets
+// dz_{j+1} be written.
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kOptBwdThreads, 1)
+    attn_opt_dq_kernel(const __grid_constant__ CUtensorMap tm_qkv,
+                       const __grid_constant__ CUtensorMap tm_do,
+                       const __grid_constant__ OptBwdArgs A) {
+  using C = OptDqCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sdO = smem + C::kTile;
+  uint8_t* sK[3] = {smem + 2 * C::kTile, smem + 3 * C::kTile, smem + 4 * C::kTile};
+  uint8_t* sV[2] = {smem + 5 * C::kTile, smem + 6 * C::kTile};
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::kTile);
+  uint64_t* r_full = bars + 0;
+  uint64_t* k_full = bars + 1;    // [3]
+  uint64_t* k_empty = bars + 4;   // [3]
+  uint64_t* v_full = bars + 7;    // [2]
+  uint64_t* v_empty = bars + 9;   // [2]
+  uint64_t* s_full = bars + 11;
+  uint64_t* s_free = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* ds_free = bars + 14;
+  uint64_t* drain = bars + 15;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  int* status = A.status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = A.s, H = A.H, a = A.H * D;
+  if (threadIdx.x == 0) {
+    mbar_init(r_full, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 256);
+    mbar_init(ds_full, 256);
+    mbar_init(ds_free, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_qkv);
+    tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the previous kernel on the stream has completed
+  const uint32_t tS = tmem, tdP = tmem + 128, tdQ = tmem + 256, tdS = tmem + 384;
+
+  int4 entry;  // sequence, query block, lowest and highest visible key
+  int hh;
+  const bool ok_entry =
+      opt_entry(A.tables, A.head_major != 0, A.b, (s + 127) / 128, entry, hh, status);
+  const int bi = entry.x;
+  const int q0 = entry.y * 128;
+  const int k_lo = max(entry.z, 0), k_hi = min(entry.w, s);
+  const int count = ok_entry && k_hi > k_lo ? (k_hi - k_lo + 127) / 128 : 0;
+
+  if (warp == 0) {
+    if (lane == 0 && count > 0) {
+      // -------------------------------------------------------- producer
+      mbar_arrive_expect_tx(r_full, 2 * C::kTile);
+      for (int c = 0; c < C::kChunks; ++c) {
+        tma_load_3d(sQ + c * 16384, &tm_qkv, r_full, hh * D + c * 64, q0, bi);
+        tma_load_3d(sdO + c * 16384, &tm_do, r_full, hh * D + c * 64, q0, bi);
+      }
+      int k_issued = 0, v_issued = 0;
+      for (int j = 0; j < count; ++j) {
+        const int ks = j % 3, kph = (j / 3) & 1, vs = j & 1, vph = (j >> 1) & 1;
+        if (!mbar_wait(&k_empty[ks], kph ^ 1u, status, kSiteAttention)) break;
+        mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_3d(sK[ks] + c * 16384, &tm_qkv, &k_full[ks], a + hh * D + c * 64,
+                      k_lo + j * 128, bi);
+        ++k_issued;
+        if (!mbar_wait(&v_empty[vs], vph ^ 1u, status, kSiteAttention)) break;
+        mbar_arrive_expect_tx(&v_full[vs], C::kTile);
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_3d(sV[vs] + c * 16384, &tm_qkv, &v_full[vs], 2 * a + hh * D + c * 64,
+                      k_lo + j * 128, bi);
+        ++v_issued;
+      }
+      pdl_launch();  // every load of this CTA is issued
+      mbar_wait(r_full, 0, status, kSiteAttention, 200000000ull, false);
+      for (int j = k_issued - 1; j >= 0 && j >= k_issued - 3; --j)
+        mbar_wait(&k_full[j % 3], (j / 3) & 1, status, kSiteAttention, 200000000ull, false);
+      for (int j = v_issued - 1; j >= 0 && j >= v_issued - 2; --j)
+        mbar_wait(&v_full[j & 1], (j >> 1) & 1, status, kSiteAttention, 200000000ull, false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && count > 0) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+      bool ok = mbar_wait(r_full, 0, status, kSiteAttention);
+      const uint32_t qb = smem_u32(sQ), dob = smem_u32(sdO);
+      for (int j = 0; ok && j <= count; ++j) {
+        if (j < count) {
+          const int ks = j % 3, vs = j & 1;
+          if (!mbar_wait(&k_full[ks], (j / 3) & 1, status, kSiteAttention)) break;
+          if (!mbar_wait(&v_full[vs], (j >> 1) & 1, status, kSiteAttention)) break;
+          // S / dP of block j - 1 are in the compute warps' registers.
+          if (j > 0 && !mbar_wait(s_free, (j - 1) & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint32_t kb = smem_u32(sK[ks]), vb = smem_u32(sV[vs]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_bf16(tS, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024),
+                      kIdescSq, kk > 0 ? 1u : 0u);
+            umma_bf16(tdP, smem_desc_sw128(dob + off, 16, 1024),
+                      smem_desc_sw128(vb + off, 16, 1024), kIdescSq, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(s_full);
+          umma_commit(&v_empty[vs]);  // V_j is done once dP_j is
+        }
+        if (j > 0) {
+          const int pj = j - 1, pks = pj % 3;
+          if (!mbar_wait(ds_full, pj & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint32_t kb = smem_u32(sK[pks]);
+#pragma unroll
+          for (int kk = 0; kk < 128 / 16; ++kk)
+            umma_bf16_ts(tdQ, tdS + kk * 8, smem_desc_sw128(kb + kk * 2048, 16384, 1024), kIdescAcc,
+                         (pj > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&k_empty[pks]);
+          umma_commit(ds_free);
+        }
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+    }
+  } else {
+    // ---------------------------------------------------------- compute
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;   // 64 of the block's 128 key columns
+    const int r = q0 + quarter * 32 + lane;  // this thread's query row
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const ScoreConst sc =
+        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, A.slopes, hh);
+    float my_l2 = 0.f, my_d = 0.f;
+    int lo = 0, hi = 0x7fffffff;  // rows past the sequence: zeros, never stored
+    if (ok_entry && r < s) {
+      const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s;
+      my_l2 = A.lse[hrow + r] * kOptLog2e;
+      my_d = A.delta[hrow + r];
+      lo = A.key_lo[static_cast<int64_t>(bi) * s + r];
+      hi = min(A.key_hi[static_cast<int64_t>(bi) * s + r], s);
+    }
+    const float add0 = (CAP ? sc.cap2 : 0.f) - my_l2;
+    bool ok = true;
+    for (int j = 0; j < count; ++j) {
+      if (!mbar_wait_warp(s_full, j & 1, status, kSiteAttention)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float sv[64], dv[64];
+      tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 64, sv);
+      tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 64 + 32, sv + 32);
+      tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64, dv);
+      tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64 + 32, dv + 32);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(s_free);
+      const int c0 = k_lo + j * 128 + half * 64;
+      const bool edge = __any_sync(0xffffffffu, lo > c0 || hi < c0 + 64);
+      const int first = lo - c0, end = hi - c0;
+      uint32_t dw[32];
+      const float2 nd2 = make_float2(-my_d, -my_d);
+      const float base = static_cast<float>(c0 - r);
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        float2 add = make_float2(add0, add0);
+        if constexpr (BIAS) {
+          add.x = fmaf(-sc.slope2, fabsf(base + e), add.x);
+          add.y = fmaf(-sc.slope2, fabsf(base + (e + 1)), add.y);
+        }
+        const float2 x = make_float2(sv[e], sv[e + 1]);
+        float2 y;
+        [[maybe_unused]] float2 rr;
+        if constexpr (CAP) {
+          rr = cap_r(x, sc.mul);
+          y = __ffma2_rn(rr, make_float2(-2.f * sc.cap2, -2.f * sc.cap2), add);
+        } else {
+          y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
+        }
+        float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+        if (edge) {
+          const bool v0 = e >= first && e < end, v1 = e + 1 >= first && e + 1 < end;
+          pv = make_float2(v0 ? pv.x : 0.f, v1 ? pv.y : 0.f);
+          if constexpr (CAP) rr = make_float2(v0 ? rr.x : 0.f, v1 ? rr.y : 0.f);
+        }
+        if constexpr (CAP) {
+          const float2 r4 = __fmul2_rn(rr, make_float2(4.f, 4.f));
+          pv = __fmul2_rn(pv, __ffma2_rn(make_float2(-r4.x, -r4.y), rr, r4));
+        }
+        const float2 ds = __fmul2_rn(pv, __fadd2_rn(make_float2(dv[e], dv[e + 1]), nd2));
+        dw[e / 2] = pack_bf16x2(ds.x, ds.y);
+      }
+      // dz_{j-1} must have been consumed by its dQ product.
+      if (j > 0 && !mbar_wait_warp(ds_free, (j - 1) & 1, status, kSiteAttention)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_st_32x32b_x32(tdS + lane_off + half * 32, dw);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    if (count > 0 && ok) ok = mbar_wait_warp(ds_free, (count - 1) & 1, status, kSiteAttention);
+    if (ok && ok_entry) {
+      tc_fence_after();
+      const float scale = rsqrtf(static_cast<float>(D));
+      const int64_t row = (static_cast<int64_t>(bi) * s + r) * 3 * static_cast<int64_t>(a);
+#pragma unroll 1
+      for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
+        float v[32] = {};
+        if (count > 0) tmem_ld_32x32b_x32(tdQ + lane_off + c * 32, v);
+        if (r < s && MC_DCHECK(r >= 0 && hh * D + c * 32 + 32 <= a, status, kSiteAttention)) {
+          uint4* dst = reinterpret_cast<uint4*>(A.dqkv + row + hh * D + c * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4 wv;
+            wv.x = pack_bf16x2(v[8 * k + 0] * scale, v[8 * k + 1] * scale);
+            wv.y = pack_bf16x2(v[8 * k + 2] * scale, v[8 * k + 3] * scale);
+            wv.z = pack_bf16x2(v[8 * k + 4] * scale, v[8 * k + 5] * scale);
+            wv.w = pack_bf16x2(v[8 * k + 6] * scale, v[8 * k + 7] * scale);
+            dst[k] = wv;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- dQ from the dz^T tiles
+template <int D>
+struct OptDqGemmCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kKTile = 128 * D * 2;
+  static constexpr int kStage = static_cast<int>(kOptTileBytes) + kKTile;
+  static constexpr int kStages = 3;
+  static constexpr int kUsed = kStages * kStage + 16 * 8;
+  static constexpr int kSmem = kUsed + 1024;  // + alignment slack
+  static_assert(kSmem <= 227 * 1024, "dq gemm shared memory");
+  static constexpr uint32_t kTmemCols = 256;  // two accumulators of 128 columns
+};
+
+// Item r of this CTA: the (query entry, head) pairs in dispatch order, handed
+// out in a snake; its key blocks are [kb0, kb0 + nj).  1: an item, 0: the
+// CTA's share is done.
+__device__ __forceinline__ int opt_dq_item(int r, const OptBwdArgs& A, int nb, int& qb, int& bi,
+                                           int& hh, int& kb0, int& nj) {
+  const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+  const int64_t n = static_cast<int64_t>(A.b) * nb;
+  const int64_t k = static_cast<int64_t>(r) * G + ((r & 1) ? G - 1 - c : c);
+  if (k >= n * A.H) return 0;
+  const int64_t rank = A.head_major ? k / A.H : k % n;
+  hh = static_cast<int>(A.head_major ? k % A.H : k / n);
+  const int4 e = *reinterpret_cast<const int4*>(A.tables + 4 * rank);
+  bi = min(max(e.x, 0), A.b - 1);
+  qb = min(max(e.y, 0), nb - 1);
+  const int lo = max(e.z, 0), hi = min(e.w, A.s);
+  kb0 = lo / 128;
+  int end = hi > lo ? (hi + 127) / 128 : kb0;
+  if (A.causal) end = min(end, qb + 1);  // the workspace has no other tiles
+  nj = max(end - kb0, 0);
+  return 1;
+}
+
+// Persistent, 192 threads: warp 0 loads per key block the dz^T tile (one bulk
+// copy of its swizzled image) and K_j into a 3-deep ring that runs on across
+// items, warp 1 issues dQ += dz_j K_j (items alternate accumulators), warps
+// 2..5 write dQ / sqrt(d) of the item before.
+template <int D>
+__global__ void __launch_bounds__(192, 1)
+    attn_opt_dq_gemm_kernel(const __grid_constant__ CUtensorMap tm_qkv,
+                            const __grid_constant__ OptBwdArgs A) {
+  using C = OptDqGemmCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
+  uint64_t* full = bars + 0;       // [3]
+  uint64_t* empty = bars + 3;      // [3]
+  uint64_t* acc_full = bars + 6;   // [2]  an item's dQ is complete in accumulator a
+  uint64_t* acc_empty = bars + 8;  // [2]  the epilogue has read accumulator a (128 threads)
+  uint64_t* drain = bars + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 11);
+  int* status = A.status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = A.s, H = A.H, a = A.H * D;
+  const int nb = (s + 127) / 128;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 128);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_qkv);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the dK/dV kernel (the tiles) has completed
+
+  int qb, bi, hh, kb0, nj;
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------- producer
+      int gt = 0;  // tiles issued, across items
+      bool ok = true;
+      for (int r = 0; ok && opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
+        for (int j = 0; j < nj; ++j, ++gt) {
+          const int st = gt % C::kStages;
+          if (!mbar_wait(&empty[st], ((gt / C::kStages) & 1) ^ 1u, status, kSiteAttention)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + st * C::kStage;
+          mbar_arrive_expect_tx(&full[st], C::kStage);
+          bulk_load(dst,
+                    A.ds_tiles + opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb,
+                                          kb0 + j) * kOptTileBytes,
+                    static_cast<uint32_t>(kOptTileBytes), &full[st]);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(dst + kOptTileBytes + c * 16384, &tm_qkv, &full[st], a + hh * D + c * 64,
+                        (kb0 + j) * 128, bi);
+        }
+      }
+      pdl_launch();  // every load of this CTA is issued
+      for (int g = gt - 1; g >= 0 && g >= gt - C::kStages; --g)
+        mbar_wait(&full[g % C::kStages], (g / C::kStages) & 1, status, kSiteAttention,
+                  200000000ull, false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, true, true);
+      bool ok = true;
+      int gt = 0;
+      for (int r = 0; ok && opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
+        const int acc = r & 1;
+        // the epilogue of item r - 2 has read this accumulator
+        if (!mbar_wait(&acc_empty[acc], ((r >> 1) & 1) ^ 1u, status, kSiteAttention)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * 128);
+        for (int j = 0; j < nj; ++j, ++gt) {
+          const int st = gt % C::kStages;
+          if (!mbar_wait(&full[st], (gt / C::kStages) & 1, status, kSiteAttention)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ab = smem_u32(smem + st * C::kStage);
+          const uint32_t kbase = ab + static_cast<uint32_t>(kOptTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // 16 keys per step: 16 rows of 128 B in both MN-major operands;
+            // 64-wide query (A) or d (B) chunks 16 KB apart
+            umma_bf16(d_tmem, smem_desc_sw128(ab + kk * 2048, 16384, 1024),
+                      smem_desc_sw128(kbase + kk * 2048, 16384, 1024), kIdesc,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&empty[st]);
+        }
+        if (ok) umma_commit(&acc_full[acc]);
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const float scale = rsqrtf(static_cast<float>(D));
+    for (int r = 0; opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
+      const int acc = r & 1;
+      const int row = qb * 128 + quarter * 32 + lane;  // this thread's query row
+      if (!mbar_wait_warp(&acc_full[acc], (r >> 1) & 1, status, kSiteAttention)) break;
+      tc_fence_after();
+      const int64_t base = (static_cast<int64_t>(bi) * s + row) * 3 * static_cast<int64_t>(a);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32] = {};
+        if (nj > 0)
+          tmem_ld_32x32b_x32(tmem + static_cast<uint32_t>(acc * 128) + lane_off + c * 32, v);
+        if (row < s && MC_DCHECK(row >= 0 && hh * D + c * 32 + 32 <= a, status, kSiteAttention)) {
+          uint4* dst = reinterpret_cast<uint4*>(A.dqkv + base + hh * D + c * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4 wv;
+            wv.x = pack_bf16x2(v[8 * k + 0] * scale, v[8 * k + 1] * scale);
+            wv.y = pack_bf16x2(v[8 * k + 2] * scale, v[8 * k + 3] * scale);
+            wv.z = pack_bf16x2(v[8 * k + 4] * scale, v[8 * k + 5] * scale);
+            wv.w = pack_bf16x2(v[8 * k + 6] * scale, v[8 * k + 7] * scale);
+            dst[k] = wv;
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[acc]);  // the accumulator may take the item after next
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+dim3 opt_grid(const OptBwdArgs& A) {
+  const unsigned n = static_cast<unsigned>(A.b) * static_cast<unsigned>((A.s + 127) / 128);
+  return A.head_major ? dim3(static_cast<unsigned>(A.H), n, 1u)
+                      : dim3(n, static_cast<unsigned>(A.H), 1u);
+}
+
+template <class K>
+cudaError_t opt_smem(PerDeviceInit& init, K kern, int bytes) {
+  return once_per_device(init, [&](long long*) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
+
+template <int D, bool CAP, bool BIAS>
+int launch_bwd(const CUtensorMap& tq, const CUtensorMap& td, const OptBwdArgs& A,
+               cudaStream_t st) {
+  static PerDeviceInit init_kv, init_q;
+  auto kv = attn_opt_dkdv_kernel<D, CAP, BIAS>;
+  if (opt_smem(init_kv, kv, OptBwdCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
+  launch_kernel(kv, opt_grid(A), dim3(kOptBwdThreads), OptBwdCfg<D>::kSmem, st, 1, tq, td, A);
+  if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
+  if (A.ds_tiles) return MC_OK;
+  auto kq = attn_opt_dq_kernel<D, CAP, BIAS>;
+  if (opt_smem(init_q, kq, OptDqCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
+  launch_kernel(kq, opt_grid(A), dim3(kOptBwdThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
+  return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
+}
+
+template <int D>
+int launch_bwd_d(const uint16_t* qkv, const uint16_t* dout, const OptBwdArgs& A,
+                 cudaStream_t st) {
+  const uint64_t a = static_cast<uint64_t>(A.H) * D, s = static_cast<uint64_t>(A.s),
+                 b = static_cast<uint64_t>(A.b);
+  const uint32_t box[3] = {64, 128, 1};
+  const uint64_t dq[3] = {3 * a, s, b}, sq[2] = {3 * a * 2, 3 * a * 2 * s};
+  const uint64_t dd[3] = {a, s, b}, sd[2] = {a * 2, a * 2 * s};
+  CUtensorMap tq, td;
+  if (!make_tmap_bf16(&tq, qkv, 3, dq, sq, box) || !make_tmap_bf16(&td, dout, 3, dd, sd, box))
+    return MC_ERR_CUDA;
+  const bool cap = A.softcap > 0.f, bias = A.slopes != nullptr;
+  int rc;
+  if (cap)
+    rc = bias ? launch_bwd<D, true, true>(tq, td, A, st) : launch_bwd<D, true, false>(tq, td, A, st);
+  else
+    rc = bias ? launch_bwd<D, false, true>(tq, td, A, st) : launch_bwd<D, false, false>(tq, td, A, st);
+  if (rc != MC_OK || !A.ds_tiles) return rc;
+  static PerDeviceInit init;
+  auto kern = attn_opt_dq_gemm_kernel<D>;
+  if (opt_smem(init, kern, OptDqGemmCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(A.b) * ((A.s + 127) / 128) * A.H;
+  const int grid = items < num_sms() ? static_cast<int>(items) : num_sms();
+  launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(192), OptDqGemmCfg<D>::kSmem, st, 1,
+                tq, A);
+  return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
+}
+
+}  // namespace
+
+int64_t attention_opt_ds_bytes(int64_t b, int64_t s, int64_t H, bool causal) {
+  const int64_t nb = (s + 127) / 128;
+  return b * H * (causal ? nb * (nb + 1) / 2 : nb * nb) * kOptTileBytes;
+}
+
+int launch_attention_opt_bwd(const uint16_t* qkv, const float* lse, const uint16_t* dout,
+                             uint16_t* dqkv, const float* delta, int b, int s, int H, int d,
+                             const mc_attention_options& opt, uint8_t* ds_tiles, int* status,
+                             cudaStream_t st) {
+  OptBwdArgs A = {};
+  A.dqkv = dqkv;
+  A.lse = lse;
+  A.delta = delta;
+  A.key_lo = opt.key_lo;
+  A.key_hi = opt.key_hi;
+  A.tables = opt.tables;
+  A.slopes = opt.slopes;
+  A.ds_tiles = ds_tiles;
+  A.softcap = opt.softcap;
+  A.b = b;
+  A.s = s;
+  A.H = H;
+  A.head_major = attention_head_major(static_cast<int64_t>(b) * ((s + 127) / 128), H, 1) ? 1 : 0;
+  A.causal = opt.causal ? 1 : 0;
+  A.status = status;
+  return d == 64 ? launch_bwd_d<64>(qkv, dout, A, st) : launch_bwd_d<128>(qkv, dout, A, st);
+}
+
+}  // namespace mc

@@ -67,9 +67,16 @@ struct Dims {
   int64_t b, s, T, h, H, d, a, f, t;
   bool fp8;       // MC_FP8_HYBRID
   bool ds_tiles;  // the attention backward's dS tiles (not MC_ATTN_DQ_RECOMPUTE)
+  bool ds_square; // of every block pair: an interval mask that looks ahead
 };
 
-Dims dims_of(const mc_layer_shape& sh) {
+// What the attention stage adds to the plain causal one (either may be NULL).
+struct AttnStage {
+  const mc_layer_rotary* rotary;
+  const mc_attention_options* options;
+};
+
+Dims dims_of(const mc_layer_shape& sh, const mc_attention_options* attention = nullptr) {
   Dims D;
   D.b = sh.micro_batch;
   D.s = sh.seq_len;
@@ -82,6 +89,7 @@ Dims dims_of(const mc_layer_shape& sh) {
   D.t = sh.tp_parts;
   D.fp8 = (sh.flags & MC_FP8_HYBRID) != 0;
   D.ds_tiles = (sh.flags & MC_ATTN_DQ_RECOMPUTE) == 0;
+  D.ds_square = attention && !attention->causal;
   return D;
 }
 
@@ -202,7 +210,9 @@ Work plan_ws(const Dims& D, bool with_saved, void* p, size_t* bytes) {
   W.dO = c.take<uint16_t>(D.T * D.a);
   W.delta = c.take<float>(D.b * D.H * D.s);
   W.dqkv = c.take<uint16_t>(D.T * 3 * D.a);
-  W.ds = D.ds_tiles ? c.take<uint8_t>(attention_ds_workspace_bytes(D.b, D.s, D.H)) : nullptr;
+  W.ds = D.ds_tiles ? c.take<uint8_t>(D.ds_square ? attention_opt_ds_bytes(D.b, D.s, D.H, false)
+                                                  : attention_ds_workspace_bytes(D.b, D.s, D.H))
+                    : nullptr;
   const size_t ln_part = layernorm_backward_scratch_floats(D.T, static_cast<int>(D.h));
   int64_t widest = D.f > 3 * D.a ? D.f : 3 * D.a;
   if (D.h > widest) widest = D.h;
@@ -272,6 +282,45 @@ int check_grads(const mc_layer_grads* g) {
     if (rc_ != MC_OK) return rc_; \
   } while (0)
 
+int check_stage(const Dims& D, const AttnStage& A) {
+  if (A.rotary) {
+    MC_TRY(check_rotary_spec(&A.rotary->spec, static_cast<int>(D.d)));
+    if (!A.rotary->positions || !A.rotary->inv_freq) return MC_ERR_NULLPTR;
+    if (!al(A.rotary->positions, 4) || !al(A.rotary->inv_freq, 4)) return MC_ERR_ALIGN;
+  }
+  return A.options ? check_attention_options(A.options) : MC_OK;
+}
+
+// The attention stage: Q and K turn in place in the packed Q|K|V rows, then
+// causal attention or attention over the interval mask.
+int attention_stage_forward(const Dims& D, const AttnStage& A, const Saved& S, const Work& W,
+                            cudaStream_t st) {
+  const int b = static_cast<int>(D.b), s = static_cast<int>(D.s), H = static_cast<int>(D.H),
+            d = static_cast<int>(D.d);
+  if (A.rotary)
+    MC_TRY(launch_rotary(S.qkv, S.qkv, true, D.T, 2 * H, d, 3 * D.a, 3 * D.a, A.rotary->positions,
+                         A.rotary->inv_freq, &A.rotary->spec, false, W.status, st));
+  if (A.options)
+    return launch_attention_forward_opt(S.qkv, S.o, S.lse, b, s, H, d, *A.options, W.status, st);
+  return launch_attention_forward(S.qkv, S.o, S.lse, b, s, H, d, W.status, st);
+}
+
+// Its backward pass: dQ | dK | dV into W.dqkv, dQ and dK turned back there.
+int attention_stage_backward(const Dims& D, const AttnStage& A, const Saved& S, const Work& W,
+                             cudaStream_t st) {
+  const int b = static_cast<int>(D.b), s = static_cast<int>(D.s), H = static_cast<int>(D.H),
+            d = static_cast<int>(D.d);
+  if (A.options)
+    MC_TRY(launch_attention_backward_opt(S.qkv, S.o, S.lse, W.dO, W.dqkv, W.delta, b, s, H, d,
+                                         *A.options, W.ds, W.status, st));
+  else
+    MC_TRY(launch_attention_backward(S.qkv, S.o, S.lse, W.dO, W.dqkv, W.delta, b, s, H, d,
+                                     W.status, st, W.ds));
+  if (!A.rotary) return MC_OK;
+  return launch_rotary(W.dqkv, W.dqkv, true, D.T, 2 * H, d, 3 * D.a, 3 * D.a, A.rotary->positions,
+                       A.rotary->inv_freq, &A.rotary->spec, true, W.status, st);
+}
+
 }  // namespace
 }  // namespace mc
 
@@ -290,9 +339,14 @@ size_t mc_layer_saved_bytes(const mc_layer_shape* shape) {
 }
 
 size_t mc_layer_workspace_bytes(const mc_layer_shape* shape) {
+  return mc_layer_workspace_bytes_opt(shape, nullptr);
+}
+
+size_t mc_layer_workspace_bytes_opt(const mc_layer_shape* shape,
+                                    const mc_attention_options* attention) {
   if (check_shape(shape) != MC_OK) return 0;
   size_t n = 0;
-  plan_ws(dims_of(*shape), recompute(*shape), nullptr, &n);
+  plan_ws(dims_of(*shape, attention), recompute(*shape), nullptr, &n);
   return n;
 }
 
@@ -322,8 +376,8 @@ constexpr int kE4M3 = 0, kE5M2 = 1;
 // E4M3 first (per-tensor current scaling) -- into a row-major copy for this
 // product and, with the same scale, a transposed copy kept for the backward
 // pass -- and the GEMM's epilogue multiplies by the two inverse scales.
-int enqueue_forward_fp8(const Dims& D, const mc_layer_weights* w, const float* x, float* y,
-                        const Saved& S, const Work& W, cudaStream_t st) {
+int enqueue_forward_fp8(const Dims& D, const AttnStage& A, const mc_layer_weights* w,
+                        const float* x, float* y, const Saved& S, const Work& W, cudaStream_t st) {
   StageRanges R("mc_layer_forward (fp8)");
   const int t = static_cast<int>(D.t);
   const int h = static_cast<int>(D.h);
@@ -347,10 +401,9 @@ int enqueue_forward_fp8(const Dims& D, const mc_layer_weights* w, const float* x
   MC_TRY(launch_gemm_fp8(D.T, 3 * D.a, D.h, W.ln1_q, D.h, kE4M3, W.wqkv_q, D.h, kE4M3, si + 0,
                          si + 4, S.qkv, 3 * D.a, MC_EPI_BIAS_BF16, w->b_qkv, nullptr, 0, 0, 1,
                          W.status, st));
-  // F3  causal attention (bf16), O quantised
+  // F3  attention (bf16), O quantised
   R.next("F3 causal attention");
-  MC_TRY(launch_attention_forward(S.qkv, S.o, S.lse, static_cast<int>(D.b), static_cast<int>(D.s),
-                                  static_cast<int>(D.H), static_cast<int>(D.d), W.status, st));
+  MC_TRY(attention_stage_forward(D, A, S, W, st));
   MC_TRY(quant(S.o, true, D.T, D.a, W.o_q, S.o_t, si + 1));
   // F4  out-projection: partition partials summed in the accumulator, + b_o + x
   R.next("F4 out-projection");
@@ -373,9 +426,9 @@ int enqueue_forward_fp8(const Dims& D, const mc_layer_weights* w, const float* x
   return MC_OK;
 }
 
-int enqueue_forward(const Dims& D, const mc_layer_weights* w, const float* x, float* y,
-                    const Saved& S, const Work& W, bool sp, cudaStream_t st) {
-  if (D.fp8) return enqueue_forward_fp8(D, w, x, y, S, W, st);
+int enqueue_forward(const Dims& D, const AttnStage& A, const mc_layer_weights* w, const float* x,
+                    float* y, const Saved& S, const Work& W, bool sp, cudaStream_t st) {
+  if (D.fp8) return enqueue_forward_fp8(D, A, w, x, y, S, W, st);
   StageRanges R("mc_layer_forward");
   const int t = static_cast<int>(D.t);
   const int h = static_cast<int>(D.h);
@@ -391,10 +444,9 @@ int enqueue_forward(const Dims& D, const mc_layer_weights* w, const float* x, fl
   R.next("F2 QKV");
   MC_TRY(launch_gemm(D.T, 3 * D.a, D.h, S.ln1, D.h, 0, w->w_qkv, D.h, 0, S.qkv, 3 * D.a,
                      MC_EPI_BIAS_BF16, w->b_qkv, nullptr, 0, 0, 1, W.status, st));
-  // F3  causal attention, local per head
+  // F3  attention, local per head
   R.next("F3 causal attention");
-  MC_TRY(launch_attention_forward(S.qkv, S.o, S.lse, static_cast<int>(D.b), static_cast<int>(D.s),
-                                  static_cast<int>(D.H), static_cast<int>(D.d), W.status, st));
+  MC_TRY(attention_stage_forward(D, A, S, W, st));
   // F4  out-projection, row-parallel: partition partials summed in the
   R.next("F4 out-projection");
   //     accumulator, then + b_o + x (per shard)
@@ -428,9 +480,9 @@ int enqueue_forward(const Dims& D, const mc_layer_weights* w, const float* x, fl
 // and dQ|dK|dV are quantised to E5M2 (row-major and transposed, one scale);
 // weight gradients contract over tokens with the transposed copies of both
 // operands, input gradients read the forward's transposed E4M3 weights.
-int enqueue_backward_fp8(const Dims& D, const mc_layer_weights* w, const float* x,
-                         const float* dy, float* dx, const mc_layer_grads& G, const Saved& S,
-                         const Work& W, int acc, cudaStream_t st) {
+int enqueue_backward_fp8(const Dims& D, const AttnStage& A, const mc_layer_weights* w,
+                         const float* x, const float* dy, float* dx, const mc_layer_grads& G,
+                         const Saved& S, const Work& W, int acc, cudaStream_t st) {
   StageRanges R("mc_layer_backward (fp8)");
   const int t = static_cast<int>(D.t);
   const int h = static_cast<int>(D.h);
@@ -471,9 +523,7 @@ int enqueue_backward_fp8(const Dims& D, const mc_layer_weights* w, const float* 
                          W.dO, D.a, MC_EPI_STORE_BF16, nullptr, nullptr, 0, 0, 1, W.status, st));
   // B5  attention backward (bf16) -> dQ | dK | dV
   R.next("B5 attention backward");
-  MC_TRY(launch_attention_backward(S.qkv, S.o, S.lse, W.dO, W.dqkv, W.delta, static_cast<int>(D.b),
-                                   static_cast<int>(D.s), static_cast<int>(D.H),
-                                   static_cast<int>(D.d), W.status, st, W.ds));
+  MC_TRY(attention_stage_backward(D, A, S, W, st));
   // B6  QKV: db_qkv; dWqkv = dqkv^T ln1; dln1 = sum_p dqkv_p Wqkv_p
   R.next("B6 QKV");
   MC_TRY(launch_colsum(W.dqkv, true, D.T, 3 * D.a, G.b_qkv, acc, nullptr, W.partials, W.status, st));
@@ -496,12 +546,21 @@ int enqueue_backward_fp8(const Dims& D, const mc_layer_weights* w, const float* 
 
 int mc_layer_forward(const mc_layer_shape* shape, const mc_layer_weights* w, const float* x,
                      float* y, void* saved, void* ws, size_t ws_bytes, void* stream) {
+  return mc_layer_forward_opt(shape, w, nullptr, nullptr, x, y, saved, ws, ws_bytes, stream);
+}
+
+int mc_layer_forward_opt(const mc_layer_shape* shape, const mc_layer_weights* w,
+                         const mc_layer_rotary* rotary, const mc_attention_options* attention,
+                         const float* x, float* y, void* saved, void* ws, size_t ws_bytes,
+                         void* stream) {
   MC_TRY(check_shape(shape));
   MC_TRY(check_weights(w));
   const bool rc_mode = recompute(*shape);
   if (!x || !y || (!saved && !rc_mode) || !ws) return MC_ERR_NULLPTR;
   if (!al(x, 16) || !al(y, 16) || (saved && !al(saved, 256)) || !al(ws, 256)) return MC_ERR_ALIGN;
-  const Dims D = dims_of(*shape);
+  const Dims D = dims_of(*shape, attention);
+  const AttnStage A = {rotary, attention};
+  MC_TRY(check_stage(D, A));
   size_t need = 0;
   plan_ws(D, rc_mode, nullptr, &need);
   if (ws_bytes < need) return MC_ERR_WORKSPACE;
@@ -509,12 +568,20 @@ int mc_layer_forward(const mc_layer_shape* shape, const mc_layer_weights* w, con
   const Work W = plan_ws(D, rc_mode, ws, nullptr);
   const Saved S = plan_saved(D, rc_mode ? W.recompute_saved : saved, nullptr);
   if (cudaMemsetAsync(W.status, 0, kStatusBytes, st) != cudaSuccess) return MC_ERR_CUDA;
-  return enqueue_forward(D, w, x, y, S, W, seq_parallel(*shape), st);
+  return enqueue_forward(D, A, w, x, y, S, W, seq_parallel(*shape), st);
 }
 
 int mc_layer_backward(const mc_layer_shape* shape, const mc_layer_weights* w, const float* x,
                       const float* dy, const void* saved, float* dx, const mc_layer_grads* grads,
                       void* ws, size_t ws_bytes, void* stream) {
+  return mc_layer_backward_opt(shape, w, nullptr, nullptr, x, dy, saved, dx, grads, ws, ws_bytes,
+                               stream);
+}
+
+int mc_layer_backward_opt(const mc_layer_shape* shape, const mc_layer_weights* w,
+                          const mc_layer_rotary* rotary, const mc_attention_options* attention,
+                          const float* x, const float* dy, const void* saved, float* dx,
+                          const mc_layer_grads* grads, void* ws, size_t ws_bytes, void* stream) {
   MC_TRY(check_shape(shape));
   MC_TRY(check_weights(w));
   MC_TRY(check_grads(grads));
@@ -522,7 +589,9 @@ int mc_layer_backward(const mc_layer_shape* shape, const mc_layer_weights* w, co
   if (!x || !dy || (!saved && !rc_mode) || !dx || !ws) return MC_ERR_NULLPTR;
   if (!al(x, 16) || !al(dy, 16) || !al(dx, 16) || (saved && !al(saved, 256)) || !al(ws, 256))
     return MC_ERR_ALIGN;
-  const Dims D = dims_of(*shape);
+  const Dims D = dims_of(*shape, attention);
+  const AttnStage A = {rotary, attention};
+  MC_TRY(check_stage(D, A));
   size_t need = 0;
   plan_ws(D, rc_mode, nullptr, &need);
   if (ws_bytes < need) return MC_ERR_WORKSPACE;
@@ -532,7 +601,7 @@ int mc_layer_backward(const mc_layer_shape* shape, const mc_layer_weights* w, co
   if (rc_mode) {
     // Activation recomputation: rebuild F1..F7's activations from x.  The
     // recomputed y lands in dx1's buffer, which B3 overwrites later.
-    MC_TRY(enqueue_forward(D, w, x, W.dx1, S, W, seq_parallel(*shape), st));
+    MC_TRY(enqueue_forward(D, A, w, x, W.dx1, S, W, seq_parallel(*shape), st));
   }
   const int acc = (shape->flags & MC_ACCUMULATE_GRADS) ? 1 : 0;
   const int t = static_cast<int>(D.t);
@@ -546,7 +615,7 @@ int mc_layer_backward(const mc_layer_shape* shape, const mc_layer_weights* w, co
   // added in shard order (the first shard honours MC_ACCUMULATE_GRADS, the
   // rest add).  Weight gradients and the column-parallel products read all
   // shards' rows, which lie side by side: the all-gather.
-  if (D.fp8) return enqueue_backward_fp8(D, w, x, dy, dx, G, S, W, acc, st);
+  if (D.fp8) return enqueue_backward_fp8(D, A, w, x, dy, dx, G, S, W, acc, st);
   StageRanges R("mc_layer_backward");
   const Shards sh = shards_of(D, seq_parallel(*shape));
   auto shard_acc = [&](int64_t p) { return p == 0 ? acc : 1; };
@@ -592,9 +661,7 @@ int mc_layer_backward(const mc_layer_shape* shape, const mc_layer_weights* w, co
                      nullptr, nullptr, 0, 0, 1, W.status, st));
   // B5  attention backward -> dQ | dK | dV
   R.next("B5 attention backward");
-  MC_TRY(launch_attention_backward(S.qkv, S.o, S.lse, W.dO, W.dqkv, W.delta, static_cast<int>(D.b),
-                                   static_cast<int>(D.s), static_cast<int>(D.H),
-                                   static_cast<int>(D.d), W.status, st, W.ds));
+  MC_TRY(attention_stage_backward(D, A, S, W, st));
   // B6  QKV: db_qkv, dWqkv = dqkv^T ln1, dln1 = sum_p dqkv_p Wqkv_p (per
   R.next("B6 QKV");
   //     shard in sequence-parallel mode)

@@ -60,6 +60,8 @@ enum ErrorSite : int {
   kSiteGemmDrain = 4,
   kSiteLayerNorm = 10,
   kSiteAttention = 20,
+  kSiteRotary = 21,
+  kSiteMask = 22,
   kSiteSelfTest = 30,
 };
 
@@ -276,6 +278,27 @@ int launch_attention_dq_parts(const uint16_t* qkv, const uint8_t* ds_tiles, uint
                               int* status, cudaStream_t stream);
 // Checks a launch's rectangles against the sequence (MC_OK or MC_ERR_ARGUMENT).
 int check_cp_rects(const CpRect* rects, int n, int s);
+
+// Rotary positions over `heads` heads at the start of each row (rotary.cu).
+constexpr int kRotaryMaxPairs = 256;
+int check_rotary_spec(const mc_rotary_spec* spec, int head_dim);
+void rotary_axes(const mc_rotary_spec* spec, uint8_t* axis);
+int launch_rotary(const void* in, void* out, bool bf16, int64_t tokens, int heads, int head_dim,
+                  int64_t ld_in, int64_t ld_out, const int32_t* positions, const float* inv_freq,
+                  const mc_rotary_spec* spec, bool inverse, int* status, cudaStream_t stream);
+
+// Attention over an interval mask with optional score cap and distance bias
+// (attention_opt.cu: checks and dispatch; attention_opt_fwd.cu,
+// attention_opt_bwd.cu: kernels).  `ds_tiles` as launch_attention_backward.
+int check_attention_options(const mc_attention_options* opt);
+int64_t attention_opt_ds_bytes(int64_t b, int64_t s, int64_t H, bool causal);
+int launch_attention_forward_opt(const uint16_t* qkv, uint16_t* o, float* lse, int b, int s, int H,
+                                 int d, const mc_attention_options& opt, int* status,
+                                 cudaStream_t stream);
+int launch_attention_backward_opt(const uint16_t* qkv, const uint16_t* o, const float* lse,
+                                  const uint16_t* dout, uint16_t* dqkv, float* delta, int b, int s,
+                                  int H, int d, const mc_attention_options& opt, uint8_t* ds_tiles,
+                                  int* status, cudaStream_t stream);
 #endif
 
 }  // namespace mc

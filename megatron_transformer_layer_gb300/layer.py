@@ -27,9 +27,12 @@ class TransformerLayer:
 
     def __init__(self, micro_batch, seq_len, hidden, heads, ffn_hidden, tp_parts=1, head_dim=0,
                  params=None, device="cuda", accumulate_grads=False, recompute=False,
-                 workspace=None, sequence_parallel=False, fp8=False, attn_dq_recompute=False):
+                 workspace=None, sequence_parallel=False, fp8=False, attn_dq_recompute=False,
+                 rotary=None, attention=None):
         # attn_dq_recompute: the attention backward forms S and dP again for
         # dQ instead of keeping dS tiles (whose workspace grows as seq_len^2)
+        # rotary (make_layer_rotary), attention (make_attention_options):
+        # positions and an interval mask of the attention stage, see set_stage
         flags = (L.MC_ACCUMULATE_GRADS if accumulate_grads else 0) | \
             (L.MC_RECOMPUTE_ACTIVATIONS if recompute else 0) | \
             (L.MC_SEQUENCE_PARALLEL if sequence_parallel else 0) | \
@@ -42,7 +45,8 @@ class TransformerLayer:
         self.tokens = micro_batch * seq_len
         self.hidden = hidden
         self.saved_bytes = L.mc_layer_saved_bytes(self.shape)
-        self.ws_bytes = L.mc_layer_workspace_bytes(self.shape)
+        self.rotary, self.attention = rotary, attention
+        self.ws_bytes = L.mc_layer_workspace_bytes_opt(self.shape, attention)
         # uint8 buffers: the caching allocator returns >= 512-byte aligned blocks.
         # With recomputation nothing is saved and a workspace may be shared by
         # the layers of a stack (pass the same `workspace` tensor to each).
@@ -87,14 +91,23 @@ class TransformerLayer:
         self.params = params
         self.weights = L.make_weights(params)
 
+    def set_stage(self, rotary=None, attention=None):
+        """Positions and interval mask of the following forward / backward pairs
+        (the tensors they point to stay the caller's).  The workspace must cover
+        them: a mask that looks ahead needs a layer built with one."""
+        if L.mc_layer_workspace_bytes_opt(self.shape, attention) > self.ws_bytes:
+            raise L.McError(L.MC_ERR_WORKSPACE, "set_stage")
+        self.rotary, self.attention = rotary, attention
+
     def _stream(self, stream):
         return stream if stream is not None else torch.cuda.current_stream(self.device)
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if y is None:
             y = torch.empty_like(x)
-        _check(L.mc_layer_forward(self.shape, self.weights, x, y, self.saved, self.ws,
-                                  self.ws_bytes, self._stream(stream)), "mc_layer_forward")
+        _check(L.mc_layer_forward_opt(self.shape, self.weights, self.rotary, self.attention, x, y,
+                                      self.saved, self.ws, self.ws_bytes, self._stream(stream)),
+               "mc_layer_forward")
         self._x = x
         return y
 
@@ -103,9 +116,9 @@ class TransformerLayer:
         x = self._x if x is None else x
         if dx is None:
             dx = torch.empty_like(dy)
-        _check(L.mc_layer_backward(self.shape, self.weights, x, dy, self.saved, dx, self._grads_c,
-                                   self.ws, self.ws_bytes, self._stream(stream)),
-               "mc_layer_backward")
+        _check(L.mc_layer_backward_opt(self.shape, self.weights, self.rotary, self.attention, x, dy,
+                                       self.saved, dx, self._grads_c, self.ws, self.ws_bytes,
+                                       self._stream(stream)), "mc_layer_backward")
         return dx
 
     def device_status(self, stream=None) -> int:
