@@ -34,8 +34,7 @@ struct ScoreConst {
 };
 
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ ScoreConst score_const(float rsqrt_d, float softcap, const float* slopes,
-                                                  int head) {
+__device__ __forceinline__ ScoreConst score_const(float rsqrt_d, float softcap, float slope) {
   ScoreConst c;
   c.mul = rsqrt_d * kOptLog2e;
   c.cap2 = 0.f;
@@ -44,7 +43,7 @@ __device__ __forceinline__ ScoreConst score_const(float rsqrt_d, float softcap, 
     c.mul = 2.f * rsqrt_d * kOptLog2e / softcap;
     c.cap2 = softcap * kOptLog2e;
   }
-  if constexpr (BIAS) c.slope2 = slopes[head] * kOptLog2e;
+  if constexpr (BIAS) c.slope2 = slope * kOptLog2e;
   return c;
 }
 
@@ -67,6 +66,40 @@ __device__ __forceinline__ bool opt_entry(const int32_t* tables, bool head_major
   const bool ok = entry.x >= 0 && entry.x < b && entry.y >= 0 && entry.y < nb;
   if (!ok && threadIdx.x == 0) record_error(status, MC_ERR_DEVICE_BOUNDS, kSiteAttention);
   return ok;
+}
+
+// Items of a persistent kernel, (table entry, head) pairs: heads are taken in
+// groups of `group`, within a group the longest entries of all its heads come
+// first, and the grid's CTAs are dealt them in a snake, so that their shares
+// are even.  A group's K and V are what the CTAs running together read again
+// and again: the group is as large as fits in L2 beside everything else.
+inline int opt_head_group(int b, int s, int H, int d) {
+  const int64_t head_bytes = static_cast<int64_t>(b) * s * d * 4;  // K and V of one head
+  const int64_t fit = (64ll << 20) / head_bytes;
+  return static_cast<int>(fit < 1 ? 1 : fit < H ? fit : H);
+}
+
+// Item r of this CTA: its table rank and head; false when its share is done.
+// (b ceil(s / 128) H < 2^31 by the entry points' limits.)
+__device__ __forceinline__ bool opt_item(int r, int n, int H, int group, int& rank, int& hh) {
+  const unsigned G = gridDim.x, c = blockIdx.x;
+  const unsigned k = static_cast<unsigned>(r) * G + ((r & 1) ? G - 1 - c : c);
+  if (k >= static_cast<unsigned>(n) * static_cast<unsigned>(H)) return false;
+  const unsigned per_group = static_cast<unsigned>(n) * static_cast<unsigned>(group);
+  const unsigned g0 = k / per_group * static_cast<unsigned>(group);  // the group's first head
+  const unsigned heads = min(static_cast<unsigned>(group), static_cast<unsigned>(H) - g0);
+  const unsigned in = k - g0 * static_cast<unsigned>(n);
+  rank = static_cast<int>(in / heads);
+  hh = static_cast<int>(g0 + in % heads);
+  return true;
+}
+
+// A table entry that is not one of this shape is reported and taken as an
+// empty one of block 0.
+__device__ __forceinline__ int4 opt_checked(int4 e, int b, int nb, int* status) {
+  if (e.x >= 0 && e.x < b && e.y >= 0 && e.y < nb) return e;
+  record_error(status, MC_ERR_DEVICE_BOUNDS, kSiteAttention);
+  return make_int4(0, 0, 0, 0);
 }
 
 }  // namespace mc

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t my_cols = lane_off + static_cast<uint32_t>(half * 64);
     const ScoreConst sc =
-        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, A.slopes, hh);
+        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, BIAS ? A.slopes[hh] : 0.f);
     const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s;  // of lse and delta
     const int64_t brow = static_cast<int64_t>(bi) * s;             // of the intervals
     // What query t of the next block brings, loaded one block ahead (half 0).
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
     const int r = q0 + quarter * 32 + lane;  // this thread's query row
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const ScoreConst sc =
-        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, A.slopes, hh);
+        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, BIAS ? A.slopes[hh] : 0.f);
     float my_l2 = 0.f, my_d = 0.f;
     int lo = 0, hi = 0x7fffffff;  // rows past the sequence: zeros, never stored
     if (ok_entry && r < s) {

@@ -2,18 +2,20 @@
 // capped by a tanh and biased by the distance:
 //   O_i = sum_j P_ij V_j over the keys j in [lo_i, hi_i), P the softmax.
 //
-// One CTA per (128-query block, head), longest key ranges first (the mask's
-// tables), walks the 128-key blocks between its rows' lowest and highest key
-// with one running maximum and sum per row.  192 threads:
-//   warp 0      TMA: Q once, K and V blocks
-//   warp 1      TMEM and the MMA thread: S = Q K^T, O += P V
-//   warps 2..5  softmax: thread = row, the row's 128 scores in registers
-// Two CTAs share an SM (256 TMEM columns and at most 113 KB of shared memory
-// each): while one is in its softmax, or fetches its first blocks or writes
-// its O, the other's products keep the tensor cores busy.  That is why S has
-// no second buffer (P_j takes S_j's columns, S_{j+1} follows O += P_j V_j),
-// and it suits packed documents, whose CTAs have one to a few key blocks.
-// TMEM: S [0, 128) with P (bf16 pairs) over [0, 64), O [128, 128 + D).
+// Persistent: one CTA per SM walks the (128-query block, head) items, each
+// over the 256-key blocks between its rows' lowest and highest key (the last
+// one only half, where 128 keys or fewer are left) with one running maximum
+// and sum per row.  384 threads:
+//   warp 0       the items' table entries into shared memory, and TMA: Q once
+//                per item, K blocks into a 2-deep ring, V as 128-key halves
+//                into a ring, running on across items
+//   warp 1       TMEM and the MMA thread: S = Q K^T, O += P V
+//   warps 4..11  softmax, two warps per TMEM lane quarter: a thread takes 128
+//                of its row's 256 scores; the two exchange maxima and sums
+// S_{g+1} is formed while the softmax of block g runs (P has TMEM columns of
+// its own), across items too: packed documents have items of one to a few
+// blocks, which start-up and drain would dominate otherwise.
+// TMEM: S [0, 256), O [256, 256 + D), P [384, 512) (bf16 pairs, 256 keys).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,23 +25,43 @@
 namespace mc {
 namespace {
 
-constexpr int kOptFwdThreads = 192;
+constexpr int kOptFwdThreads = 384;
+// The launch gives every thread 168 registers (384 x 168 = 64,512); the
+// softmax warpgroups, which hold a row's 128 scores, take what the producer's
+// leaves: 128 x 72 + 256 x 216 = 64,512.
+constexpr int kOptRegsIo = 72, kOptRegsSoftmax = 216;
+constexpr int kOptKeys = 256;  // keys per block
+constexpr int kOptRing = 4;    // items in shared memory
 // O is rescaled only when a row's maximum grows by more than this (log2
 // units): P stays below 2^8 and the final division by the sum, taken against
 // the same maximum, cancels the difference.
 constexpr float kOptRescale = 8.0f;
 
+// What every role needs to know of an item.
+struct alignas(16) OptItem {
+  int4 entry;  // sequence, query block, lowest visible key, 128-key halves (-1: no more items)
+  int head;
+  int pad[3];
+};
+
 template <int D>
 struct OptFwdCfg {
-  static constexpr int kChunks = D / 64;        // 128-byte boxes per row
-  static constexpr int kTile = 128 * D * 2;     // 128 rows of Q, K or V
-  static constexpr int kStages = D == 64 ? 2 : 1;
-  static constexpr int kBars = 16 * 8;
-  static constexpr int kUsed = kTile + 2 * kStages * kTile + kBars;
-  static constexpr int kSmem = kUsed + 1024;    // + alignment slack
-  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
-  static constexpr uint32_t kTmemCols = 256;
-  static constexpr uint32_t kColS = 0, kColO = 128;
+  static constexpr int kChunks = D / 64;           // 128-byte boxes per row
+  static constexpr int kQTile = 128 * D * 2;       // Q [128][D] bf16
+  static constexpr int kKTile = kOptKeys * D * 2;  // K [256][D] bf16
+  static constexpr int kChunkBytes = kOptKeys * 128;  // one 64-wide d chunk of 256 rows
+  static constexpr int kHalf = 128 * D * 2;        // 128 rows of K or V
+  static constexpr int kVSlots = D == 64 ? 4 : 2;
+  static constexpr int kXch = 2 * 2 * 128 * 4;     // [parity][half][row] floats
+  static constexpr int kBars = 40 * 8;
+  // The dynamic shared memory starts 1024-byte aligned (checked at run time),
+  // so no alignment slack is reserved: at D = 128 it would not fit.
+  static constexpr int kUsed = kQTile + 2 * kKTile + kVSlots * kHalf + kXch +
+                               kOptRing * static_cast<int>(sizeof(OptItem)) + kBars;
+  static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
+  static_assert(kUsed <= 227 * 1024, "forward shared memory");
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0, kColO = 256, kColP = 384;
 };
 
 struct OptFwdArgs {
@@ -51,49 +73,69 @@ struct OptFwdArgs {
   const float* slopes;
   float softcap;
   int b, s, H;
-  int head_major;
+  int head_group;
   int* status;
 };
 
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kOptFwdThreads, 2)
+__global__ void __launch_bounds__(kOptFwdThreads, 1)
     attn_opt_fwd_kernel(const __grid_constant__ CUtensorMap tm,
                         const __grid_constant__ OptFwdArgs A) {
   using C = OptFwdCfg<D>;
-  constexpr int KS = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sK = smem + C::kTile;
-  uint8_t* sV = sK + KS * C::kTile;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + KS * C::kTile);
-  uint64_t* q_full = bars + 0;
-  uint64_t* k_full = bars + 1;    // [KS]
-  uint64_t* k_empty = bars + 3;   // [KS]  after S_j
-  uint64_t* v_full = bars + 5;    // [KS]
-  uint64_t* v_empty = bars + 7;   // [KS]  after O += P_j V_j
-  uint64_t* s_full = bars + 9;    // S_j in TMEM
-  uint64_t* p_full = bars + 10;   // P_j in TMEM (128 threads)
-  uint64_t* pv_done = bars + 11;  // O += P_j V_j complete
-  uint64_t* drain = bars + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 13);
+  constexpr int VS = C::kVSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
   int* status = A.status;
+  if (smem_u32(smem) & 1023u) {  // the 128-byte swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) record_error(status, MC_ERR_DEVICE_BOUNDS, kSiteAttention);
+    return;
+  }
+  uint8_t* sQ = smem;
+  uint8_t* sK[2] = {smem + C::kQTile, smem + C::kQTile + C::kKTile};
+  uint8_t* sV0 = smem + C::kQTile + 2 * C::kKTile;
+  float* xch = reinterpret_cast<float*>(sV0 + VS * C::kHalf);
+  OptItem* items = reinterpret_cast<OptItem*>(reinterpret_cast<uint8_t*>(xch) + C::kXch);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kOptRing);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;    // the item's last S
+  uint64_t* k_full = bars + 2;     // [2]
+  uint64_t* k_empty = bars + 4;    // [2]  after S
+  uint64_t* v_full = bars + 6;     // [4] per half-tile slot (VS used)
+  uint64_t* v_empty = bars + 10;   // [4]  after the half's PV steps
+  uint64_t* s_full = bars + 14;    // S in TMEM
+  uint64_t* s_free = bars + 15;    // the softmax holds S in registers (256 threads)
+  uint64_t* p_full = bars + 16;    // P in TMEM (256 threads)
+  uint64_t* pv_done = bars + 17;   // O += P V complete
+  uint64_t* o_free = bars + 18;    // the item's O is in registers (256 threads)
+  uint64_t* drain = bars + 19;
+  uint64_t* xbar = bars + 20;      // [4] per lane quarter: the halves' exchange (64 threads)
+  uint64_t* it_full = bars + 24;   // [kOptRing]
+  uint64_t* it_empty = bars + 28;  // [kOptRing] read by the MMA thread and the softmax (257)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = A.s, a = A.H * D;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int i = 0; i < KS; ++i) {
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < VS; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_full, 128);
+    mbar_init(s_free, 256);
+    mbar_init(p_full, 256);
     mbar_init(pv_done, 1);
+    mbar_init(o_free, 256);
     mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 64);
+    for (int i = 0; i < kOptRing; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 257);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tm);
   }
@@ -106,234 +148,411 @@ __global__ void __launch_bounds__(kOptFwdThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the previous kernel on the stream has completed
-  const uint32_t tS = tmem + C::kColS, tO = tmem + C::kColO;
+  const uint32_t tS = tmem + C::kColS, tO = tmem + C::kColO, tP = tmem + C::kColP;
 
-  int4 entry;  // sequence, query block, lowest and highest visible key
-  int hh;
-  const bool ok_entry =
-      opt_entry(A.tables, A.head_major != 0, A.b, (s + 127) / 128, entry, hh, status);
-  const int bi = entry.x;
-  const int q0 = entry.y * 128;
-  const int k_lo = max(entry.z, 0), k_hi = min(entry.w, s);
-  const int n_kb = ok_entry && k_hi > k_lo ? (k_hi - k_lo + 127) / 128 : 0;
-
-  if (warp == 0) {
-    if (lane == 0 && n_kb > 0) {
-      // -------------------------------------------------------- producer
-      mbar_arrive_expect_tx(q_full, C::kTile);
-      for (int c = 0; c < C::kChunks; ++c)
-        tma_load_3d(sQ + c * 16384, &tm, q_full, hh * D + c * 64, q0, bi);
-      int k_issued = 0, v_issued = 0;
-      for (int j = 0; j < n_kb; ++j) {
-        const int st = j % KS;
-        const uint32_t ph = ((j / KS) & 1) ^ 1u;
-        if (!mbar_wait(&k_empty[st], ph, status, kSiteAttention)) break;
-        mbar_arrive_expect_tx(&k_full[st], C::kTile);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d(sK + st * C::kTile + c * 16384, &tm, &k_full[st], a + hh * D + c * 64,
-                      k_lo + j * 128, bi);
-        ++k_issued;
-        if (!mbar_wait(&v_empty[st], ph, status, kSiteAttention)) break;
-        mbar_arrive_expect_tx(&v_full[st], C::kTile);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d(sV + st * C::kTile + c * 16384, &tm, &v_full[st], 2 * a + hh * D + c * 64,
-                      k_lo + j * 128, bi);
-        ++v_issued;
-      }
-      pdl_launch();  // every load of this CTA is issued
-      // Copies still in flight must land before the CTA exits.
-      mbar_wait(q_full, 0, status, kSiteAttention, 200000000ull, false);
-      for (int j = k_issued - 1; j >= 0 && j >= k_issued - KS; --j)
-        mbar_wait(&k_full[j % KS], (j / KS) & 1, status, kSiteAttention, 200000000ull, false);
-      for (int j = v_issued - 1; j >= 0 && j >= v_issued - KS; --j)
-        mbar_wait(&v_full[j % KS], (j / KS) & 1, status, kSiteAttention, 200000000ull, false);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && n_kb > 0) {
-      // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
-      const uint32_t qb = smem_u32(sQ);
-      auto issue_s = [&](int j) -> bool {
-        const int st = j % KS;
-        if (!mbar_wait(&k_full[st], (j / KS) & 1, status, kSiteAttention)) return false;
-        tc_fence_after();
-        const uint32_t kbase = smem_u32(sK + st * C::kTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_bf16(tS, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kbase + off, 16, 1024),
-                    kIdescQK, kk > 0 ? 1u : 0u);
+  // Every role walks the same items (r) and blocks (g, across items).
+  if (warp < 4) {
+    setmaxnreg_dec<kOptRegsIo>();
+    if (warp == 0) {
+      if (lane == 0) {
+        // -------------------------------------------------------- producer
+        const int nb = (s + 127) / 128;
+        int g = 0, u = 0, q_n = 0;  // K blocks, V halves and Q tiles issued
+        bool ok = true;
+        // V of a block is loaded after K of the next: what is left to load
+        int v_halves = 0, v_row = 0, v_col = 0, v_bi = 0;
+        auto load_v = [&]() {
+          for (int h = 0; ok && h < v_halves; ++h) {
+            const int slot = u % VS;
+            if (!mbar_wait(&v_empty[slot], ((u / VS) & 1) ^ 1u, status, kSiteAttention)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&v_full[slot], C::kHalf);
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(sV0 + slot * C::kHalf + c * 16384, &tm, &v_full[slot], v_col + c * 64,
+                          v_row + h * 128, v_bi);
+            ++u;
+          }
+          v_halves = 0;
+        };
+        // Items are announced one ahead, so that the softmax can fetch the next
+        // one's intervals early, and their table entries are read two ahead.
+        int4 e_next = make_int4(0, 0, 0, 0);
+        int h_next = 0;
+        bool more = true;
+        auto read_entry = [&](int r) {
+          int rank = 0;
+          more = opt_item(r, A.b * nb, A.H, A.head_group, rank, h_next);
+          if (more) e_next = *reinterpret_cast<const int4*>(A.tables + 4ll * rank);
+        };
+        auto announce = [&](int r, OptItem& it) -> bool {
+          it.entry = make_int4(0, 0, 0, -1);
+          it.head = h_next;
+          if (more) {
+            const int4 e = opt_checked(e_next, A.b, nb, status);
+            const int k_lo = max(e.z, 0), k_hi = min(e.w, s);
+            it.entry = make_int4(e.x, e.y, k_lo, k_hi > k_lo ? (k_hi - k_lo + 127) / 128 : 0);
+          }
+          const int slot = r % kOptRing;
+          if (!mbar_wait(&it_empty[slot], ((r / kOptRing) & 1) ^ 1u, status, kSiteAttention))
+            return false;
+          items[slot].entry = it.entry;
+          items[slot].head = it.head;
+          mbar_arrive(&it_full[slot]);
+          read_entry(r + 1);
+          return true;
+        };
+        OptItem cur, next;
+        read_entry(0);
+        ok = announce(0, cur);
+        for (int r = 0; ok && cur.entry.w >= 0; ++r, cur = next) {
+          const int bi = cur.entry.x, k_lo = cur.entry.z, halves = cur.entry.w;
+          const int hh = cur.head;
+          // Announcing waits for an earlier item's softmax, which waits for its
+          // last V: with empty items in between that V is not left pending.
+          if (halves == 0) load_v();
+          if (!ok || !(ok = announce(r + 1, next))) break;
+          for (int j = 0; ok && 2 * j < halves; ++j, ++g) {
+            if (j == 0) {
+              if (!(ok = mbar_wait(q_empty, (q_n & 1) ^ 1u, status, kSiteAttention))) break;
+              mbar_arrive_expect_tx(q_full, C::kQTile);
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(sQ + c * 16384, &tm, q_full, hh * D + c * 64, cur.entry.y * 128, bi);
+              ++q_n;
+            }
+            const int ks = g & 1, nh = min(2, halves - 2 * j);
+            if (!(ok = mbar_wait(&k_empty[ks], ((g >> 1) & 1) ^ 1u, status, kSiteAttention))) break;
+            mbar_arrive_expect_tx(&k_full[ks], nh * C::kHalf);
+            for (int c = 0; c < C::kChunks; ++c)
+              for (int h = 0; h < nh; ++h)
+                tma_load_3d(sK[ks] + c * C::kChunkBytes + h * 16384, &tm, &k_full[ks],
+                            a + hh * D + c * 64, k_lo + j * kOptKeys + h * 128, bi);
+            load_v();
+            v_halves = nh;
+            v_row = k_lo + j * kOptKeys;
+            v_col = 2 * a + hh * D;
+            v_bi = bi;
+          }
         }
-        umma_commit(s_full);
-        umma_commit(&k_empty[st]);
+        if (ok) load_v();
+        pdl_launch();  // every load of this CTA is issued
+        // Copies still in flight must land before the CTA exits.
+        if (q_n > 0) mbar_wait(q_full, (q_n - 1) & 1, status, kSiteAttention, 200000000ull, false);
+        for (int i = g - 1; i >= 0 && i >= g - 2; --i)
+          mbar_wait(&k_full[i & 1], (i >> 1) & 1, status, kSiteAttention, 200000000ull, false);
+        for (int i = u - 1; i >= 0 && i >= u - VS; --i)
+          mbar_wait(&v_full[i % VS], (i / VS) & 1, status, kSiteAttention, 200000000ull, false);
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      // The whole warp walks the loop, so that addresses and descriptors stay
+      // in uniform registers; one lane issues.
+      constexpr uint32_t kIdescQK1 = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdescQK2 = idesc_bf16_f32(128, 256, false, false);
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
+      const bool leader = elect_one();
+      // K-major Q and K (1024 B per 8 rows), MN-major V (64-wide d chunks 16 KB apart)
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sK[0]), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sV0), 16384, 1024);
+      int g = 0, u = 0, n_items = 0;  // blocks and V halves (of the products), items with blocks
+      int p_halves = 0;               // the block whose O += P V is still to be issued
+      bool p_first = false, ok = true;
+      auto issue_pv = [&](int gp) -> bool {
+        if (!mbar_wait_warp(p_full, gp & 1, status, kSiteAttention)) return false;
+        // the previous item's O has been read
+        if (p_first && n_items > 1 &&
+            !mbar_wait_warp(o_free, n_items & 1, status, kSiteAttention))
+          return false;
+        for (int h = 0; h < p_halves; ++h, ++u) {
+          const int slot = u % VS;
+          if (!mbar_wait_warp(&v_full[slot], (u / VS) & 1, status, kSiteAttention)) return false;
+          tc_fence_after();
+          const uint64_t vd = smem_desc_add(v_desc, slot * C::kHalf);
+          const uint32_t acc = !p_first || h > 0 ? 1u : 0u;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              // 16 keys: 8 packed columns of P, 16 rows of 128 B of V
+              umma_bf16_ts(tO, tP + (8 * h + kk) * 8, smem_desc_add(vd, kk * 2048), kIdescPV,
+                           kk > 0 ? 1u : acc);
+            umma_commit(&v_empty[slot]);
+          }
+        }
+        if (leader) umma_commit(pv_done);
+        __syncwarp();
         return true;
       };
-      bool ok = mbar_wait(q_full, 0, status, kSiteAttention) && issue_s(0);
-      for (int j = 0; ok && j < n_kb; ++j) {
-        const int st = j % KS;
-        if (!mbar_wait(p_full, j & 1, status, kSiteAttention)) break;
-        if (!mbar_wait(&v_full[st], (j / KS) & 1, status, kSiteAttention)) break;
-        tc_fence_after();
-        const uint32_t vb = smem_u32(sV + st * C::kTile);
+      for (int r = 0; ok; ++r) {
+        const int slot = r % kOptRing;
+        if (!(ok = mbar_wait_warp(&it_full[slot], (r / kOptRing) & 1, status, kSiteAttention)))
+          break;
+        const int halves = __shfl_sync(0xffffffffu, items[slot].entry.w, 0);
+        if (leader) mbar_arrive(&it_empty[slot]);
+        if (halves < 0) break;
+        if (halves == 0 && p_halves > 0) {
+          // nothing to overlap with, and the items behind may wait for this one
+          if (!(ok = issue_pv(g - 1))) break;
+          p_halves = 0;
+        }
+        for (int j = 0; ok && 2 * j < halves; ++j, ++g) {
+          const int ks = g & 1, nh = min(2, halves - 2 * j);
+          // S_g before the products of block g - 1, unless those are ready
+          // first (an item's first S waits for its Q).
+          if (j == 0) {
+            if (p_halves > 0) {
+              const int first = mbar_wait_first(q_full, n_items & 1, p_full, (g - 1) & 1, status,
+                                                kSiteAttention);
+              if (__all_sync(0xffffffffu, first == 2)) {
+                if (!(ok = issue_pv(g - 1))) break;
+                p_halves = 0;
+              }
+            }
+            if (!(ok = mbar_wait_warp(q_full, n_items & 1, status, kSiteAttention))) break;
+          }
+          if (!(ok = mbar_wait_warp(&k_full[ks], (g >> 1) & 1, status, kSiteAttention))) break;
+          // S still holds block g - 1 until the softmax has it in registers.
+          if (g > 0 && !(ok = mbar_wait_warp(s_free, (g - 1) & 1, status, kSiteAttention))) break;
+          tc_fence_after();
+          const uint64_t kd = smem_desc_add(k_desc, ks * C::kKTile);
+          const uint32_t idesc = nh == 2 ? kIdescQK2 : kIdescQK1;
+          if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          // P: 16 keys = 8 packed columns; V (MN-major): 16 key rows of
-          // 128 B, 64-wide d chunks 16 KB apart
-          umma_bf16_ts(tO, tS + kk * 8, smem_desc_sw128(vb + kk * 2048, 16384, 1024), kIdescPV,
-                       (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&v_empty[st]);
-        umma_commit(pv_done);
-        if (j + 1 < n_kb) {
-          // S_{j+1} overwrites the P_j that the products above read
-          if (!mbar_wait(pv_done, j & 1, status, kSiteAttention)) break;
-          ok = issue_s(j + 1);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_bf16(tS, smem_desc_add(q_desc, (kk >> 2) * 16384 + (kk & 3) * 32),
+                        smem_desc_add(kd, (kk >> 2) * C::kChunkBytes + (kk & 3) * 32), idesc,
+                        kk > 0 ? 1u : 0u);
+            umma_commit(s_full);
+            umma_commit(&k_empty[ks]);
+            if (2 * (j + 1) >= halves) umma_commit(q_empty);
+          }
+          __syncwarp();
+          if (p_halves > 0 && !(ok = issue_pv(g - 1))) break;
+          p_halves = nh;
+          p_first = j == 0;
+          if (j == 0) ++n_items;
         }
       }
-      umma_commit(drain);
-      mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+      if (ok && p_halves > 0) issue_pv(g - 1);
+      if (leader) {
+        umma_commit(drain);
+        mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------- softmax
+    setmaxnreg_inc<kOptRegsSoftmax>();
     const int quarter = warp & 3;
+    const int half = (warp - 4) >> 2;  // keys [128 half, 128 half + 128) of a block
     const int row = quarter * 32 + lane;
-    const int q = q0 + row;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // Rows past the sequence (zeros from the TMA, never stored) see everything,
-    // so that they do not make a block an edge.
-    int lo = 0, hi = 0x7fffffff;
-    if (ok_entry && q < s) {
-      lo = A.key_lo[static_cast<int64_t>(bi) * s + q];
-      hi = min(A.key_hi[static_cast<int64_t>(bi) * s + q], s);
-    }
-    const ScoreConst sc =
-        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, A.slopes, hh);
-    float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n_kb; ++j) {
-      // S_j in TMEM also means that O += P_{j-1} V_{j-1} is complete
-      if (!mbar_wait_warp(s_full, j & 1, status, kSiteAttention)) {
+    // Exchange with the other half of the row (bounded wait on the quarter's
+    // barrier); slots alternate by phase so a fast peer never overwrites a
+    // value the other has not read.
+    int xphase = 0;
+    auto exchange = [&](float v) -> float {
+      float* slot = xch + (xphase & 1) * 256;
+      slot[half * 128 + row] = v;
+      mbar_arrive(&xbar[quarter]);
+      if (!mbar_wait(&xbar[quarter], xphase & 1, status, kSiteAttention)) ok = false;
+      const float peer = slot[(half ^ 1) * 128 + row];
+      ++xphase;
+      return peer;
+    };
+    // This row's interval and slope in item r, fetched one item ahead.  Rows
+    // past the sequence (zeros from the TMA, never stored) see everything, so
+    // that they do not make a block an edge.
+    int lo = 0, hi = 0;
+    float slope = 0.f;
+    auto fetch = [&](int r) {
+      const int slot = r % kOptRing;
+      if (!mbar_wait_warp(&it_full[slot], (r / kOptRing) & 1, status, kSiteAttention)) {
         ok = false;
-        break;
+        return;
       }
-      tc_fence_after();
-      float x[128];
+      const OptItem& it = items[slot];
+      lo = 0;
+      hi = 0x7fffffff;
+      const int q = it.entry.y * 128 + row;
+      if (it.entry.w >= 0 && q < s) {
+        lo = A.key_lo[static_cast<int64_t>(it.entry.x) * s + q];
+        hi = A.key_hi[static_cast<int64_t>(it.entry.x) * s + q];
+        if constexpr (BIAS) slope = A.slopes[it.head];
+      }
+    };
+    fetch(0);
+    int g = 0;
+    for (int r = 0; ok; ++r) {
+      const OptItem& it = items[r % kOptRing];
+      const int halves = it.entry.w;
+      if (halves < 0) break;
+      const int q = it.entry.y * 128 + row, k_lo = it.entry.z;
+      const int row_lo = lo, row_hi = q < s ? min(hi, s) : hi;
+      const ScoreConst sc =
+          score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
+      fetch(r + 1);
+      if (!ok) break;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; 2 * j < halves; ++j, ++g) {
+        if (!mbar_wait_warp(s_full, g & 1, status, kSiteAttention)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float x[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32_nowait(tS + lane_off + 32 * c, x + 32 * c);
-      tmem_ld_wait();
-      const int key0 = k_lo + j * 128;
-      // ---- scores in log2 units (without cap and bias the scale is folded
-      //      into the exponent's argument below)
-      if constexpr (CAP || BIAS) {
-        float2 add = make_float2(sc.cap2, sc.cap2);
-        const float base = static_cast<float>(key0 - q);
+        for (int c = 0; c < 4; ++c)
+          tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 128 + 32 * c, x + 32 * c);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(s_free);
+        const int key0 = k_lo + j * kOptKeys + half * 128;
+        // ---- scores in log2 units (without cap and bias the scale is folded
+        //      into the exponent's argument below)
+        if constexpr (CAP || BIAS) {
+          const float base = sc.slope2 * static_cast<float>(key0 - q);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            float2 y = make_float2(x[2 * i], x[2 * i + 1]);
+            if constexpr (CAP)
+              y = __ffma2_rn(cap_r(y, sc.mul), make_float2(-2.f * sc.cap2, -2.f * sc.cap2),
+                             make_float2(sc.cap2, sc.cap2));
+            else
+              y = __fmul2_rn(y, make_float2(sc.mul, sc.mul));
+            if constexpr (BIAS) {
+              y.x -= fabsf(fmaf(sc.slope2, static_cast<float>(2 * i), base));
+              y.y -= fabsf(fmaf(sc.slope2, static_cast<float>(2 * i + 1), base));
+            }
+            x[2 * i] = y.x;
+            x[2 * i + 1] = y.y;
+          }
+        }
+        // ---- keys [first, end) of this half are visible
+        // (the last block may lack its second half, whose S is an older one)
+        const int first = row_lo - key0;
+        const int end = 2 * j + half < halves ? row_hi - key0 : 0;
+        if (__any_sync(0xffffffffu, end < 128)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = i < end ? x[i] : -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, first > 0)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = i >= first ? x[i] : -INFINITY;
+        }
+        // ---- row maximum: four chains of three-input maxima, then a tree
+        float mc[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int p = 0; p < 62; ++p) mc[p & 3] = fmax3f(mc[p & 3], x[4 + 2 * p], x[5 + 2 * p]);
+        float mx = fmaxf(fmax3f(mc[0], mc[1], mc[2]), mc[3]);
+        mx = fmaxf(mx, exchange(mx));
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const float mul = CAP || BIAS ? 1.f : sc.mul;
+        mx *= mul;  // > 0
+        const float m_new = fmaxf(m, mx);
+        // a row that has seen nothing yet (m = -infinity) has l = 0 and O = 0
+        const bool need = j > 0 && m_new > m + kOptRescale;
+        float alpha = 1.f;
+        if (j == 0) m = m_new;
+        if (need) {
+          alpha = fast_exp2(m - m_new);
+          l *= alpha;
+          m = m_new;
+        }
+        const float m_use = m == -INFINITY ? 0.f : m;
+        // ---- P, its row sum in 32 bits, and P as bf16 in registers, while the
+        //      products of the block before may still run
+        //      (in place: pair i of the bf16 P takes score i's register, which
+        //      pair i / 2 was the last to need)
+        float2 sm2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+        const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-m_use, -m_use);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          float2 y = make_float2(x[2 * i], x[2 * i + 1]);
-          if constexpr (BIAS) {
-            add.x = fmaf(-sc.slope2, fabsf(base + (2 * i)), sc.cap2);
-            add.y = fmaf(-sc.slope2, fabsf(base + (2 * i + 1)), sc.cap2);
+          const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
+          const float2 y = CAP || BIAS ? __fadd2_rn(xi, negm2) : __ffma2_rn(xi, mul2, negm2);
+          const float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          sm2[i & 3] = __fadd2_rn(sm2[i & 3], pv);
+          x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));
+        }
+        const float2 s01 = __fadd2_rn(__fadd2_rn(sm2[0], sm2[1]), __fadd2_rn(sm2[2], sm2[3]));
+        l += s01.x + s01.y;
+        // The products of block g - 1 have to be complete before O is rescaled
+        // or P overwritten.
+        if (g > 0 && !mbar_wait_warp(pv_done, (g - 1) & 1, status, kSiteAttention)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+          for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+            float v[16];
+            tmem_ld_32x32b_x16(tO + lane_off + c * 16, v);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * alpha);
+            tmem_st_32x32b_x16(tO + lane_off + c * 16, w);
           }
-          if constexpr (CAP)
-            y = __ffma2_rn(cap_r(y, sc.mul), make_float2(-2.f * sc.cap2, -2.f * sc.cap2), add);
-          else
-            y = __ffma2_rn(y, make_float2(sc.mul, sc.mul), add);
-          x[2 * i] = y.x;
-          x[2 * i + 1] = y.y;
         }
-      }
-      // ---- keys [lo, hi) are visible
-      if (__any_sync(0xffffffffu, lo > key0 || hi < key0 + 128)) {
-        const int first = lo - key0, end = hi - key0;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) x[i] = (i >= first && i < end) ? x[i] : -INFINITY;
-      }
-      // ---- running maximum: four chains of three-input maxima, then a tree
-      float mc[4] = {x[0], x[1], x[2], x[3]};
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
 #pragma unroll
-      for (int p = 0; p < 62; ++p) mc[p & 3] = fmax3f(mc[p & 3], x[4 + 2 * p], x[5 + 2 * p]);
-      float mx = fmaxf(fmax3f(mc[0], mc[1], mc[2]), mc[3]);
-      const float mul = CAP || BIAS ? 1.f : sc.mul;
-      mx *= mul;  // > 0
-      const float m_new = fmaxf(m, mx);
-      // a row that has seen nothing yet (m = -infinity) has l = 0 and O = 0
-      const bool need = j > 0 && m_new > m + kOptRescale;
-      float alpha = 1.f;
-      if (j == 0) m = m_new;
-      if (need) {
-        alpha = fast_exp2(m - m_new);
-        l *= alpha;
-        m = m_new;
-      }
-      const float m_use = m == -INFINITY ? 0.f : m;
-      // ---- P, its row sum in 32 bits, and P as bf16 for the product
-      uint32_t pk[64];
-      float2 sm2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-      const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-m_use, -m_use);
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
-        const float2 y = CAP || BIAS ? __fadd2_rn(xi, negm2) : __ffma2_rn(xi, mul2, negm2);
-        const float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-        sm2[i & 3] = __fadd2_rn(sm2[i & 3], pv);
-        pk[i] = pack_bf16x2(pv.x, pv.y);
-      }
-      const float2 s01 = __fadd2_rn(__fadd2_rn(sm2[0], sm2[1]), __fadd2_rn(sm2[2], sm2[3]));
-      l += s01.x + s01.y;
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          float v[16];
-          tmem_ld_32x32b_x16(tO + lane_off + c * 16, v);
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * alpha);
-          tmem_st_32x32b_x16(tO + lane_off + c * 16, w);
+          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(x[c * 32 + i]);
+          tmem_st_32x32b_x32(tP + lane_off + half * 64 + c * 32, w);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full);
       }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = pk[c * 32 + i];
-        tmem_st_32x32b_x32(tS + lane_off + c * 32, w);
+      if (!ok) break;
+      const bool empty = halves == 0;
+      if (!empty) {
+        l += exchange(l);  // both halves' sums, taken against the same maximum
+        if (ok) ok = mbar_wait(pv_done, (g - 1) & 1, status, kSiteAttention);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_full);
-    }
-    if (n_kb > 0 && ok)
-      ok = mbar_wait_warp(pv_done, (n_kb - 1) & 1, status, kSiteAttention);
-    if (ok && ok_entry) {
-      tc_fence_after();
+      const int bi = it.entry.x, head = it.head;
       // a row that sees nothing: O = 0, log-sum-exp = -infinity
-      const bool empty = l == 0.f;
-      const float inv = empty ? 0.f : 1.f / l;
-      uint16_t* orow = A.out + (static_cast<int64_t>(bi) * s + q) * a + hh * D;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float v[32];
-        if (n_kb > 0) {
-          tmem_ld_32x32b_x32(tO + lane_off + c * 32, v);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* orow = A.out + (static_cast<int64_t>(bi) * s + q) * a + head * D + half * (D / 2);
+      const bool store =
+          q < s && MC_DCHECK(q >= 0 && bi < A.b && head * D + D <= a, status, kSiteAttention);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {  // this thread's half of the row's O
+        float v[32] = {};
+        if (!empty) tmem_ld_32x32b_x32(tO + lane_off + half * (D / 2) + c * 32, v);
+        if (!empty && c == D / 64 - 1) {
+          tc_fence_before();
+          mbar_arrive(o_free);  // the next item's products may overwrite O
         }
-        if (q < s && MC_DCHECK(q >= 0 && hh * D + c * 32 + 32 <= a, status, kSiteAttention)) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+        if (store) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint4 wv = make_uint4(0u, 0u, 0u, 0u);
-            if (!empty) {
+            if (l != 0.f) {
               wv.x = pack_bf16x2(v[8 * i + 0] * inv, v[8 * i + 1] * inv);
               wv.y = pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv);
               wv.z = pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv);
               wv.w = pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv);
             }
-            dst[i] = wv;
+            reinterpret_cast<uint4*>(orow + c * 32)[i] = wv;
           }
         }
       }
-      if (q < s)
-        A.lse[(static_cast<int64_t>(bi) * A.H + hh) * s + q] =
-            empty ? -INFINITY : (m + log2f(l)) * kOptLn2;
+      if (store && half == 0)
+        A.lse[(static_cast<int64_t>(bi) * A.H + head) * s + q] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * kOptLn2;
+      mbar_arrive(&it_empty[r % kOptRing]);
     }
   }
 
@@ -360,10 +579,10 @@ int launch_fwd(const uint16_t* qkv, const OptFwdArgs& A, cudaStream_t st) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (attr != cudaSuccess) return MC_ERR_CUDA;
-  const unsigned n = static_cast<unsigned>(A.b) * static_cast<unsigned>((A.s + 127) / 128);
-  const dim3 grid = A.head_major ? dim3(static_cast<unsigned>(A.H), n, 1u)
-                                 : dim3(n, static_cast<unsigned>(A.H), 1u);
-  launch_kernel(kern, grid, dim3(kOptFwdThreads), C::kSmem, st, 1, tm, A);
+  const int64_t items = static_cast<int64_t>(A.b) * ((A.s + 127) / 128) * A.H;
+  const int64_t ctas = num_sms();
+  launch_kernel(kern, dim3(static_cast<unsigned>(items < ctas ? items : ctas)),
+                dim3(kOptFwdThreads), C::kSmem, st, 1, tm, A);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
 
@@ -390,7 +609,7 @@ int launch_attention_opt_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int b
   A.b = b;
   A.s = s;
   A.H = H;
-  A.head_major = attention_head_major(static_cast<int64_t>(b) * ((s + 127) / 128), H, 1) ? 1 : 0;
+  A.head_group = opt_head_group(b, s, H, d);
   A.status = status;
   return d == 64 ? launch_fwd_d<64>(qkv, A, st) : launch_fwd_d<128>(qkv, A, st);
 }

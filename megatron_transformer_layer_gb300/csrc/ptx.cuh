@@ -137,6 +137,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
+// Waits until either of two phases has completed: 1 (the first one), 2 (the
+// second, the first one not), or 0 when the time limit passes as above.
+__device__ __forceinline__ int mbar_wait_first(uint64_t* bar1, uint32_t parity1, uint64_t* bar2,
+                                               uint32_t parity2, int* status, int where) {
+  const uint64_t t0 = globaltimer();
+  uint32_t spins = 0;
+  while (true) {
+    if (mbar_try_wait(bar1, parity1)) return 1;
+    if (mbar_try_wait(bar2, parity2)) return 2;
+    if ((++spins & 255u) == 0) {
+      if (peek_status(status) != 0) return 0;
+      if (globaltimer() - t0 > MC_WAIT_TIMEOUT_NS) {
+        record_error(status, MC_ERR_DEVICE_TIMEOUT, where);
+        return 0;
+      }
+    }
+  }
+}
+
 // mbar_wait for a whole warp: every lane polls (bounded), then the warp
 // agrees on one result, so warp-collective instructions that follow
 // (tcgen05.ld/st, __any_sync) always run with all lanes converged.
@@ -265,6 +284,18 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- registers
+// A warpgroup gives up or takes registers per thread; the sum over the
+// block's warpgroups must stay within what the block was launched with.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -473,6 +504,29 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   d |= static_cast<uint64_t>(1u) << 46;  // version
   d |= static_cast<uint64_t>(2u) << 61;  // SWIZZLE_128B
   return d;
+}
+
+// The descriptor `bytes` (a multiple of 16) further on; the start stays
+// within its 14 bits.
+__device__ __forceinline__ uint64_t smem_desc_add(uint64_t d, uint32_t bytes) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(d));
+  lo += bytes >> 4;
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+
+// One lane of a converged warp (the same one each time), chosen in a way that
+// keeps the warp's values uniform for the compiler.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
 }
 
 // Instruction descriptor of kind::f16 with bf16 A/B and fp32 D.

@@ -5,12 +5,13 @@
 // orthogonal).  Bound by HBM: every element is read and written once, and an
 // angle is formed once per (token, pair) and shared by all heads.
 //
-// The angle of a far position needs more than 32 bits: w is kept as a number
-// of turns in 64-bit fixed point, where whole turns drop out of the product
-// position * (inv_freq / 2 pi) by the wrap of integer arithmetic.  The
-// quotient is rounded once (53 bits), so a position of 2^24 leaves an angle
-// error of 2^-53 * 2^24 * 2 pi * inv_freq, and sincospif gets 32 bits of the
-// turn.
+// The angle of a far position needs more than 32 bits: inv_freq / 2 pi is
+// formed in integer arithmetic as turns in 64-bit fixed point (the float's 24
+// bits times 1 / 2 pi to 128 bits), and whole turns drop out of the product
+// with the position by the wrap of 64-bit integers.  A position of 2^31 leaves
+// an error of 2^-33 turns; sincospif gets 32 bits of the turn.  (The same in
+// 64-bit floats is exact enough too, but they run at 1/64 of the 32-bit rate
+// here.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,6 +28,7 @@ constexpr int kRotMaxTokens = 32;   // tokens of a block
 struct RotaryArgs {
   int64_t tokens, ld_in, ld_out;
   int heads, head_dim, pairs;
+  uint32_t div_nu, div_units_head, div_pairs;  // 2^32 / d rounded up, for divisions (fast_div)
   int units;        // work units per token: heads * units_head
   int units_head;   // pairs / VEC rotating units, then the vectors that are copied
   int tok_block;    // tokens per block
@@ -37,7 +39,7 @@ struct RotaryArgs {
 };
 
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) RotVec {
+struct alignas(sizeof(T) * VEC > 16 ? 16 : sizeof(T) * VEC) RotVec {
   T e[VEC];
 };
 
@@ -52,18 +54,61 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// n / d for n d < 2^32, with m = 2^32 / d rounded up (m d - 2^32 < d, so the
+// quotient is off by less than n / 2^32 < 1 / d); d = 1 has m = 0 (2^32).
+__device__ __forceinline__ int fast_div(int n, uint32_t m) {
+  return m == 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m));
+}
+
+// 1 / 2 pi = 0.28BE60DB 9391054A 7F09D5F4 7D4D3770 (hexadecimal), in words of
+// 32 bits from the least significant one.
+__device__ constexpr uint32_t kInvTwoPi[4] = {0x7D4D3770u, 0x7F09D5F4u, 0x9391054Au, 0x28BE60DBu};
+
+// f / 2 pi modulo 1 as 64-bit fixed point, rounded down.
+__device__ __forceinline__ uint64_t turns_fixed(float f) {
+  const uint32_t bits = __float_as_uint(f);
+  const int e = static_cast<int>((bits >> 23) & 255u);
+  const uint32_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  // f = m 2^(max(e, 1) - 150); the product m * kInvTwoPi has 5 words and 128
+  // bits behind its point
+  uint32_t w[6];
+  uint64_t carry = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    carry += static_cast<uint64_t>(m) * kInvTwoPi[i];
+    w[i] = static_cast<uint32_t>(carry);
+    carry >>= 32;
+  }
+  w[4] = static_cast<uint32_t>(carry);
+  w[5] = 0;
+  // the 64 bits from bit `at` up
+  const int at = 128 - 64 - ((e ? e : 1) - 150);
+  uint64_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const int sh = 32 * i - at;  // where word i lands
+    const uint64_t v = w[i];
+    if (sh >= 0 && sh < 64) r |= v << sh;
+    if (sh < 0 && sh > -32) r |= v >> -sh;
+  }
+  return bits >> 31 ? 0 - r : r;
+}
+
 // A unit is VEC pairs of one head (two vectors of VEC elements: the halves of
 // the pairs, or 2 VEC adjacent elements) or one copied vector.  A block takes
 // unit_block units of each of tok_block tokens, up to UPT per thread; their
 // loads are issued before the cos / sin table is formed, so one DRAM round
 // trip covers both.
 template <typename T, int VEC, bool ADJACENT, int UPT>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, UPT > 1 ? 3 : 4)
     rotary_kernel(const T* in, T* out, const int32_t* __restrict__ positions,
                   const float* __restrict__ inv_freq, const __grid_constant__ RotaryArgs A,
                   int* status) {
   using V = RotVec<T, VEC>;
-  extern __shared__ float2 table[];  // [tok_block][pairs]: cos, sin
+  // cos and sin, [tok_block][pairs] each
+  extern __shared__ __align__(16) float table[];
+  float* const t_cos = table;
+  float* const t_sin = table + A.tok_block * A.pairs;
   pdl_wait();  // the previous kernel on the stream has completed
   pdl_launch();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * A.tok_block;
@@ -75,7 +120,7 @@ __global__ void __launch_bounds__(kRotThreads)
 
   V a[UPT], b[UPT];
   int tok[UPT], pair[UPT];  // pair < 0: nothing, or a copied vector
-  int64_t off[UPT];         // of the unit's first vector within its row
+  int off[UPT];             // of the unit's first vector within its row
 #pragma unroll
   for (int k = 0; k < UPT; ++k) {
     const int e = static_cast<int>(threadIdx.x) + k * kRotThreads;
@@ -83,9 +128,9 @@ __global__ void __launch_bounds__(kRotThreads)
     off[k] = -1;
     tok[k] = 0;
     if (e < total) {
-      const int tk = e / nu;
+      const int tk = nu == A.unit_block ? fast_div(e, A.div_nu) : e / nu;
       const int u = u0 + (e - tk * nu);
-      const int h = u / A.units_head;
+      const int h = fast_div(u, A.div_units_head);
       const int w = u - h * A.units_head;
       tok[k] = tk;
       const T* row = in + (t0 + tk) * A.ld_in;
@@ -103,35 +148,40 @@ __global__ void __launch_bounds__(kRotThreads)
   }
 
   for (int i = threadIdx.x; i < ntok * A.pairs; i += kRotThreads) {
-    const int tk = i / A.pairs, p = i - tk * A.pairs;
-    const double turns = static_cast<double>(inv_freq[p]) * 0.15915494309189535;  // / 2 pi
-    const double frac = turns - floor(turns);
-    // 2^64 * frac; a frac that rounds to 1 is 0 turns
-    const uint64_t f = frac < 1.0 ? static_cast<uint64_t>(__double2ull_rn(frac * 18446744073709551616.0)) : 0;
+    const int tk = fast_div(i, A.div_pairs), p = i - tk * A.pairs;
+    const uint64_t f = turns_fixed(inv_freq[p]);
     const int64_t pos = positions[A.axis[p] * A.tokens + t0 + tk];
     const uint64_t w = static_cast<uint64_t>(A.inverse ? -pos : pos) * f;
     const float x = static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>((w + 0x80000000ull) >> 32)));
     float s, c;
     sincospif(x * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-    table[i] = make_float2(c, s);
+    t_cos[i] = c;
+    t_sin[i] = s;
   }
   __syncthreads();
 
+  int held = -1;  // the table place whose VEC entries are in cs / sn
+  RotVec<float, VEC> cs, sn;
 #pragma unroll
   for (int k = 0; k < UPT; ++k) {
     if (off[k] < 0) continue;
     T* row = out + (t0 + tok[k]) * A.ld_out;
     const int rest = pair[k] >= 0 ? (ADJACENT ? VEC : A.pairs) : 0;
     if (!MC_DCHECK(t0 + tok[k] < A.tokens &&
-                       off[k] + rest + VEC <= static_cast<int64_t>(A.heads) * A.head_dim,
+                       off[k] + rest + VEC <= A.heads * A.head_dim,
                    status, kSiteRotary))
       continue;
     if (pair[k] >= 0) {
-      const float2* cs = table + tok[k] * A.pairs + pair[k];
+      const int at = tok[k] * A.pairs + pair[k];
+      if (at != held) {
+        held = at;
+        cs = *reinterpret_cast<const RotVec<float, VEC>*>(t_cos + at);
+        sn = *reinterpret_cast<const RotVec<float, VEC>*>(t_sin + at);
+      }
       V ya, yb;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float2 r = cs[j];
+        const float2 r = make_float2(cs.e[j], sn.e[j]);
         float u, v;
         if constexpr (ADJACENT) {  // pair j: elements 2j, 2j + 1 of a | b
           u = to_f32(2 * j < VEC ? a[k].e[(2 * j) % VEC] : b[k].e[(2 * j) % VEC]);
@@ -162,7 +212,7 @@ int rotary_launch(const T* in, T* out, const int32_t* positions, const float* in
                   const RotaryArgs& A, int64_t gx, int64_t gy, int* status, cudaStream_t st) {
   launch_kernel(rotary_kernel<T, VEC, ADJACENT, UPT>,
                 dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(kRotThreads),
-                sizeof(float2) * A.tok_block * A.pairs, st, 1, in, out, positions, inv_freq, A,
+                2 * sizeof(float) * A.tok_block * A.pairs, st, 1, in, out, positions, inv_freq, A,
                 status);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
@@ -172,8 +222,7 @@ int rotary_plan(const T* in, T* out, const int32_t* positions, const float* inv_
                 int* status, cudaStream_t st) {
   const int rest = A.copy_rest ? (A.head_dim - 2 * A.pairs) / VEC : 0;
   A.units_head = A.pairs / VEC + rest;
-  const int64_t units = static_cast<int64_t>(A.heads) * A.units_head;
-  if (units > (1 << 24)) return MC_ERR_UNSUPPORTED;
+  const int64_t units = static_cast<int64_t>(A.heads) * A.units_head;  // <= 2^22
   A.units = static_cast<int>(units);
   // Four units per thread keep enough loads in flight; few units in all take
   // one per thread, so that more SMs share the call.
@@ -185,9 +234,13 @@ int rotary_plan(const T* in, T* out, const int32_t* positions, const float* inv_
   if (tb > kRotMaxTable / A.pairs) tb = kRotMaxTable / A.pairs;
   if (tb > A.tokens) tb = static_cast<int>(A.tokens);
   A.tok_block = tb;
+  auto magic = [](int d) { return d == 1 ? 0u : static_cast<uint32_t>((0x100000000ull + d - 1) / d); };
+  A.div_nu = magic(A.unit_block);
+  A.div_units_head = magic(A.units_head);
+  A.div_pairs = magic(A.pairs);
   const int64_t gx = (A.tokens + tb - 1) / tb;
   const int64_t gy = (A.units + A.unit_block - 1) / A.unit_block;
-  if (gx > 0x7fffffff || gy > 65535) return MC_ERR_UNSUPPORTED;
+  if (gx > 0x7fffffff) return MC_ERR_UNSUPPORTED;
   return small ? rotary_launch<T, VEC, ADJACENT, 1>(in, out, positions, inv_freq, A, gx, gy, status, st)
                : rotary_launch<T, VEC, ADJACENT, 4>(in, out, positions, inv_freq, A, gx, gy, status, st);
 }
@@ -241,7 +294,8 @@ int launch_rotary(const void* in, void* out, bool bf16, int64_t tokens, int head
   if (rc != MC_OK) return rc;
   if (tokens < 1 || heads < 1) return MC_ERR_SHAPE;
   const int64_t width = static_cast<int64_t>(heads) * head_dim;
-  if (width > (1 << 24)) return MC_ERR_UNSUPPORTED;
+  // (2^22 units of at most 512 per head: within fast_div)
+  if (width > (1 << 22)) return MC_ERR_UNSUPPORTED;
   if (ld_in < width || ld_out < width) return MC_ERR_SHAPE;
   if (!in || !out || !positions || !inv_freq) return MC_ERR_NULLPTR;
   const uintptr_t size = bf16 ? 2 : 4;

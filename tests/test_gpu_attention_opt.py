@@ -291,6 +291,43 @@ def test_attention_many_blocks():
     Problem("window", 6, 1200, 12, 64).check()
 
 
+@pytest.mark.parametrize("where", ["front", "back", "both"])
+def test_attention_many_empty_blocks(where):
+    """Long padding: a CTA's share is one block with keys among many without."""
+    p = Problem("causal", 1, 4000, 40, 64)
+    lo, hi = p.lo.copy(), p.hi.copy()
+    if where == "front":
+        lo[:, 100:], hi[:, 100:] = 0, 0
+    elif where == "back":
+        lo[:, :3900], hi[:, :3900] = 0, 0
+    else:
+        lo[:, 100:3900], hi[:, 100:3900] = 0, 0
+    seen = lo[0] < hi[0]
+    lo[:, 3900:] = np.where(lo[:, 3900:] < hi[:, 3900:], 3900, 0)
+    p.klo.copy_(i32(lo))
+    p.khi.copy_(i32(hi))
+    assert L.mc_attention_mask_intervals(1, 4000, p.klo, p.khi, p.tab) == 0
+    o, lse = p.forward()
+    assert (o[0, ~seen] == 0).all() and (lse[0][:, ~seen] == -np.inf).all()
+    d = [p.backward(t) for t in (False, True)]
+    # the two ends are independent short sequences
+    for at, n in ((0, 100), (3900, 100)):
+        if not seen[at]:
+            continue
+        q = Problem("causal", 1, n, 40, 64)
+        q.qkv.copy_(p.qkv[:, at:at + n])
+        q.dout.copy_(p.dout[:, at:at + n])
+        o2, lse2 = q.forward()
+        assert np.abs(lse[0][:, at:at + n] - lse2[0]).max() < 1e-4
+        assert np.linalg.norm(o[0, at:at + n] - o2[0]) <= 2 * O.HALF_BF16 * np.linalg.norm(o2)
+        for t in (False, True):
+            d2 = q.backward(t)
+            assert np.linalg.norm(d[t][0, at:at + n] - d2[0]) <= \
+                2 * O.HALF_BF16 * np.linalg.norm(d2)
+            rest = d[t][0, ~seen]
+            assert (rest == 0).all()
+
+
 def test_attention_scores_far_beyond_the_cap():
     # scores of several hundred against a cap of 2: the cap's derivative is 0, nothing overflows
     Problem("documents", 1, 200, 2, 64, cap=2.0, qstd=300.0).check()
