@@ -29,18 +29,44 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // 2 c 2^-24, which is what counts in an exponent.
 struct ScoreConst {
   float mul;     // no cap: log2(e) / sqrt(d); cap: 2 log2(e) / (sqrt(d) c)
+  float arg;     // cap: 1 / (sqrt(d) c), the tanh's argument per raw score
   float cap2;    // c log2(e)
   float slope2;  // slope log2(e)
 };
+
+// For |t| <= kCapSmall, tanh(t) = t p(t^2) with the degree-5 polynomial p of
+// least largest error in tanh: 5.5e-8 (fitted on a Chebyshev grid by
+// reweighted least squares; 1.2e-7 with 32-bit arithmetic, as the quotient
+// form's).  It takes no special-function operations, whose rate (32 results
+// per clock and SM, three of them per score with the quotient form and the
+// exponential) would bound a capped softmax: 8 packed products and sums per
+// pair of scores here.  Scores mostly are that far below their cap; a warp
+// with one that is not takes the quotient form.
+constexpr float kCapSmall = 0.875f;
+
+__device__ __forceinline__ float2 cap_small_tanh(float2 t) {
+  constexpr float k0 = 0.9999991655349731f, k1 = -0.3333015441894531f, k2 = 0.13298341631889343f,
+                  k3 = -0.052287403494119644f, k4 = 0.017785653471946716f,
+                  k5 = -0.0036076814867556095f;
+  const float2 u = __fmul2_rn(t, t);
+  float2 p = __ffma2_rn(make_float2(k5, k5), u, make_float2(k4, k4));
+  p = __ffma2_rn(p, u, make_float2(k3, k3));
+  p = __ffma2_rn(p, u, make_float2(k2, k2));
+  p = __ffma2_rn(p, u, make_float2(k1, k1));
+  p = __ffma2_rn(p, u, make_float2(k0, k0));
+  return __fmul2_rn(t, p);
+}
 
 template <bool CAP, bool BIAS>
 __device__ __forceinline__ ScoreConst score_const(float rsqrt_d, float softcap, float slope) {
   ScoreConst c;
   c.mul = rsqrt_d * kOptLog2e;
+  c.arg = 0.f;
   c.cap2 = 0.f;
   c.slope2 = 0.f;
   if constexpr (CAP) {
-    c.mul = 2.f * rsqrt_d * kOptLog2e / softcap;
+    c.arg = rsqrt_d / softcap;
+    c.mul = 2.f * kOptLog2e * c.arg;
     c.cap2 = softcap * kOptLog2e;
   }
   if constexpr (BIAS) c.slope2 = slope * kOptLog2e;
@@ -68,29 +94,19 @@ __device__ __forceinline__ bool opt_entry(const int32_t* tables, bool head_major
   return ok;
 }
 
-// Items of a persistent kernel, (table entry, head) pairs: heads are taken in
-// groups of `group`, within a group the longest entries of all its heads come
-// first, and the grid's CTAs are dealt them in a snake, so that their shares
-// are even.  A group's K and V are what the CTAs running together read again
-// and again: the group is as large as fits in L2 beside everything else.
-inline int opt_head_group(int b, int s, int H, int d) {
-  const int64_t head_bytes = static_cast<int64_t>(b) * s * d * 4;  // K and V of one head
-  const int64_t fit = (64ll << 20) / head_bytes;
-  return static_cast<int>(fit < 1 ? 1 : fit < H ? fit : H);
-}
-
+// Items of a persistent kernel, (table entry, head) pairs: the longest entries
+// of all heads come first, and the grid's CTAs are dealt them in a snake, so
+// that their shares are even.  (Groups of 1 to 7 heads at a time, whose K and V
+// stay in L2, cost more by their uneven shares than they saved: 742 to 839 us
+// against 734 us over 16,384 tokens and 16 heads.)
 // Item r of this CTA: its table rank and head; false when its share is done.
 // (b ceil(s / 128) H < 2^31 by the entry points' limits.)
-__device__ __forceinline__ bool opt_item(int r, int n, int H, int group, int& rank, int& hh) {
+__device__ __forceinline__ bool opt_item(int r, int n, int H, int& rank, int& hh) {
   const unsigned G = gridDim.x, c = blockIdx.x;
   const unsigned k = static_cast<unsigned>(r) * G + ((r & 1) ? G - 1 - c : c);
   if (k >= static_cast<unsigned>(n) * static_cast<unsigned>(H)) return false;
-  const unsigned per_group = static_cast<unsigned>(n) * static_cast<unsigned>(group);
-  const unsigned g0 = k / per_group * static_cast<unsigned>(group);  // the group's first head
-  const unsigned heads = min(static_cast<unsigned>(group), static_cast<unsigned>(H) - g0);
-  const unsigned in = k - g0 * static_cast<unsigned>(n);
-  rank = static_cast<int>(in / heads);
-  hh = static_cast<int>(g0 + in % heads);
+  rank = static_cast<int>(k / static_cast<unsigned>(H));
+  hh = static_cast<int>(k % static_cast<unsigned>(H));
   return true;
 }
 

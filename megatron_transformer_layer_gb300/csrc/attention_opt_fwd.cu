@@ -73,7 +73,6 @@ struct OptFwdArgs {
   const float* slopes;
   float softcap;
   int b, s, H;
-  int head_group;
   int* status;
 };
 
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         bool more = true;
         auto read_entry = [&](int r) {
           int rank = 0;
-          more = opt_item(r, A.b * nb, A.H, A.head_group, rank, h_next);
+          more = opt_item(r, A.b * nb, A.H, rank, h_next);
           if (more) e_next = *reinterpret_cast<const int4*>(A.tables + 4ll * rank);
         };
         auto announce = [&](int r, OptItem& it) -> bool {
@@ -384,6 +383,49 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       }
     };
     fetch(0);
+    // The item before, whose O is still in TMEM: its products run during this
+    // item's first softmax, and it is stored once they are complete.
+    bool pending = false;
+    float p_l = 0.f, p_m = 0.f;
+    int p_q = 0, p_bi = 0, p_head = 0;
+    auto store_item = [&](bool from_tmem) {
+      // a row that sees nothing: O = 0, log-sum-exp = -infinity
+      const float inv = p_l == 0.f ? 0.f : 1.f / p_l;
+      const int q_warp = p_q - lane;  // the warp's first row
+      uint16_t* base = A.out + (static_cast<int64_t>(p_bi) * s + q_warp) * a + p_head * D +
+                       half * (D / 2);
+      const bool in_range = MC_DCHECK(q_warp >= 0 && p_bi >= 0 && p_bi < A.b && p_head * D + D <= a,
+                                      status, kSiteAttention);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {  // this thread's half of the row's O
+        float v[32] = {};
+        if (from_tmem) {
+          tmem_ld_32x32b_x32(tO + lane_off + half * (D / 2) + c * 32, v);
+          if (c == D / 64 - 1) {
+            tc_fence_before();
+            mbar_arrive(o_free);  // the next products may overwrite O
+          }
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = p_l == 0.f ? 0u : pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+        transpose_16b_x4(w, lane);
+        if (in_range) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r4 = (lane & ~3) + k;  // row of the warp: 4 lanes store its 64 bytes
+            if (q_warp + r4 < s)
+              *reinterpret_cast<uint4*>(base + static_cast<int64_t>(r4) * a + c * 32 +
+                                        (lane & 3) * 8) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        }
+      }
+      if (half == 0 && in_range && p_q < s)
+        A.lse[(static_cast<int64_t>(p_bi) * A.H + p_head) * s + p_q] =
+            p_l == 0.f ? -INFINITY : (p_m + log2f(p_l)) * kOptLn2;
+    };
     int g = 0;
     for (int r = 0; ok; ++r) {
       const OptItem& it = items[r % kOptRing];
@@ -410,35 +452,63 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         tc_fence_before();
         mbar_arrive(s_free);
         const int key0 = k_lo + j * kOptKeys + half * 128;
-        // ---- scores in log2 units (without cap and bias the scale is folded
-        //      into the exponent's argument below)
-        if constexpr (CAP || BIAS) {
-          const float base = sc.slope2 * static_cast<float>(key0 - q);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            float2 y = make_float2(x[2 * i], x[2 * i + 1]);
-            if constexpr (CAP)
-              y = __ffma2_rn(cap_r(y, sc.mul), make_float2(-2.f * sc.cap2, -2.f * sc.cap2),
-                             make_float2(sc.cap2, sc.cap2));
-            else
-              y = __fmul2_rn(y, make_float2(sc.mul, sc.mul));
-            if constexpr (BIAS) {
-              y.x -= fabsf(fmaf(sc.slope2, static_cast<float>(2 * i), base));
-              y.y -= fabsf(fmaf(sc.slope2, static_cast<float>(2 * i + 1), base));
-            }
-            x[2 * i] = y.x;
-            x[2 * i + 1] = y.y;
-          }
-        }
-        // ---- keys [first, end) of this half are visible
-        // (the last block may lack its second half, whose S is an older one)
+        // ---- keys [first, end) of this half are visible (the last block may lack
+        //      its second half, whose S is an older one)
         const int first = row_lo - key0;
         const int end = 2 * j + half < halves ? row_hi - key0 : 0;
-        if (__any_sync(0xffffffffu, end < 128)) {
+        const bool cut_end = __any_sync(0xffffffffu, end < 128);
+        const bool cut_first = __any_sync(0xffffffffu, first > 0);
+        // ---- scores in log2 units (without cap and bias the scale is folded
+        //      into the exponent's argument below)
+        if constexpr (CAP) {
+          // (what is masked must not decide how the cap is formed)
+          if (cut_end || cut_first) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i] = i >= first && i < end ? x[i] : 0.f;
+          }
+          float hi0 = x[0], hi1 = x[1], lo0 = x[0], lo1 = x[1];
+#pragma unroll
+          for (int i = 2; i < 126; i += 4) {
+            hi0 = fmax3f(hi0, x[i], x[i + 1]);
+            lo0 = fmin3f(lo0, x[i], x[i + 1]);
+            hi1 = fmax3f(hi1, x[i + 2], x[i + 3]);
+            lo1 = fmin3f(lo1, x[i + 2], x[i + 3]);
+          }
+          hi0 = fmaxf(fmax3f(hi0, x[126], x[127]), hi1);
+          lo0 = fminf(fmin3f(lo0, x[126], x[127]), lo1);
+          if (__all_sync(0xffffffffu, fmaxf(hi0, -lo0) * sc.arg <= kCapSmall)) {
+            const float2 arg2 = make_float2(sc.arg, sc.arg), cap2 = make_float2(sc.cap2, sc.cap2);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const float2 y = __fmul2_rn(
+                  cap_small_tanh(__fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), arg2)), cap2);
+              x[2 * i] = y.x;
+              x[2 * i + 1] = y.y;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const float2 y = __ffma2_rn(cap_r(make_float2(x[2 * i], x[2 * i + 1]), sc.mul),
+                                          make_float2(-2.f * sc.cap2, -2.f * sc.cap2),
+                                          make_float2(sc.cap2, sc.cap2));
+              x[2 * i] = y.x;
+              x[2 * i + 1] = y.y;
+            }
+          }
+        }
+        if constexpr (BIAS) {
+          const float base = sc.slope2 * static_cast<float>(key0 - q);
+#pragma unroll
+          for (int i = 0; i < 128; ++i) {
+            const float z = CAP ? x[i] : x[i] * sc.mul;
+            x[i] = z - fabsf(fmaf(sc.slope2, static_cast<float>(i), base));
+          }
+        }
+        if (cut_end) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) x[i] = i < end ? x[i] : -INFINITY;
         }
-        if (__any_sync(0xffffffffu, first > 0)) {
+        if (cut_first) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) x[i] = i >= first ? x[i] : -INFINITY;
         }
@@ -488,6 +558,10 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           break;
         }
         tc_fence_after();
+        if (pending) {
+          store_item(true);
+          pending = false;
+        }
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll 1
           for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
@@ -511,48 +585,34 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         mbar_arrive(p_full);
       }
       if (!ok) break;
-      const bool empty = halves == 0;
-      if (!empty) {
+      if (halves > 0) {
         l += exchange(l);  // both halves' sums, taken against the same maximum
-        if (ok) ok = mbar_wait(pv_done, (g - 1) & 1, status, kSiteAttention);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        tc_fence_after();
+        p_l = l;
+        p_m = m;
+        p_q = q;
+        p_bi = it.entry.x;
+        p_head = it.head;
+        pending = true;
+      } else {
+        // nothing to see: stored at once (what is pending waits in its TMEM)
+        const float l0 = p_l, m0 = p_m;
+        const int q0 = p_q, b0 = p_bi, h0 = p_head;
+        p_l = 0.f;
+        p_q = q;
+        p_bi = it.entry.x;
+        p_head = it.head;
+        store_item(false);
+        p_l = l0, p_m = m0, p_q = q0, p_bi = b0, p_head = h0;
       }
-      const int bi = it.entry.x, head = it.head;
-      // a row that sees nothing: O = 0, log-sum-exp = -infinity
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* orow = A.out + (static_cast<int64_t>(bi) * s + q) * a + head * D + half * (D / 2);
-      const bool store =
-          q < s && MC_DCHECK(q >= 0 && bi < A.b && head * D + D <= a, status, kSiteAttention);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {  // this thread's half of the row's O
-        float v[32] = {};
-        if (!empty) tmem_ld_32x32b_x32(tO + lane_off + half * (D / 2) + c * 32, v);
-        if (!empty && c == D / 64 - 1) {
-          tc_fence_before();
-          mbar_arrive(o_free);  // the next item's products may overwrite O
-        }
-        if (store) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 wv = make_uint4(0u, 0u, 0u, 0u);
-            if (l != 0.f) {
-              wv.x = pack_bf16x2(v[8 * i + 0] * inv, v[8 * i + 1] * inv);
-              wv.y = pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv);
-              wv.z = pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv);
-              wv.w = pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv);
-            }
-            reinterpret_cast<uint4*>(orow + c * 32)[i] = wv;
-          }
-        }
-      }
-      if (store && half == 0)
-        A.lse[(static_cast<int64_t>(bi) * A.H + head) * s + q] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * kOptLn2;
       mbar_arrive(&it_empty[r % kOptRing]);
+    }
+    if (ok && pending && mbar_wait_warp(pv_done, (g - 1) & 1, status, kSiteAttention)) {
+      tc_fence_after();
+      store_item(true);
     }
   }
 
@@ -609,7 +669,6 @@ int launch_attention_opt_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int b
   A.b = b;
   A.s = s;
   A.H = H;
-  A.head_group = opt_head_group(b, s, H, d);
   A.status = status;
   return d == 64 ? launch_fwd_d<64>(qkv, A, st) : launch_fwd_d<128>(qkv, A, st);
 }

@@ -567,6 +567,13 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   return d;
 }
 
+// min(a, b, c) likewise.
+__device__ __forceinline__ float fmin3f(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -589,6 +596,32 @@ __device__ __forceinline__ void attention_cta(bool head_major, int H, int& t, in
     hh = static_cast<int>(blockIdx.y);
     bi = static_cast<int>(blockIdx.z);
   }
+}
+
+// Every lane holds four 16-byte units of its row (w[4 u .. 4 u + 3]); four
+// neighbouring lanes exchange them, after which lane i of the four holds unit
+// i of the four rows (row k in w[4 k ..]): a store per row then covers 64
+// contiguous bytes instead of 16.
+__device__ __forceinline__ void transpose_16b_x4(uint32_t (&w)[16], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // units (2v, 2v + 1) with the lane beside
+      const uint32_t x = w[8 * v + e], y = w[8 * v + 4 + e];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, b0 ? x : y, 1);
+      w[8 * v + e] = b0 ? got : x;
+      w[8 * v + 4 + e] = b0 ? y : got;
+    }
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // unit pairs with the lanes two further
+      const uint32_t x = w[4 * v + e], y = w[8 + 4 * v + e];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2);
+      w[4 * v + e] = b1 ? got : x;
+      w[8 + 4 * v + e] = b1 ? y : got;
+    }
 }
 
 // 32 values of one row added to a running fp32 sum (the context-parallel
