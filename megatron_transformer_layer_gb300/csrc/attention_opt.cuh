@@ -14,6 +14,11 @@ struct BoolC {
   static constexpr bool value = B;
 };
 
+template <int N>
+struct IntC {
+  static constexpr int value = N;
+};
+
 // 1 / x (one ulp; 1 / infinity = 0), x >= 1 here.
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
@@ -34,27 +39,29 @@ struct ScoreConst {
   float slope2;  // slope log2(e)
 };
 
-// For |t| <= kCapSmall, tanh(t) = t p(t^2) with the degree-5 polynomial p of
-// least largest error in tanh: 5.5e-8 (fitted on a Chebyshev grid by
+// For |t| <= kCapSmall, tanh(t) = t p(t^2) with the degree-4 polynomial p of
+// least largest error in tanh: 5.0e-08 (fitted on a Chebyshev grid by
 // reweighted least squares; 1.2e-7 with 32-bit arithmetic, as the quotient
-// form's).  It takes no special-function operations, whose rate (32 results
-// per clock and SM, three of them per score with the quotient form and the
-// exponential) would bound a capped softmax: 8 packed products and sums per
-// pair of scores here.  Scores mostly are that far below their cap; a warp
-// with one that is not takes the quotient form.
-constexpr float kCapSmall = 0.875f;
+// form's).  It takes no special-function operations, of which the quotient
+// form needs two per score beside the exponential: those run at 32 results per
+// clock and SM.  Scores mostly are that far below their cap; a warp with one
+// that is not takes the quotient form.
+constexpr float kCapSmall = 0.65625f;
 
-__device__ __forceinline__ float2 cap_small_tanh(float2 t) {
-  constexpr float k0 = 0.9999991655349731f, k1 = -0.3333015441894531f, k2 = 0.13298341631889343f,
-                  k3 = -0.052287403494119644f, k4 = 0.017785653471946716f,
-                  k5 = -0.0036076814867556095f;
+// p(t^2), times `scale`: c = scale * coefficients.
+struct CapPoly {
+  float k0, k1, k2, k3, k4;
+};
+__device__ __forceinline__ CapPoly cap_poly(float scale) {
+  return {0.9999991655349731f * scale, -0.33329296112060547f * scale, 0.13278807699680328f * scale,
+          -0.05090659484267235f * scale, 0.013971595093607903f * scale};
+}
+__device__ __forceinline__ float2 cap_small(float2 t, const CapPoly& c) {
   const float2 u = __fmul2_rn(t, t);
-  float2 p = __ffma2_rn(make_float2(k5, k5), u, make_float2(k4, k4));
-  p = __ffma2_rn(p, u, make_float2(k3, k3));
-  p = __ffma2_rn(p, u, make_float2(k2, k2));
-  p = __ffma2_rn(p, u, make_float2(k1, k1));
-  p = __ffma2_rn(p, u, make_float2(k0, k0));
-  return __fmul2_rn(t, p);
+  float2 p = __ffma2_rn(make_float2(c.k4, c.k4), u, make_float2(c.k3, c.k3));
+  p = __ffma2_rn(p, u, make_float2(c.k2, c.k2));
+  p = __ffma2_rn(p, u, make_float2(c.k1, c.k1));
+  return __ffma2_rn(p, u, make_float2(c.k0, c.k0));
 }
 
 template <bool CAP, bool BIAS>

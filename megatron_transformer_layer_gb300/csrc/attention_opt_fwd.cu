@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       const int row_lo = lo, row_hi = q < s ? min(hi, s) : hi;
       const ScoreConst sc =
           score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
+      const CapPoly poly = cap_poly(sc.cap2);
       fetch(r + 1);
       if (!ok) break;
       float m = -INFINITY, l = 0.f;
@@ -458,46 +459,65 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         const int end = 2 * j + half < halves ? row_hi - key0 : 0;
         const bool cut_end = __any_sync(0xffffffffu, end < 128);
         const bool cut_first = __any_sync(0xffffffffu, first > 0);
-        // ---- scores in log2 units (without cap and bias the scale is folded
-        //      into the exponent's argument below)
+        const bool cut = cut_end || cut_first;
+        // With a bias the scores are formed here, in log2 units.  Without one
+        // they stay raw until the exponent: the scale is positive and the cap
+        // monotone, so the raw maximum gives the row's.
+        float low = INFINITY;  // a cap needs the lowest visible score too
         if constexpr (CAP) {
-          // (what is masked must not decide how the cap is formed)
-          if (cut_end || cut_first) {
+          float lo1 = INFINITY;
+          if (cut) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) x[i] = i >= first && i < end ? x[i] : 0.f;
-          }
-          float hi0 = x[0], hi1 = x[1], lo0 = x[0], lo1 = x[1];
-#pragma unroll
-          for (int i = 2; i < 126; i += 4) {
-            hi0 = fmax3f(hi0, x[i], x[i + 1]);
-            lo0 = fmin3f(lo0, x[i], x[i + 1]);
-            hi1 = fmax3f(hi1, x[i + 2], x[i + 3]);
-            lo1 = fmin3f(lo1, x[i + 2], x[i + 3]);
-          }
-          hi0 = fmaxf(fmax3f(hi0, x[126], x[127]), hi1);
-          lo0 = fminf(fmin3f(lo0, x[126], x[127]), lo1);
-          if (__all_sync(0xffffffffu, fmaxf(hi0, -lo0) * sc.arg <= kCapSmall)) {
-            const float2 arg2 = make_float2(sc.arg, sc.arg), cap2 = make_float2(sc.cap2, sc.cap2);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const float2 y = __fmul2_rn(
-                  cap_small_tanh(__fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), arg2)), cap2);
-              x[2 * i] = y.x;
-              x[2 * i + 1] = y.y;
+            for (int i = 0; i < 128; i += 2) {
+              low = fminf(low, i >= first && i < end ? x[i] : INFINITY);
+              lo1 = fminf(lo1, i + 1 >= first && i + 1 < end ? x[i + 1] : INFINITY);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const float2 y = __ffma2_rn(cap_r(make_float2(x[2 * i], x[2 * i + 1]), sc.mul),
-                                          make_float2(-2.f * sc.cap2, -2.f * sc.cap2),
-                                          make_float2(sc.cap2, sc.cap2));
-              x[2 * i] = y.x;
-              x[2 * i + 1] = y.y;
+            for (int i = 0; i < 128; i += 4) {
+              low = fmin3f(low, x[i], x[i + 1]);
+              lo1 = fmin3f(lo1, x[i + 2], x[i + 3]);
             }
           }
+          low = fminf(low, lo1);
         }
+        // The visible scores of the warp's rows are far enough below the cap
+        // (masked ones must not decide how the cap is formed).
+        auto below_cap = [&](float high) {
+          return __all_sync(0xffffffffu, fmaxf(high, -low) * sc.arg <= kCapSmall);
+        };
+        const float2 arg2 = make_float2(sc.arg, sc.arg);
+        const float2 m2cap2 = make_float2(-2.f * sc.cap2, -2.f * sc.cap2);
         if constexpr (BIAS) {
           const float base = sc.slope2 * static_cast<float>(key0 - q);
+          if constexpr (CAP) {
+            float high = -INFINITY;
+            if (cut) {
+#pragma unroll
+              for (int i = 0; i < 128; ++i)
+                high = fmaxf(high, i >= first && i < end ? x[i] : -INFINITY);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 128; i += 2) high = fmax3f(high, x[i], x[i + 1]);
+            }
+            if (below_cap(high)) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) {
+                const float2 t = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), arg2);
+                const float2 y = __fmul2_rn(t, cap_small(t, poly));
+                x[2 * i] = y.x;
+                x[2 * i + 1] = y.y;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) {
+                const float2 y = __ffma2_rn(cap_r(make_float2(x[2 * i], x[2 * i + 1]), sc.mul),
+                                            m2cap2, make_float2(sc.cap2, sc.cap2));
+                x[2 * i] = y.x;
+                x[2 * i + 1] = y.y;
+              }
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 128; ++i) {
             const float z = CAP ? x[i] : x[i] * sc.mul;
@@ -517,13 +537,19 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
 #pragma unroll
         for (int p = 0; p < 62; ++p) mc[p & 3] = fmax3f(mc[p & 3], x[4 + 2 * p], x[5 + 2 * p]);
         float mx = fmaxf(fmax3f(mc[0], mc[1], mc[2]), mc[3]);
+        const bool small = CAP && !BIAS && below_cap(mx);
         mx = fmaxf(mx, exchange(mx));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        const float mul = CAP || BIAS ? 1.f : sc.mul;
-        mx *= mul;  // > 0
+        if constexpr (!BIAS) {
+          if constexpr (CAP) {
+            if (mx > -INFINITY) mx = fmaf(cap_r(make_float2(mx, mx), sc.mul).x, m2cap2.x, sc.cap2);
+          } else {
+            mx *= sc.mul;
+          }
+        }
         const float m_new = fmaxf(m, mx);
         // a row that has seen nothing yet (m = -infinity) has l = 0 and O = 0
         const bool need = j > 0 && m_new > m + kOptRescale;
@@ -536,18 +562,54 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         }
         const float m_use = m == -INFINITY ? 0.f : m;
         // ---- P, its row sum in 32 bits, and P as bf16 in registers, while the
-        //      products of the block before may still run
-        //      (in place: pair i of the bf16 P takes score i's register, which
-        //      pair i / 2 was the last to need)
+        //      products of the block before may still run (in place: pair i of
+        //      the bf16 P takes score i's register, which pair i / 2 was the
+        //      last to need)
         float2 sm2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-        const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(-m_use, -m_use);
+        // kForm 0: y = x mul - m, 1: x is y, 2: capped by the polynomial, 3: by
+        // the quotient
+        auto exponentials = [&](auto form_c, auto cut_c) {
+          constexpr int kForm = decltype(form_c)::value;
+          constexpr bool CUT = decltype(cut_c)::value;
+          const float2 mul2 = make_float2(sc.mul, sc.mul), negm2 = make_float2(-m_use, -m_use);
+          const float2 off2 = make_float2(sc.cap2 - m_use, sc.cap2 - m_use);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
-          const float2 y = CAP || BIAS ? __fadd2_rn(xi, negm2) : __ffma2_rn(xi, mul2, negm2);
-          const float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-          sm2[i & 3] = __fadd2_rn(sm2[i & 3], pv);
-          x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));
+          for (int i = 0; i < 64; ++i) {
+            const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
+            float2 y;
+            if constexpr (kForm == 0) {
+              y = __ffma2_rn(xi, mul2, negm2);
+            } else if constexpr (kForm == 1) {
+              y = __fadd2_rn(xi, negm2);
+            } else {
+              if constexpr (kForm == 2) {
+                const float2 t = __fmul2_rn(xi, arg2);
+                y = __ffma2_rn(t, cap_small(t, poly), negm2);
+              } else {
+                y = __ffma2_rn(cap_r(xi, sc.mul), m2cap2, off2);
+              }
+            }
+            float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            if constexpr (CUT)  // (the cap of -infinity is not -infinity)
+              pv = make_float2(2 * i >= first && 2 * i < end ? pv.x : 0.f,
+                               2 * i + 1 >= first && 2 * i + 1 < end ? pv.y : 0.f);
+            sm2[i & 3] = __fadd2_rn(sm2[i & 3], pv);
+            x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));
+          }
+        };
+        if constexpr (BIAS) {
+          exponentials(IntC<1>{}, BoolC<false>{});
+        } else if constexpr (CAP) {
+          if (small) {
+            if (cut)
+              exponentials(IntC<2>{}, BoolC<true>{});
+            else
+              exponentials(IntC<2>{}, BoolC<false>{});
+          } else {
+            exponentials(IntC<3>{}, BoolC<true>{});
+          }
+        } else {
+          exponentials(IntC<0>{}, BoolC<false>{});
         }
         const float2 s01 = __fadd2_rn(__fadd2_rn(sm2[0], sm2[1]), __fadd2_rn(sm2[2], sm2[3]));
         l += s01.x + s01.y;
