@@ -179,63 +179,82 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
         mbar_wait(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention, 200000000ull, false);
     }
   } else if (warp == 1) {
-    if (lane == 0 && count > 0) {
-      // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
-      bool ok = mbar_wait(r_full, 0, status, kSiteAttention);
-      const uint32_t kbase = smem_u32(sK), vbase = smem_u32(sV);
-      for (int i = 0; ok && i <= count; ++i) {
-        const int st = i & 1;
-        if (i < count) {
-          if (!mbar_wait(&st_full[st], (i >> 1) & 1, status, kSiteAttention)) break;
-          // tS was read into registers for block i - 1.
-          if (i > 0 && !mbar_wait(s_free, (i - 1) & 1, status, kSiteAttention)) break;
-          tc_fence_after();
-          const uint32_t qb = smem_u32(sQ[st]);
+    // ---------------------------------------------------------- MMA issuer
+    // The whole warp walks the loop, so that addresses and descriptors stay in
+    // uniform registers; one lane issues.
+    constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+    const bool leader = elect_one();
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), 16, 1024);
+    // Q_i and dO_i, K-major (S, dP) and MN-major (dK, dV)
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ[0]), 16, 1024);
+    const uint64_t do_desc = smem_desc_sw128(smem_u32(sdO[0]), 16, 1024);
+    const uint64_t qt_desc = smem_desc_sw128(smem_u32(sQ[0]), 16384, 1024);
+    const uint64_t dot_desc = smem_desc_sw128(smem_u32(sdO[0]), 16384, 1024);
+    bool ok = count > 0 && mbar_wait_warp(r_full, 0, status, kSiteAttention);
+    for (int i = 0; ok && i <= count; ++i) {
+      const uint32_t st = (i & 1) * C::kTile;
+      if (i < count) {
+        if (!mbar_wait_warp(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention)) break;
+        // tS was read into registers for block i - 1.
+        if (i > 0 && !mbar_wait_warp(s_free, (i - 1) & 1, status, kSiteAttention)) break;
+        tc_fence_after();
+        const uint64_t qd = smem_desc_add(q_desc, st);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tS, smem_desc_sw128(kbase + off, 16, 1024), smem_desc_sw128(qb + off, 16, 1024),
-                      kIdescSq, kk > 0 ? 1u : 0u);
+            umma_bf16(tS, smem_desc_add(k_desc, off), smem_desc_add(qd, off), kIdescSq,
+                      kk > 0 ? 1u : 0u);
           }
           umma_commit(s_full);
         }
-        if (i > 0) {
-          const int pi = i - 1, pst = pi & 1;
-          if (!mbar_wait(p_full, pi & 1, status, kSiteAttention)) break;
-          tc_fence_after();
-          const uint32_t qb = smem_u32(sQ[pst]), dob = smem_u32(sdO[pst]);
+        __syncwarp();
+      }
+      if (i > 0) {
+        const int pi = i - 1;
+        const uint32_t pst = (pi & 1) * C::kTile;
+        if (!mbar_wait_warp(p_full, pi & 1, status, kSiteAttention)) break;
+        tc_fence_after();
+        const uint64_t qd = smem_desc_add(qt_desc, pst), dod = smem_desc_add(dot_desc, pst);
+        const uint32_t acc0 = pi > 0 ? 1u : 0u;
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 128 / 16; ++kk) {
-            // 16 queries = group kk: P at 16 kk, dz at 16 kk + 8; B tiles viewed MN-major
+            // 16 queries = group kk: P at 16 kk, dz at 16 kk + 8
             const uint32_t pcol = static_cast<uint32_t>(kk * 16);
-            const uint32_t acc = (pi > 0 || kk > 0) ? 1u : 0u;
-            umma_bf16_ts(tdV, tdP + pcol, smem_desc_sw128(dob + kk * 2048, 16384, 1024), kIdescAcc,
-                         acc);
-            umma_bf16_ts(tdK, tdP + pcol + 8, smem_desc_sw128(qb + kk * 2048, 16384, 1024),
-                         kIdescAcc, acc);
+            const uint32_t acc = kk > 0 ? 1u : acc0;
+            umma_bf16_ts(tdV, tdP + pcol, smem_desc_add(dod, kk * 2048), kIdescAcc, acc);
+            umma_bf16_ts(tdK, tdP + pcol + 8, smem_desc_add(qd, kk * 2048), kIdescAcc, acc);
           }
-          umma_commit(&st_empty[pst]);
+          umma_commit(&st_empty[pi & 1]);
           umma_commit(acc_done);
         }
-        if (i < count) {
-          // dP^T_i overwrites the P^T / dz^T that the products above read.
-          if (i > 0 && !mbar_wait(acc_done, (i - 1) & 1, status, kSiteAttention)) break;
-          tc_fence_after();
-          const uint32_t dob = smem_u32(sdO[st]);
+        __syncwarp();
+      }
+      if (i < count) {
+        // dP^T_i overwrites the P^T / dz^T that the products above read.
+        if (i > 0 && !mbar_wait_warp(acc_done, (i - 1) & 1, status, kSiteAttention)) break;
+        tc_fence_after();
+        const uint64_t dod = smem_desc_add(do_desc, st);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tdP, smem_desc_sw128(vbase + off, 16, 1024),
-                      smem_desc_sw128(dob + off, 16, 1024), kIdescSq, kk > 0 ? 1u : 0u);
+            umma_bf16(tdP, smem_desc_add(v_desc, off), smem_desc_add(dod, off), kIdescSq,
+                      kk > 0 ? 1u : 0u);
           }
           umma_commit(dp_full);
         }
+        __syncwarp();
       }
+    }
+    if (leader) {
       umma_commit(drain);
       mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------- compute
     // Two warps per TMEM lane quarter; `half` picks 64 of the 128 query columns.
@@ -593,48 +612,63 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
         mbar_wait(&v_full[j & 1], (j >> 1) & 1, status, kSiteAttention, 200000000ull, false);
     }
   } else if (warp == 1) {
-    if (lane == 0 && count > 0) {
-      // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
-      constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
-      bool ok = mbar_wait(r_full, 0, status, kSiteAttention);
-      const uint32_t qb = smem_u32(sQ), dob = smem_u32(sdO);
-      for (int j = 0; ok && j <= count; ++j) {
-        if (j < count) {
-          const int ks = j % 3, vs = j & 1;
-          if (!mbar_wait(&k_full[ks], (j / 3) & 1, status, kSiteAttention)) break;
-          if (!mbar_wait(&v_full[vs], (j >> 1) & 1, status, kSiteAttention)) break;
-          // S / dP of block j - 1 are in the compute warps' registers.
-          if (j > 0 && !mbar_wait(s_free, (j - 1) & 1, status, kSiteAttention)) break;
-          tc_fence_after();
-          const uint32_t kb = smem_u32(sK[ks]), vb = smem_u32(sV[vs]);
+    // ---------------------------------------------------------- MMA issuer
+    // (converged, as in the dK/dV kernel)
+    constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+    const bool leader = elect_one();
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t do_desc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(sK[0]), 16, 1024);
+    const uint64_t kt_desc = smem_desc_sw128(smem_u32(sK[0]), 16384, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(sV[0]), 16, 1024);
+    bool ok = count > 0 && mbar_wait_warp(r_full, 0, status, kSiteAttention);
+    for (int j = 0; ok && j <= count; ++j) {
+      if (j < count) {
+        const int ks = j % 3, vs = j & 1;
+        if (!mbar_wait_warp(&k_full[ks], (j / 3) & 1, status, kSiteAttention)) break;
+        if (!mbar_wait_warp(&v_full[vs], (j >> 1) & 1, status, kSiteAttention)) break;
+        // S / dP of block j - 1 are in the compute warps' registers.
+        if (j > 0 && !mbar_wait_warp(s_free, (j - 1) & 1, status, kSiteAttention)) break;
+        tc_fence_after();
+        const uint64_t kd = smem_desc_add(k_desc, ks * C::kTile);
+        const uint64_t vd = smem_desc_add(v_desc, vs * C::kTile);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tS, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024),
-                      kIdescSq, kk > 0 ? 1u : 0u);
-            umma_bf16(tdP, smem_desc_sw128(dob + off, 16, 1024),
-                      smem_desc_sw128(vb + off, 16, 1024), kIdescSq, kk > 0 ? 1u : 0u);
+            umma_bf16(tS, smem_desc_add(q_desc, off), smem_desc_add(kd, off), kIdescSq,
+                      kk > 0 ? 1u : 0u);
+            umma_bf16(tdP, smem_desc_add(do_desc, off), smem_desc_add(vd, off), kIdescSq,
+                      kk > 0 ? 1u : 0u);
           }
           umma_commit(s_full);
           umma_commit(&v_empty[vs]);  // V_j is done once dP_j is
         }
-        if (j > 0) {
-          const int pj = j - 1, pks = pj % 3;
-          if (!mbar_wait(ds_full, pj & 1, status, kSiteAttention)) break;
-          tc_fence_after();
-          const uint32_t kb = smem_u32(sK[pks]);
+        __syncwarp();
+      }
+      if (j > 0) {
+        const int pj = j - 1, pks = pj % 3;
+        if (!mbar_wait_warp(ds_full, pj & 1, status, kSiteAttention)) break;
+        tc_fence_after();
+        const uint64_t kd = smem_desc_add(kt_desc, pks * C::kTile);
+        const uint32_t acc0 = pj > 0 ? 1u : 0u;
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 128 / 16; ++kk)
-            umma_bf16_ts(tdQ, tdS + kk * 8, smem_desc_sw128(kb + kk * 2048, 16384, 1024), kIdescAcc,
-                         (pj > 0 || kk > 0) ? 1u : 0u);
+            umma_bf16_ts(tdQ, tdS + kk * 8, smem_desc_add(kd, kk * 2048), kIdescAcc,
+                         kk > 0 ? 1u : acc0);
           umma_commit(&k_empty[pks]);
           umma_commit(ds_free);
         }
+        __syncwarp();
       }
+    }
+    if (leader) {
       umma_commit(drain);
       mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------- compute
     const int quarter = warp & 3;
@@ -859,41 +893,48 @@ __global__ void __launch_bounds__(192, 1)
                   200000000ull, false);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, true, true);
-      bool ok = true;
-      int gt = 0;
-      for (int r = 0; ok && opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
-        const int acc = r & 1;
-        // the epilogue of item r - 2 has read this accumulator
-        if (!mbar_wait(&acc_empty[acc], ((r >> 1) & 1) ^ 1u, status, kSiteAttention)) break;
+    // ---------------------------------------------------------- MMA issuer
+    // (converged, as in the dK/dV kernel)
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, true, true);
+    const bool leader = elect_one();
+    // both operands MN-major: 16 keys per step are 16 rows of 128 B; 64-wide
+    // query (A) or d (B) chunks 16 KB apart
+    const uint64_t a_desc = smem_desc_sw128(smem_u32(smem), 16384, 1024);
+    bool ok = true;
+    int gt = 0;
+    for (int r = 0; ok && opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
+      const int acc = r & 1;
+      // the epilogue of item r - 2 has read this accumulator
+      if (!mbar_wait_warp(&acc_empty[acc], ((r >> 1) & 1) ^ 1u, status, kSiteAttention)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * 128);
+      for (int j = 0; j < nj; ++j, ++gt) {
+        const int st = gt % C::kStages;
+        if (!mbar_wait_warp(&full[st], (gt / C::kStages) & 1, status, kSiteAttention)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * 128);
-        for (int j = 0; j < nj; ++j, ++gt) {
-          const int st = gt % C::kStages;
-          if (!mbar_wait(&full[st], (gt / C::kStages) & 1, status, kSiteAttention)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t ab = smem_u32(smem + st * C::kStage);
-          const uint32_t kbase = ab + static_cast<uint32_t>(kOptTileBytes);
+        const uint64_t ad = smem_desc_add(a_desc, st * C::kStage);
+        const uint64_t kd = smem_desc_add(ad, static_cast<uint32_t>(kOptTileBytes));
+        const uint32_t acc0 = j > 0 ? 1u : 0u;
+        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            // 16 keys per step: 16 rows of 128 B in both MN-major operands;
-            // 64-wide query (A) or d (B) chunks 16 KB apart
-            umma_bf16(d_tmem, smem_desc_sw128(ab + kk * 2048, 16384, 1024),
-                      smem_desc_sw128(kbase + kk * 2048, 16384, 1024), kIdesc,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(d_tmem, smem_desc_add(ad, kk * 2048), smem_desc_add(kd, kk * 2048), kIdesc,
+                      kk > 0 ? 1u : acc0);
           umma_commit(&empty[st]);
         }
-        if (ok) umma_commit(&acc_full[acc]);
+        __syncwarp();
       }
+      if (ok && leader) umma_commit(&acc_full[acc]);
+      __syncwarp();
+    }
+    if (leader) {
       umma_commit(drain);
       mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3;
