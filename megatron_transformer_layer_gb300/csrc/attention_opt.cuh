@@ -39,27 +39,26 @@ struct ScoreConst {
   float slope2;  // slope log2(e)
 };
 
-// For |t| <= kCapSmall, tanh(t) = t p(t^2) with the degree-4 polynomial p of
-// least largest error in tanh: 5.0e-08 (fitted on a Chebyshev grid by
-// reweighted least squares; 1.2e-7 with 32-bit arithmetic, as the quotient
-// form's).  It takes no special-function operations, of which the quotient
-// form needs two per score beside the exponential: those run at 32 results per
-// clock and SM.  Scores mostly are that far below their cap; a warp with one
-// that is not takes the quotient form.
-constexpr float kCapSmall = 0.65625f;
+// For |t| <= kCapSmall, tanh(t) = t p(t^2) with the cubic p of least largest
+// error in tanh: 7.4e-08 (fitted on a Chebyshev grid by reweighted least squares;
+// 1.2e-7 with 32-bit arithmetic, as the quotient form's).  It takes no
+// special-function operations, of which the quotient form needs two per score
+// beside the exponential (an exponential 4 clocks per warp and quarter SM, a
+// reciprocal 8, a packed multiply-add of two scores 2).  Scores mostly are
+// that far below their cap; a warp with one that is not takes the quotient form.
+constexpr float kCapSmall = 0.46875f;
 
-// p(t^2), times `scale`: c = scale * coefficients.
+// p(t^2), times `scale`.
 struct CapPoly {
-  float k0, k1, k2, k3, k4;
+  float k0, k1, k2, k3;
 };
 __device__ __forceinline__ CapPoly cap_poly(float scale) {
-  return {0.9999991655349731f * scale, -0.33329296112060547f * scale, 0.13278807699680328f * scale,
-          -0.05090659484267235f * scale, 0.013971595093607903f * scale};
+  return {0.9999985694885254f * scale, -0.3332448899745941f * scale, 0.13184478878974915f * scale,
+          -0.04449363797903061f * scale};
 }
 __device__ __forceinline__ float2 cap_small(float2 t, const CapPoly& c) {
   const float2 u = __fmul2_rn(t, t);
-  float2 p = __ffma2_rn(make_float2(c.k4, c.k4), u, make_float2(c.k3, c.k3));
-  p = __ffma2_rn(p, u, make_float2(c.k2, c.k2));
+  float2 p = __ffma2_rn(make_float2(c.k3, c.k3), u, make_float2(c.k2, c.k2));
   p = __ffma2_rn(p, u, make_float2(c.k1, c.k1));
   return __ffma2_rn(p, u, make_float2(c.k0, c.k0));
 }
@@ -101,21 +100,89 @@ __device__ __forceinline__ bool opt_entry(const int32_t* tables, bool head_major
   return ok;
 }
 
-// Items of a persistent kernel, (table entry, head) pairs: the longest entries
-// of all heads come first, and the grid's CTAs are dealt them in a snake, so
-// that their shares are even.  (Groups of 1 to 7 heads at a time, whose K and V
-// stay in L2, cost more by their uneven shares than they saved: 742 to 839 us
-// against 734 us over 16,384 tokens and 16 heads.)
-// Item r of this CTA: its table rank and head; false when its share is done.
-// (b ceil(s / 128) H < 2^31 by the entry points' limits.)
-__device__ __forceinline__ bool opt_item(int r, int n, int H, int& rank, int& hh) {
-  const unsigned G = gridDim.x, c = blockIdx.x;
-  const unsigned k = static_cast<unsigned>(r) * G + ((r & 1) ? G - 1 - c : c);
-  if (k >= static_cast<unsigned>(n) * static_cast<unsigned>(H)) return false;
-  rank = static_cast<int>(k / static_cast<unsigned>(H));
-  hh = static_cast<int>(k % static_cast<unsigned>(H));
-  return true;
+// Items of a persistent kernel: (table entry, head) pairs.  Up to four waves of
+// them are dealt to one CTA per SM in a snake, the longest entries of all heads
+// first.  More are one CTA each, of which as many start as fit and steal the
+// others' indices as they finish (clc_request: a request takes one to two
+// microseconds, which a short grid shows: 29 us against 23 us for a backward of
+// 192 items).  Those take heads in groups whose K and V (or Q and dO), read
+// again and again by the CTAs running together, stay in L2, each group's
+// longest entries first: 64 MB against 32 or 96 MB at a time took 722, 751 and
+// 743 us for a causal forward over 16,384 tokens and 16 heads.
+struct OptGrid {
+  int ctas;
+  int steal;
+  int head_group;
+};
+inline OptGrid opt_grid(int b, int s, int H, int d) {
+  const int64_t items = static_cast<int64_t>(b) * ((s + 127) / 128) * H;
+  if (items <= 4ll * num_sms())
+    return {static_cast<int>(items < num_sms() ? items : num_sms()), 0, H};
+  const int64_t head_bytes = static_cast<int64_t>(b) * s * d * 4;
+  const int64_t fit = (64ll << 20) / head_bytes;
+  // equal groups: a small last one would leave its long items for the end
+  const int groups = fit < 1 ? H : fit < H ? static_cast<int>(H / fit) : 1;
+  return {static_cast<int>(items), 1, (H + groups - 1) / groups};
 }
+
+// Item k of the grid: its table rank and head.
+// (n = b ceil(s / 128) entries; n H < 2^31 by the entry points' limits.)
+__device__ __forceinline__ void opt_item(int k, int n, int H, int group, int& rank, int& hh) {
+  const unsigned per_group = static_cast<unsigned>(n) * static_cast<unsigned>(group);
+  const unsigned g0 = static_cast<unsigned>(k) / per_group * static_cast<unsigned>(group);
+  const unsigned heads = min(static_cast<unsigned>(group), static_cast<unsigned>(H) - g0);
+  const unsigned in = static_cast<unsigned>(k) - g0 * static_cast<unsigned>(n);
+  rank = static_cast<int>(in / heads);
+  hh = static_cast<int>(g0 + in % heads);
+}
+
+// This CTA's items, for one thread: its own, then its share of the snake, or
+// stolen ones, each requested one ahead.  `response` is 16 aligned bytes of
+// shared memory, `bar` an mbarrier of one arrival.
+struct OptItems {
+  void* response;
+  uint64_t* bar;
+  int total;    // items of the grid
+  int steal;
+  int k;        // the item at hand
+  int n;        // items taken before it
+  bool more;    // `k` is valid
+  bool asked;   // a request is under way
+  __device__ __forceinline__ OptItems(void* r, uint64_t* b, int items, int steal_)
+      : response(r), bar(b), total(items), steal(steal_), k(static_cast<int>(blockIdx.x)), n(0),
+        more(true), asked(false) {
+    ask();
+  }
+  __device__ __forceinline__ void ask() {
+    if (!steal) return;
+    clc_request(response, bar);
+    asked = true;
+  }
+  // The next item into k; asks for the one after it.  False on a timeout.
+  __device__ __forceinline__ bool next(int* status) {
+    if (!steal) {
+      ++n;
+      const unsigned G = gridDim.x, c = blockIdx.x;
+      const unsigned at = static_cast<unsigned>(n) * G + ((n & 1) ? G - 1 - c : c);
+      more = at < static_cast<unsigned>(total);
+      k = static_cast<int>(at);
+      return true;
+    }
+    if (!mbar_wait(bar, n & 1, status, kSiteAttention)) return false;
+    asked = false;
+    ++n;
+    more = clc_response(response, k);
+    if (more) {
+      fence_proxy_async_smem();  // the response has been read before it is overwritten
+      ask();
+    }
+    return true;
+  }
+  // A response still under way must land before the CTA exits.
+  __device__ __forceinline__ void finish(int* status) {
+    if (asked) mbar_wait(bar, n & 1, status, kSiteAttention, 200000000ull, false);
+  }
+};
 
 // A table entry that is not one of this shape is reported and taken as an
 // empty one of block 0.

@@ -21,7 +21,7 @@
 namespace mc {
 namespace {
 
-constexpr int kOptBwdThreads = 320;  // producer, MMA, 8 compute warps
+constexpr int kOptBwdThreads = 320;  // the dQ kernel: producer, MMA, 8 compute warps
 constexpr int64_t kOptTileBytes = 128 * 128 * 2;  // one bf16 dz^T tile (128 keys x 128 queries)
 
 struct OptBwdArgs {
@@ -35,7 +35,9 @@ struct OptBwdArgs {
   uint8_t* ds_tiles;
   float softcap;
   int b, s, H;
-  int head_major;
+  int head_major;         // the dQ kernel without tiles
+  int steal, head_group;  // the persistent kernels
+  int ctas;
   int causal;  // the tiles are of the lower triangle only
   int* status;
 };
@@ -48,22 +50,38 @@ __device__ __forceinline__ int64_t opt_tile(int causal, int nb, int64_t hb, int 
 }
 
 // ---------------------------------------------------------------- dK, dV
+// What every role needs to know of an item: a (key block, head) pair.
+struct alignas(16) OptKvItem {
+  int4 entry;  // sequence, key block, first query block, query blocks (-1: no more items)
+  int head;
+  int pad[3];
+};
+constexpr int kOptKvRing = 4;
+
 template <int D>
 struct OptBwdCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = 128 * D * 2;
   // K, V, two (Q_i, dO_i) stages, the dz^T tile staged for its bulk store,
   // lse / delta [2][128], the queries' key ranges relative to the block
-  // [2][128] (two bytes each), their edge flags [2][4], barriers.  The
+  // [2][128] (two bytes each), their edge flags [2][4], items, barriers.  The
   // dynamic shared memory starts 1024-byte aligned (checked at run time).
   static constexpr int kUsed = 6 * kTile + static_cast<int>(kOptTileBytes) + 4 * 128 * 4 +
-                               2 * 128 * 2 + 2 * 4 * 4 + 24 * 8;
+                               2 * 128 * 2 + 2 * 4 * 4 +
+                               kOptKvRing * static_cast<int>(sizeof(OptKvItem)) + 30 * 8;
   // one CTA per SM: it takes all 512 TMEM columns
   static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kUsed <= 227 * 1024, "dkdv kernel shared memory");
 };
 
+constexpr int kOptKvThreads = 384;
+// As in the forward: 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kOptKvRegsIo = 72, kOptKvRegsCompute = 216;
+
+// Persistent: one CTA per SM walks the (key block, head) items, each against
+// the query blocks that see it (blocks i, counted across items).  384 threads:
+// warp 0 loads, warp 1 issues, warps 4..11 compute.
 // TMEM: S^T [0, 128), dP^T [128, 256), dV [256, 256 + D), dK [384, 384 + D).
 // Per query block i:
 //   MMA      S^T_i = K Q_i^T (as soon as the compute warps hold S^T_{i-1} in
@@ -72,10 +90,12 @@ struct OptBwdCfg {
 //   compute  P^T (and the cap's derivative) from S^T_i while the products
 //            above run, then dz^T from dP^T_i.
 // A compute thread owns one key row and 64 query columns: the 16 queries of
-// group g (dP^T columns [16g, 16g + 16)) leave P at columns [16g, 16g + 8)
-// and dz at [16g + 8, 16g + 16), over columns that the thread itself has read.
+// group g (dP^T columns [16g, 16g + 16)) leave P at columns [16g, 16g + 8) and
+// dz at [16g + 8, 16g + 16), over columns that the thread itself has read.
+// An item's dV and dK are stored during the next item's first block: its
+// S^T and weights run meanwhile, as do the loads of its K and V.
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kOptBwdThreads, 1)
+__global__ void __launch_bounds__(kOptKvThreads, 1)
     attn_opt_dkdv_kernel(const __grid_constant__ CUtensorMap tm_qkv,
                          const __grid_constant__ CUtensorMap tm_do,
                          const __grid_constant__ OptBwdArgs A) {
@@ -88,46 +108,62 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
   }
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::kTile;
-  uint8_t* sQ[2] = {smem + 2 * C::kTile, smem + 3 * C::kTile};
-  uint8_t* sdO[2] = {smem + 4 * C::kTile, smem + 5 * C::kTile};
+  uint8_t* sQ = smem + 2 * C::kTile;   // [2]
+  uint8_t* sdO = smem + 4 * C::kTile;  // [2]
   uint8_t* sDs = smem + 6 * C::kTile;  // dz^T tile image (swizzled), 32 KB
   float* sL = reinterpret_cast<float*>(sDs + kOptTileBytes);  // [2][128] lse * log2(e)
   float* sD = sL + 256;                                        // [2][128] delta
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + 256);
-  uint64_t* r_full = bars + 0;
-  uint64_t* st_full = bars + 1;    // [2]
-  uint64_t* st_empty = bars + 3;   // [2]
-  uint64_t* s_full = bars + 5;     // S^T_i in TMEM
-  uint64_t* s_free = bars + 6;     // compute warps hold S^T_i in registers
-  uint64_t* dp_full = bars + 7;    // dP^T_i in TMEM
-  uint64_t* p_full = bars + 8;     // P^T_i, dz^T_i in TMEM
-  uint64_t* acc_done = bars + 9;   // dV, dK products of block i complete
-  uint64_t* drain = bars + 10;
-  uint64_t* lse_ready = bars + 11;  // [2]
-  uint64_t* ds_full = bars + 13;    // the dz^T tile of block i is in sDs (256 threads)
-  uint64_t* ds_free = bars + 14;    // its bulk store has read sDs
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
-  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 24);  // [2][128] first | end << 8
+  OptKvItem* items = reinterpret_cast<OptKvItem*>(sD + 256);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(items + kOptKvRing);
+  uint64_t* k_full = bars + 0;
+  uint64_t* k_empty = bars + 1;    // the item's last S^T
+  uint64_t* v_full = bars + 2;
+  uint64_t* v_empty = bars + 3;    // the item's last dP^T
+  uint64_t* st_full = bars + 4;    // [2]
+  uint64_t* st_empty = bars + 6;   // [2]
+  uint64_t* s_full = bars + 8;     // S^T_i in TMEM
+  uint64_t* s_free = bars + 9;     // compute warps hold S^T_i in registers
+  uint64_t* dp_full = bars + 10;   // dP^T_i in TMEM
+  uint64_t* p_full = bars + 11;    // P^T_i, dz^T_i in TMEM
+  uint64_t* acc_done = bars + 12;  // dV, dK products of block i complete
+  uint64_t* drain = bars + 13;
+  uint64_t* lse_ready = bars + 14;  // [2]
+  uint64_t* ds_full = bars + 16;    // the dz^T tile of block i is in sDs (8 warps)
+  uint64_t* ds_free = bars + 17;    // its bulk store has read sDs
+  uint64_t* it_full = bars + 18;    // [kOptKvRing]
+  uint64_t* it_empty = bars + 22;   // [kOptKvRing] read by the MMA warp and the compute warps (9)
+  uint64_t* steal_bar = bars + 26;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
+  void* response = bars + 28;  // 16 bytes, aligned as the items are
+  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 30);  // [2][128] first | end << 8
   int* sF = reinterpret_cast<int*>(sM + 256);             // [2][4] the 32 queries see the whole block
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = A.s, H = A.H, a = A.H * D;
   const int nb = (s + 127) / 128;
   if (threadIdx.x == 0) {
-    mbar_init(r_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&st_full[i], 1);
       mbar_init(&st_empty[i], 1);
-      mbar_init(&lse_ready[i], 256);
+      mbar_init(&lse_ready[i], 8);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 256);
+    mbar_init(s_free, 8);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 256);
+    mbar_init(p_full, 8);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
-    mbar_init(ds_full, 256);
+    mbar_init(ds_full, 8);
     mbar_init(ds_free, 1);
+    mbar_init(steal_bar, 1);
+    for (int i = 0; i < kOptKvRing; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 9);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tm_qkv);
     tma_prefetch_desc(&tm_do);
@@ -143,82 +179,124 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
   pdl_wait();  // the previous kernel on the stream has completed
   const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 384;
 
-  int4 entry;  // sequence, key block, first and end of the query blocks that see it
-  int hh;
-  const bool ok_entry = opt_entry(A.tables + 4ll * A.b * nb, A.head_major != 0, A.b, nb, entry, hh,
-                                  status);
-  const int bi = entry.x, kb = entry.y;
-  const int r0 = kb * 128;
-  const int qb0 = max(entry.z, 0);
-  const int count = ok_entry ? max(min(entry.w, nb) - qb0, 0) : 0;
-
-  if (warp == 0) {
-    if (lane == 0 && count > 0) {
-      // -------------------------------------------------------- producer
-      const int cq = hh * D, ck = a + hh * D, cv = 2 * a + hh * D;
-      mbar_arrive_expect_tx(r_full, 2 * C::kTile);
-      for (int c = 0; c < C::kChunks; ++c) {
-        tma_load_3d(sK + c * 16384, &tm_qkv, r_full, ck + c * 64, r0, bi);
-        tma_load_3d(sV + c * 16384, &tm_qkv, r_full, cv + c * 64, r0, bi);
-      }
-      int issued = 0;
-      for (int i = 0; i < count; ++i) {
-        const int st = i & 1;
-        const int row = (qb0 + i) * 128;
-        if (!mbar_wait(&st_empty[st], ((i >> 1) & 1) ^ 1u, status, kSiteAttention)) break;
-        mbar_arrive_expect_tx(&st_full[st], 2 * C::kTile);
-        for (int c = 0; c < C::kChunks; ++c) {
-          tma_load_3d(sQ[st] + c * 16384, &tm_qkv, &st_full[st], cq + c * 64, row, bi);
-          tma_load_3d(sdO[st] + c * 16384, &tm_do, &st_full[st], hh * D + c * 64, row, bi);
-        }
-        ++issued;
-      }
-      pdl_launch();  // every load of this CTA is issued
-      mbar_wait(r_full, 0, status, kSiteAttention, 200000000ull, false);
-      for (int i = issued - 1; i >= 0 && i >= issued - 2; --i)
-        mbar_wait(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention, 200000000ull, false);
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    // The whole warp walks the loop, so that addresses and descriptors stay in
-    // uniform registers; one lane issues.
-    constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
-    const bool leader = elect_one();
-    const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), 16, 1024);
-    // Q_i and dO_i, K-major (S, dP) and MN-major (dK, dV)
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ[0]), 16, 1024);
-    const uint64_t do_desc = smem_desc_sw128(smem_u32(sdO[0]), 16, 1024);
-    const uint64_t qt_desc = smem_desc_sw128(smem_u32(sQ[0]), 16384, 1024);
-    const uint64_t dot_desc = smem_desc_sw128(smem_u32(sdO[0]), 16384, 1024);
-    bool ok = count > 0 && mbar_wait_warp(r_full, 0, status, kSiteAttention);
-    for (int i = 0; ok && i <= count; ++i) {
-      const uint32_t st = (i & 1) * C::kTile;
-      if (i < count) {
-        if (!mbar_wait_warp(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention)) break;
-        // tS was read into registers for block i - 1.
-        if (i > 0 && !mbar_wait_warp(s_free, (i - 1) & 1, status, kSiteAttention)) break;
-        tc_fence_after();
-        const uint64_t qd = smem_desc_add(q_desc, st);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tS, smem_desc_add(k_desc, off), smem_desc_add(qd, off), kIdescSq,
-                      kk > 0 ? 1u : 0u);
+  if (warp < 4) {
+    setmaxnreg_dec<kOptKvRegsIo>();
+    if (warp == 0) {
+      if (lane == 0) {
+        // -------------------------------------------------------- producer
+        int g = 0, n = 0;  // query blocks and items (with blocks) loaded
+        bool ok = true, v_loaded = true;
+        int4 e_next = make_int4(0, 0, 0, 0);
+        int h_next = 0;
+        OptItems steal(response, steal_bar, A.b * nb * H, A.steal);
+        const int32_t* table = A.tables + 4ll * A.b * nb;  // the key entries
+        auto read_entry = [&]() {
+          int rank = 0;
+          if (steal.more) {
+            opt_item(steal.k, A.b * nb, H, A.head_group, rank, h_next);
+            e_next = *reinterpret_cast<const int4*>(table + 4ll * rank);
           }
-          umma_commit(s_full);
+        };
+        auto announce = [&](int r, OptKvItem& it) -> bool {
+          it.entry = make_int4(0, 0, 0, -1);
+          it.head = h_next;
+          if (steal.more) {
+            const int4 e = opt_checked(e_next, A.b, nb, status);
+            const int first = max(e.z, 0);
+            it.entry = make_int4(e.x, e.y, first, max(min(e.w, nb) - first, 0));
+          }
+          const int slot = r % kOptKvRing;
+          if (!mbar_wait(&it_empty[slot], ((r / kOptKvRing) & 1) ^ 1u, status, kSiteAttention))
+            return false;
+          items[slot].entry = it.entry;
+          items[slot].head = it.head;
+          mbar_arrive(&it_full[slot]);
+          return true;
+        };
+        OptKvItem cur, next;
+        read_entry();
+        ok = announce(0, cur);
+        // (an item's first loads are issued before the next item is asked about)
+        auto go_on = [&](int r) -> bool {
+          if (steal.more) {
+            if (!steal.next(status)) return false;
+            read_entry();
+          }
+          return announce(r + 1, next);
+        };
+        for (int r = 0; ok && cur.entry.w >= 0; ++r, cur = next) {
+          const int bi = cur.entry.x, r0 = cur.entry.y * 128, hh = cur.head;
+          const int cq = hh * D, ck = a + hh * D, cv = 2 * a + hh * D;
+          const bool early = r > 0 || cur.entry.w == 0;  // (the first item's loads go first)
+          if (early && !(ok = go_on(r))) break;
+          for (int i = 0; ok && i < cur.entry.w; ++i, ++g) {
+            if (i == 0) {
+              if (!(ok = mbar_wait(k_empty, (n & 1) ^ 1u, status, kSiteAttention))) break;
+              mbar_arrive_expect_tx(k_full, C::kTile);
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(sK + c * 16384, &tm_qkv, k_full, ck + c * 64, r0, bi);
+              v_loaded = false;
+            }
+            const int st = g & 1, row = (cur.entry.z + i) * 128;
+            if (!(ok = mbar_wait(&st_empty[st], ((g >> 1) & 1) ^ 1u, status, kSiteAttention)))
+              break;
+            mbar_arrive_expect_tx(&st_full[st], 2 * C::kTile);
+            for (int c = 0; c < C::kChunks; ++c) {
+              tma_load_3d(sQ + st * C::kTile + c * 16384, &tm_qkv, &st_full[st], cq + c * 64, row,
+                          bi);
+              tma_load_3d(sdO + st * C::kTile + c * 16384, &tm_do, &st_full[st], hh * D + c * 64,
+                          row, bi);
+            }
+            if (i == 0) {
+              if (!(ok = mbar_wait(v_empty, (n & 1) ^ 1u, status, kSiteAttention))) {
+                ++g;
+                break;
+              }
+              mbar_arrive_expect_tx(v_full, C::kTile);
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(sV + c * 16384, &tm_qkv, v_full, cv + c * 64, r0, bi);
+              v_loaded = true;
+              ++n;
+              if (!early && !(ok = go_on(r))) {
+                ++g;
+                break;
+              }
+            }
+          }
         }
-        __syncwarp();
+        steal.finish(status);
+        pdl_launch();  // every load of this CTA is issued
+        // Copies still in flight must land before the CTA exits.
+        const int kn = v_loaded ? n : n + 1;  // K tiles issued
+        if (kn > 0) mbar_wait(k_full, (kn - 1) & 1, status, kSiteAttention, 200000000ull, false);
+        if (n > 0) mbar_wait(v_full, (n - 1) & 1, status, kSiteAttention, 200000000ull, false);
+        for (int i = g - 1; i >= 0 && i >= g - 2; --i)
+          mbar_wait(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention, 200000000ull, false);
       }
-      if (i > 0) {
-        const int pi = i - 1;
-        const uint32_t pst = (pi & 1) * C::kTile;
-        if (!mbar_wait_warp(p_full, pi & 1, status, kSiteAttention)) break;
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      // The whole warp walks the loop, so that addresses and descriptors stay
+      // in uniform registers; one lane issues.
+      constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+      const bool leader = elect_one();
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), 16, 1024);
+      // Q_i and dO_i, K-major (S, dP) and MN-major (dK, dV)
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t do_desc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
+      const uint64_t qt_desc = smem_desc_sw128(smem_u32(sQ), 16384, 1024);
+      const uint64_t dot_desc = smem_desc_sw128(smem_u32(sdO), 16384, 1024);
+      int g = 0, n = 0;     // blocks, items with blocks
+      bool pend = false;    // the products of block g - 1 are still to be issued,
+      bool pend_first = false;  // as the first ones of their item
+      bool ok = true;
+      auto products = [&](int pg) -> bool {
+        if (!mbar_wait_warp(p_full, pg & 1, status, kSiteAttention)) return false;
         tc_fence_after();
-        const uint64_t qd = smem_desc_add(qt_desc, pst), dod = smem_desc_add(dot_desc, pst);
-        const uint32_t acc0 = pi > 0 ? 1u : 0u;
+        const uint64_t qd = smem_desc_add(qt_desc, (pg & 1) * C::kTile);
+        const uint64_t dod = smem_desc_add(dot_desc, (pg & 1) * C::kTile);
+        const uint32_t acc0 = pend_first ? 0u : 1u;
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 128 / 16; ++kk) {
@@ -228,263 +306,396 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
             umma_bf16_ts(tdV, tdP + pcol, smem_desc_add(dod, kk * 2048), kIdescAcc, acc);
             umma_bf16_ts(tdK, tdP + pcol + 8, smem_desc_add(qd, kk * 2048), kIdescAcc, acc);
           }
-          umma_commit(&st_empty[pi & 1]);
+          umma_commit(&st_empty[pg & 1]);
           umma_commit(acc_done);
         }
         __syncwarp();
-      }
-      if (i < count) {
-        // dP^T_i overwrites the P^T / dz^T that the products above read.
-        if (i > 0 && !mbar_wait_warp(acc_done, (i - 1) & 1, status, kSiteAttention)) break;
-        tc_fence_after();
-        const uint64_t dod = smem_desc_add(do_desc, st);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tdP, smem_desc_add(v_desc, off), smem_desc_add(dod, off), kIdescSq,
-                      kk > 0 ? 1u : 0u);
-          }
-          umma_commit(dp_full);
+        return true;
+      };
+      for (int r = 0; ok; ++r) {
+        const int slot = r % kOptKvRing;
+        if (!(ok = mbar_wait_warp(&it_full[slot], (r / kOptKvRing) & 1, status, kSiteAttention)))
+          break;
+        const int count = __shfl_sync(0xffffffffu, items[slot].entry.w, 0);
+        if (leader) mbar_arrive(&it_empty[slot]);
+        if (count < 0) break;
+        if (count == 0 && pend) {
+          // nothing to overlap with, and the items behind may wait for this one
+          if (!(ok = products(g - 1))) break;
+          pend = false;
         }
-        __syncwarp();
+        for (int i = 0; ok && i < count; ++i, ++g) {
+          const int st = g & 1;
+          if (i == 0) {
+            // S^T_g before the products of block g - 1, unless those are ready
+            // first (an item's first S^T waits for its K).
+            if (pend) {
+              const int first = mbar_wait_first(k_full, n & 1, p_full, (g - 1) & 1, status,
+                                                kSiteAttention);
+              if (__all_sync(0xffffffffu, first == 2)) {
+                if (!(ok = products(g - 1))) break;
+                pend = false;
+              }
+            }
+            if (!(ok = mbar_wait_warp(k_full, n & 1, status, kSiteAttention))) break;
+          }
+          if (!(ok = mbar_wait_warp(&st_full[st], (g >> 1) & 1, status, kSiteAttention))) break;
+          // tS was read into registers for block g - 1.
+          if (g > 0 && !(ok = mbar_wait_warp(s_free, (g - 1) & 1, status, kSiteAttention))) break;
+          tc_fence_after();
+          const uint64_t qd = smem_desc_add(q_desc, st * C::kTile);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              umma_bf16(tS, smem_desc_add(k_desc, off), smem_desc_add(qd, off), kIdescSq,
+                        kk > 0 ? 1u : 0u);
+            }
+            umma_commit(s_full);
+            if (i == count - 1) umma_commit(k_empty);
+          }
+          __syncwarp();
+          if (pend && !(ok = products(g - 1))) break;
+          pend = true;
+          pend_first = i == 0;
+          if (i == 0 && !(ok = mbar_wait_warp(v_full, n & 1, status, kSiteAttention))) break;
+          // dP^T_g overwrites the P^T / dz^T that the products above read.
+          if (g > 0 && !(ok = mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteAttention))) break;
+          tc_fence_after();
+          const uint64_t dod = smem_desc_add(do_desc, st * C::kTile);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              umma_bf16(tdP, smem_desc_add(v_desc, off), smem_desc_add(dod, off), kIdescSq,
+                        kk > 0 ? 1u : 0u);
+            }
+            umma_commit(dp_full);
+            if (i == count - 1) umma_commit(v_empty);
+          }
+          __syncwarp();
+          if (i == 0) ++n;
+        }
       }
+      if (ok && pend) products(g - 1);
+      if (leader) {
+        umma_commit(drain);
+        mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+      }
+      __syncwarp();
     }
-    if (leader) {
-      umma_commit(drain);
-      mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
-    }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- compute
+    setmaxnreg_inc<kOptKvRegsCompute>();
     // Two warps per TMEM lane quarter; `half` picks 64 of the 128 query columns.
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - 4) >> 2;
     const int t = quarter * 32 + lane;  // key row within the block
-    const int r = r0 + t;               // this thread's key
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t my_cols = lane_off + static_cast<uint32_t>(half * 64);
-    const ScoreConst sc =
-        score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, BIAS ? A.slopes[hh] : 0.f);
-    const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s;  // of lse and delta
-    const int64_t brow = static_cast<int64_t>(bi) * s;             // of the intervals
+    bool ok = true;
     // What query t of the next block brings, loaded one block ahead (half 0).
     // Queries past the sequence see the whole block: their Q and dO are zeros.
     float nl2 = 0.f, nd = 0.f;
     int nrange = 128 << 8;
-    auto load_query = [&](int qn) {
+    auto load_query = [&](int bi, int hh, int r0, int qn) {
       nl2 = 0.f;
       nd = 0.f;
       nrange = 128 << 8;
       if (qn < s) {
-        nl2 = A.lse[hrow + qn] * kOptLog2e;
-        nd = A.delta[hrow + qn];
-        const int first = min(max(A.key_lo[brow + qn] - r0, 0), 128);
-        const int end = min(max(min(A.key_hi[brow + qn], s) - r0, 0), 128);
+        const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s + qn;
+        const int64_t brow = static_cast<int64_t>(bi) * s + qn;
+        nl2 = A.lse[hrow] * kOptLog2e;
+        nd = A.delta[hrow];
+        const int first = min(max(A.key_lo[brow] - r0, 0), 128);
+        const int end = min(max(min(A.key_hi[brow], s) - r0, 0), 128);
         nrange = first | (end << 8);
       }
     };
-    if (half == 0 && count > 0) load_query(qb0 * 128 + t);
-    bool ok = true;
-    for (int i = 0; i < count; ++i) {
-      const int c0 = (qb0 + i) * 128;  // first query of this block
-      const float* l2 = sL + (i & 1) * 128 + half * 64;
-      const float* dl = sD + (i & 1) * 128 + half * 64;
-      if (half == 0) {
-        sL[(i & 1) * 128 + t] = nl2;
-        sD[(i & 1) * 128 + t] = nd;
-        sM[(i & 1) * 128 + t] = static_cast<uint16_t>(nrange);
-        const bool whole = __all_sync(0xffffffffu, nrange == (128 << 8));
-        if (lane == 0) sF[(i & 1) * 4 + quarter] = whole ? 1 : 0;
-        load_query(c0 + 128 + t);
-      }
-      mbar_arrive(&lse_ready[i & 1]);
-      if (!mbar_wait_warp(&lse_ready[i & 1], (i >> 1) & 1, status, kSiteAttention) ||
-          !mbar_wait_warp(s_full, i & 1, status, kSiteAttention)) {
+    float slope = 0.f, n_slope = 0.f;
+    // waits for item r's announcement and loads its first block's queries
+    auto look_ahead = [&](int r) {
+      const int slot = r % kOptKvRing;
+      if (!mbar_wait_warp(&it_full[slot], (r / kOptKvRing) & 1, status, kSiteAttention)) {
         ok = false;
-        break;
+        return;
       }
-      tc_fence_after();
-      float p[64];
-      tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
-      tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(s_free);
-      const bool edge = (sF[(i & 1) * 4 + 2 * half] & sF[(i & 1) * 4 + 2 * half + 1]) == 0;
-      // P (bf16 pairs in pp with a cap, else still in p), and in p what dP -
-      // delta is multiplied by: P, with a cap P (1 - tanh^2).
-      uint32_t pp[CAP ? 32 : 1];
-      const float base = static_cast<float>(c0 + half * 64 - r);
-      const uint16_t* mrow = sM + (i & 1) * 128 + half * 64;
-      auto weights = [&](auto edge_c) {
-        constexpr bool EDGE = decltype(edge_c)::value;
-#pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const float4 lv = *reinterpret_cast<const float4*>(l2 + e);
-          uint32_t mm[2] = {0u, 0u};
-          if constexpr (EDGE) {
-            const uint2 w = *reinterpret_cast<const uint2*>(mrow + e);
-            mm[0] = w.x;
-            mm[1] = w.y;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = e + 2 * h;
-            float2 add = h == 0 ? make_float2(-lv.x, -lv.y) : make_float2(-lv.z, -lv.w);
-            if constexpr (CAP) add = __fadd2_rn(add, make_float2(sc.cap2, sc.cap2));
-            if constexpr (BIAS) {
-              add.x = fmaf(-sc.slope2, fabsf(base + k), add.x);
-              add.y = fmaf(-sc.slope2, fabsf(base + (k + 1)), add.y);
-            }
-            const float2 x = make_float2(p[k], p[k + 1]);
-            float2 y;
-            [[maybe_unused]] float2 rr;
-            if constexpr (CAP) {
-              rr = cap_r(x, sc.mul);
-              y = __ffma2_rn(rr, make_float2(-2.f * sc.cap2, -2.f * sc.cap2), add);
-            } else {
-              y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
-            }
-            float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            if constexpr (EDGE) {
-              const int f0 = mm[h] & 255, e0 = (mm[h] >> 8) & 255;
-              const int f1 = (mm[h] >> 16) & 255, e1 = mm[h] >> 24;
-              const bool v0 = t >= f0 && t < e0, v1 = t >= f1 && t < e1;
-              pv = make_float2(v0 ? pv.x : 0.f, v1 ? pv.y : 0.f);
-              if constexpr (CAP) rr = make_float2(v0 ? rr.x : 0.f, v1 ? rr.y : 0.f);
-            }
-            if constexpr (CAP) {
-              pp[k / 2] = pack_bf16x2(pv.x, pv.y);
-              // 1 - tanh^2 = 4 r (1 - r)
-              const float2 r4 = __fmul2_rn(rr, make_float2(4.f, 4.f));
-              const float2 om = __ffma2_rn(make_float2(-r4.x, -r4.y), rr, r4);
-              pv = __fmul2_rn(pv, om);
-            }
-            p[k] = pv.x;
-            p[k + 1] = pv.y;
-          }
-        }
-      };
-      if (edge)
-        weights(BoolC<true>{});
-      else
-        weights(BoolC<false>{});
-      if (!mbar_wait_warp(dp_full, i & 1, status, kSiteAttention)) {
-        ok = false;
-        break;
+      const int4 e = items[slot].entry;
+      if (e.w > 0) {
+        if (half == 0) load_query(e.x, items[slot].head, e.y * 128, e.z * 128 + t);
+        if constexpr (BIAS) n_slope = A.slopes[items[slot].head];
       }
-      tc_fence_after();
-      // dz^T of this block pair also goes to `ds_tiles` for the dQ product, as
-      // the 128-byte-swizzled shared-memory image of an MN-major A operand:
-      // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit of
-      // queries [8u, 8u + 8) at unit u ^ (t & 7); assembled in sDs, sent as
-      // one bulk store, whose predecessor must have read sDs first.
-      const bool store_ds = A.ds_tiles != nullptr;
-      uint8_t* ds_row = sDs + half * 16384 + t * 128;
-      if (store_ds && i > 0) {
-        if (threadIdx.x == 64) {
-          bulk_wait_read();
-          mbar_arrive(ds_free);
-        }
-        if (!mbar_wait_warp(ds_free, (i - 1) & 1, status, kSiteAttention)) {
-          ok = false;
-          break;
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float dv[16];
-        tmem_ld_32x32b_x16(tdP + my_cols + g * 16, dv);
-        uint32_t w[16];  // [P of the 16 queries | dz of the 16 queries]
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 dlv = *reinterpret_cast<const float4*>(dl + g * 16 + e);
-          const float* pq = p + g * 16 + e;
-          const float2 d0 = __fmul2_rn(make_float2(pq[0], pq[1]),
-                                       __fadd2_rn(make_float2(dv[e], dv[e + 1]),
-                                                  make_float2(-dlv.x, -dlv.y)));
-          const float2 d1 = __fmul2_rn(make_float2(pq[2], pq[3]),
-                                       __fadd2_rn(make_float2(dv[e + 2], dv[e + 3]),
-                                                  make_float2(-dlv.z, -dlv.w)));
-          if constexpr (CAP) {
-            w[e / 2] = pp[(g * 16 + e) / 2];
-            w[e / 2 + 1] = pp[(g * 16 + e) / 2 + 1];
-          } else {
-            w[e / 2] = pack_bf16x2(pq[0], pq[1]);
-            w[e / 2 + 1] = pack_bf16x2(pq[2], pq[3]);
-          }
-          w[8 + e / 2] = pack_bf16x2(d0.x, d0.y);
-          w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
-        }
-        if (store_ds) {
-          *reinterpret_cast<uint4*>(ds_row + (((2 * g) ^ (t & 7)) << 4)) =
-              make_uint4(w[8], w[9], w[10], w[11]);
-          *reinterpret_cast<uint4*>(ds_row + (((2 * g + 1) ^ (t & 7)) << 4)) =
-              make_uint4(w[12], w[13], w[14], w[15]);
-        }
-        // over this thread's own dP^T columns, already in registers
-        tmem_st_32x32b_x16(tdP + my_cols + g * 16, w);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_full);
-      if (store_ds) {
-        fence_proxy_async_smem();  // sDs writes visible to the bulk copy
-        mbar_arrive(ds_full);
-        if (warp == 2) {
-          // one thread stores the assembled tile
-          if (!mbar_wait_warp(ds_full, i & 1, status, kSiteAttention)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            const int qb = qb0 + i;
-            // the workspace of a causal mask has no tile above the diagonal
-            if (check_index(!A.causal || kb <= qb, status, kSiteAttention)) {
-              bulk_store(A.ds_tiles +
-                             opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb, kb) *
-                                 kOptTileBytes,
-                         sDs, static_cast<uint32_t>(kOptTileBytes));
-              bulk_commit();
-            }
-          }
-        }
-      }
-    }
-    // the tile stores must be complete (and done with sDs) before exit
-    if (A.ds_tiles && threadIdx.x == 64) bulk_wait_all();
-    if (count > 0 && ok) ok = mbar_wait_warp(acc_done, (count - 1) & 1, status, kSiteAttention);
-    if (ok && ok_entry) {
-      tc_fence_after();
-      const float scale = rsqrtf(static_cast<float>(D));
-      const int64_t row = (brow + r) * 3 * static_cast<int64_t>(a);
+    };
+    // dV and dK of the item before, in TMEM until its last products are done,
+    // or (a key block that no query sees) zeros.
+    bool pending = false;
+    int p_row = 0, p_bi = 0, p_head = 0;
+    auto store_item = [&](bool from_tmem, int row0, int bi, int hh) {
+      const int warp_row = row0 + quarter * 32;
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
         // w = 0: dV (V's columns of dqkv), w = 1: dK scaled by 1/sqrt(d)
-        const uint32_t tacc = w == 0 ? tdV : tdK;
-        // (a key block that no query sees gets zeros)
-        const float mul = w == 0 ? 1.f : scale;
+        const float mul = w == 0 ? 1.f : rsqrtf(static_cast<float>(D));
         const int col = (w == 0 ? 2 * a : a) + hh * D;
+        uint16_t* base = A.dqkv + (static_cast<int64_t>(bi) * s + warp_row) * 3 * a + col;
+        const bool in_range = MC_DCHECK(warp_row >= 0 && bi >= 0 && bi < A.b && col + D <= 3 * a,
+                                        status, kSiteAttention);
 #pragma unroll 1
         for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
           float v[32] = {};
-          if (count > 0) tmem_ld_32x32b_x32(tacc + lane_off + c * 32, v);
-          if (r < s && MC_DCHECK(r >= 0 && col + c * 32 + 32 <= 3 * a, status, kSiteAttention)) {
-            uint4* dst = reinterpret_cast<uint4*>(A.dqkv + row + col + c * 32);
+          if (from_tmem) tmem_ld_32x32b_x32((w == 0 ? tdV : tdK) + lane_off + c * 32, v);
+          store_rows32(base + c * 32, 3ll * a, in_range ? s - warp_row : 0, v, mul, lane);
+        }
+      }
+    };
+    look_ahead(0);
+    int g = 0;
+    for (int r = 0; ok; ++r) {
+      const OptKvItem& it = items[r % kOptKvRing];
+      const int count = it.entry.w;
+      if (count < 0) break;
+      const int bi = it.entry.x, r0 = it.entry.y * 128, qb0 = it.entry.z, kb = it.entry.y;
+      const int hh = it.head;
+      slope = n_slope;
+      const ScoreConst sc =
+          score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
+      const CapPoly poly = cap_poly(1.f);
+      for (int i = 0; i < count; ++i, ++g) {
+        const int c0 = (qb0 + i) * 128;  // first query of this block
+        const float* l2 = sL + (g & 1) * 128 + half * 64;
+        const float* dl = sD + (g & 1) * 128 + half * 64;
+        if (half == 0) {
+          sL[(g & 1) * 128 + t] = nl2;
+          sD[(g & 1) * 128 + t] = nd;
+          sM[(g & 1) * 128 + t] = static_cast<uint16_t>(nrange);
+          const bool whole = __all_sync(0xffffffffu, nrange == (128 << 8));
+          if (lane == 0) sF[(g & 1) * 4 + quarter] = whole ? 1 : 0;
+          if (i + 1 < count) load_query(bi, hh, r0, c0 + 128 + t);
+        }
+        if (r > 0 && i + 1 == count) look_ahead(r + 1);
+        mbar_arrive_warp(&lse_ready[g & 1], lane);
+        if (!ok || !mbar_wait_warp(&lse_ready[g & 1], (g >> 1) & 1, status, kSiteAttention) ||
+            !mbar_wait_warp(s_full, g & 1, status, kSiteAttention)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float p[64];
+        tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
+        tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive_warp(s_free, lane);
+        const bool edge = (sF[(g & 1) * 4 + 2 * half] & sF[(g & 1) * 4 + 2 * half + 1]) == 0;
+        const uint16_t* mrow = sM + (g & 1) * 128 + half * 64;
+        // the warp's visible scores are far enough below the cap
+        bool small = false;
+        if constexpr (CAP) {
+          float hi = -INFINITY, low = INFINITY;
+          if (edge) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 wv;
-              wv.x = pack_bf16x2(v[8 * k + 0] * mul, v[8 * k + 1] * mul);
-              wv.y = pack_bf16x2(v[8 * k + 2] * mul, v[8 * k + 3] * mul);
-              wv.z = pack_bf16x2(v[8 * k + 4] * mul, v[8 * k + 5] * mul);
-              wv.w = pack_bf16x2(v[8 * k + 6] * mul, v[8 * k + 7] * mul);
-              dst[k] = wv;
+            for (int e = 0; e < 64; e += 2) {
+              const uint32_t m2 = *reinterpret_cast<const uint32_t*>(mrow + e);
+              const bool v0 = t >= static_cast<int>(m2 & 255) && t < static_cast<int>((m2 >> 8) & 255);
+              const bool v1 = t >= static_cast<int>((m2 >> 16) & 255) && t < static_cast<int>(m2 >> 24);
+              hi = fmax3f(hi, v0 ? p[e] : -INFINITY, v1 ? p[e + 1] : -INFINITY);
+              low = fmin3f(low, v0 ? p[e] : INFINITY, v1 ? p[e + 1] : INFINITY);
+            }
+          } else {
+            float hi1 = -INFINITY, low1 = INFINITY;
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              hi = fmax3f(hi, p[e], p[e + 1]);
+              low = fmin3f(low, p[e], p[e + 1]);
+              hi1 = fmax3f(hi1, p[e + 2], p[e + 3]);
+              low1 = fmin3f(low1, p[e + 2], p[e + 3]);
+            }
+            hi = fmaxf(hi, hi1);
+            low = fminf(low, low1);
+          }
+          small = __all_sync(0xffffffffu, fmaxf(hi, -low) * sc.arg <= kCapSmall);
+        }
+        // P (bf16 pairs in pp with a cap, else still in p), and in p what dP -
+        // delta is multiplied by: P, with a cap P (1 - tanh^2).
+        uint32_t pp[CAP ? 32 : 1];
+        const float base = sc.slope2 * static_cast<float>(c0 + half * 64 - (r0 + t));
+        auto weights = [&](auto edge_c, auto small_c) {
+          constexpr bool EDGE = decltype(edge_c)::value;
+          [[maybe_unused]] constexpr bool SMALL = decltype(small_c)::value;
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float4 lv = *reinterpret_cast<const float4*>(l2 + e);
+            uint32_t mm[2] = {0u, 0u};
+            if constexpr (EDGE) {
+              const uint2 w = *reinterpret_cast<const uint2*>(mrow + e);
+              mm[0] = w.x;
+              mm[1] = w.y;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k = e + 2 * h;
+              float2 add = h == 0 ? make_float2(-lv.x, -lv.y) : make_float2(-lv.z, -lv.w);
+              if constexpr (BIAS) {
+                add.x -= fabsf(fmaf(sc.slope2, static_cast<float>(k), base));
+                add.y -= fabsf(fmaf(sc.slope2, static_cast<float>(k + 1), base));
+              }
+              const float2 x = make_float2(p[k], p[k + 1]);
+              float2 y;
+              [[maybe_unused]] float2 th;  // tanh
+              if constexpr (CAP) {
+                if constexpr (SMALL) {
+                  const float2 arg = __fmul2_rn(x, make_float2(sc.arg, sc.arg));
+                  th = __fmul2_rn(arg, cap_small(arg, poly));
+                } else {
+                  th = __ffma2_rn(cap_r(x, sc.mul), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
+                }
+                y = __ffma2_rn(th, make_float2(sc.cap2, sc.cap2), add);
+              } else {
+                y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
+              }
+              float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              if constexpr (EDGE) {
+                const int f0 = mm[h] & 255, e0 = (mm[h] >> 8) & 255;
+                const int f1 = (mm[h] >> 16) & 255, e1 = mm[h] >> 24;
+                const bool v0 = t >= f0 && t < e0, v1 = t >= f1 && t < e1;
+                pv = make_float2(v0 ? pv.x : 0.f, v1 ? pv.y : 0.f);
+                if constexpr (CAP) th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
+              }
+              if constexpr (CAP) {
+                pp[k / 2] = pack_bf16x2(pv.x, pv.y);
+                const float2 om = __ffma2_rn(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f));
+                pv = __fmul2_rn(pv, om);
+              }
+              p[k] = pv.x;
+              p[k + 1] = pv.y;
+            }
+          }
+        };
+        if constexpr (CAP) {
+          if (small) {
+            if (edge)
+              weights(BoolC<true>{}, BoolC<true>{});
+            else
+              weights(BoolC<false>{}, BoolC<true>{});
+          } else {
+            weights(BoolC<true>{}, BoolC<false>{});
+          }
+        } else {
+          if (edge)
+            weights(BoolC<true>{}, BoolC<false>{});
+          else
+            weights(BoolC<false>{}, BoolC<false>{});
+        }
+        if (pending) {
+          if (!mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteAttention)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          store_item(true, p_row, p_bi, p_head);
+          tc_fence_before();
+          pending = false;
+        }
+        if (!mbar_wait_warp(dp_full, g & 1, status, kSiteAttention)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // dz^T of this block pair also goes to `ds_tiles` for the dQ product, as
+        // the 128-byte-swizzled shared-memory image of an MN-major A operand:
+        // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit of
+        // queries [8u, 8u + 8) at unit u ^ (t & 7); assembled in sDs, sent as
+        // one bulk store, whose predecessor must have read sDs first.
+        const bool store_ds = A.ds_tiles != nullptr;
+        uint8_t* ds_row = sDs + half * 16384 + t * 128;
+        if (store_ds && g > 0) {
+          if (threadIdx.x == 128) {
+            bulk_wait_read();
+            mbar_arrive(ds_free);
+          }
+          if (!mbar_wait_warp(ds_free, (g - 1) & 1, status, kSiteAttention)) {
+            ok = false;
+            break;
+          }
+        }
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          float dv[16];
+          tmem_ld_32x32b_x16(tdP + my_cols + gr * 16, dv);
+          uint32_t w[16];  // [P of the 16 queries | dz of the 16 queries]
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 dlv = *reinterpret_cast<const float4*>(dl + gr * 16 + e);
+            const float* pq = p + gr * 16 + e;
+            const float2 d0 = __fmul2_rn(make_float2(pq[0], pq[1]),
+                                         __fadd2_rn(make_float2(dv[e], dv[e + 1]),
+                                                    make_float2(-dlv.x, -dlv.y)));
+            const float2 d1 = __fmul2_rn(make_float2(pq[2], pq[3]),
+                                         __fadd2_rn(make_float2(dv[e + 2], dv[e + 3]),
+                                                    make_float2(-dlv.z, -dlv.w)));
+            if constexpr (CAP) {
+              w[e / 2] = pp[(gr * 16 + e) / 2];
+              w[e / 2 + 1] = pp[(gr * 16 + e) / 2 + 1];
+            } else {
+              w[e / 2] = pack_bf16x2(pq[0], pq[1]);
+              w[e / 2 + 1] = pack_bf16x2(pq[2], pq[3]);
+            }
+            w[8 + e / 2] = pack_bf16x2(d0.x, d0.y);
+            w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
+          }
+          if (store_ds) {
+            *reinterpret_cast<uint4*>(ds_row + (((2 * gr) ^ (t & 7)) << 4)) =
+                make_uint4(w[8], w[9], w[10], w[11]);
+            *reinterpret_cast<uint4*>(ds_row + (((2 * gr + 1) ^ (t & 7)) << 4)) =
+                make_uint4(w[12], w[13], w[14], w[15]);
+          }
+          // over this thread's own dP^T columns, already in registers
+          tmem_st_32x32b_x16(tdP + my_cols + gr * 16, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(p_full, lane);
+        if (store_ds) {
+          fence_proxy_async_smem();  // sDs writes visible to the bulk copy
+          mbar_arrive_warp(ds_full, lane);
+          if (warp == 4) {
+            // one thread stores the assembled tile
+            if (!mbar_wait_warp(ds_full, g & 1, status, kSiteAttention)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              const int qb = qb0 + i;
+              // the workspace of a causal mask has no tile above the diagonal
+              if (check_index(!A.causal || kb <= qb, status, kSiteAttention)) {
+                bulk_store(A.ds_tiles +
+                               opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb, kb) *
+                                   kOptTileBytes,
+                           sDs, static_cast<uint32_t>(kOptTileBytes));
+                bulk_commit();
+              }
             }
           }
         }
       }
+      if (!ok) break;
+      if (r == 0 || count == 0) look_ahead(r + 1);
+      if (count > 0) {
+        p_row = r0;
+        p_bi = bi;
+        p_head = hh;
+        pending = true;
+      } else {
+        store_item(false, r0, bi, hh);
+      }
+      mbar_arrive_warp(&it_empty[r % kOptKvRing], lane);
     }
+    if (ok && pending && mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteAttention)) {
+      tc_fence_after();
+      store_item(true, p_row, p_bi, p_head);
+    }
+    // the tile stores must be complete (and done with sDs) before exit
+    if (A.ds_tiles && threadIdx.x == 128) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -552,8 +763,8 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 256);
-    mbar_init(ds_full, 256);
+    mbar_init(s_free, 8);
+    mbar_init(ds_full, 8);
     mbar_init(ds_free, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -701,7 +912,7 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
       tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64 + 32, dv + 32);
       tmem_ld_wait();
       tc_fence_before();
-      mbar_arrive(s_free);
+      mbar_arrive_warp(s_free, lane);
       const int c0 = k_lo + j * 128 + half * 64;
       const bool edge = __any_sync(0xffffffffu, lo > c0 || hi < c0 + 64);
       const int first = lo - c0, end = hi - c0;
@@ -746,29 +957,21 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
       tmem_st_32x32b_x32(tdS + lane_off + half * 32, dw);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(ds_full);
+      mbar_arrive_warp(ds_full, lane);
     }
     if (count > 0 && ok) ok = mbar_wait_warp(ds_free, (count - 1) & 1, status, kSiteAttention);
     if (ok && ok_entry) {
       tc_fence_after();
-      const float scale = rsqrtf(static_cast<float>(D));
-      const int64_t row = (static_cast<int64_t>(bi) * s + r) * 3 * static_cast<int64_t>(a);
+      const int warp_row = q0 + quarter * 32;
+      uint16_t* base =
+          A.dqkv + (static_cast<int64_t>(bi) * s + warp_row) * 3 * a + hh * D;
+      const bool in_range = MC_DCHECK(warp_row >= 0 && hh * D + D <= a, status, kSiteAttention);
 #pragma unroll 1
       for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
         float v[32] = {};
         if (count > 0) tmem_ld_32x32b_x32(tdQ + lane_off + c * 32, v);
-        if (r < s && MC_DCHECK(r >= 0 && hh * D + c * 32 + 32 <= a, status, kSiteAttention)) {
-          uint4* dst = reinterpret_cast<uint4*>(A.dqkv + row + hh * D + c * 32);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 wv;
-            wv.x = pack_bf16x2(v[8 * k + 0] * scale, v[8 * k + 1] * scale);
-            wv.y = pack_bf16x2(v[8 * k + 2] * scale, v[8 * k + 3] * scale);
-            wv.z = pack_bf16x2(v[8 * k + 4] * scale, v[8 * k + 5] * scale);
-            wv.w = pack_bf16x2(v[8 * k + 6] * scale, v[8 * k + 7] * scale);
-            dst[k] = wv;
-          }
-        }
+        store_rows32(base + c * 32, 3ll * a, in_range ? s - warp_row : 0, v,
+                     rsqrtf(static_cast<float>(D)), lane);
       }
     }
   }
@@ -788,33 +991,20 @@ struct OptDqGemmCfg {
   static constexpr int kKTile = 128 * D * 2;
   static constexpr int kStage = static_cast<int>(kOptTileBytes) + kKTile;
   static constexpr int kStages = 3;
-  static constexpr int kUsed = kStages * kStage + 16 * 8;
-  static constexpr int kSmem = kUsed + 1024;  // + alignment slack
+  static constexpr int kUsed = kStages * kStage + 24 * 8 + 4 * 32;  // barriers, items
+  // one CTA per SM, so that the CTAs that do not start are there to be stolen
+  static constexpr int kSmem = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;
   static_assert(kSmem <= 227 * 1024, "dq gemm shared memory");
   static constexpr uint32_t kTmemCols = 256;  // two accumulators of 128 columns
 };
 
-// Item r of this CTA: the (query entry, head) pairs in dispatch order, handed
-// out in a snake; its key blocks are [kb0, kb0 + nj).  1: an item, 0: the
-// CTA's share is done.
-__device__ __forceinline__ int opt_dq_item(int r, const OptBwdArgs& A, int nb, int& qb, int& bi,
-                                           int& hh, int& kb0, int& nj) {
-  const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-  const int64_t n = static_cast<int64_t>(A.b) * nb;
-  const int64_t k = static_cast<int64_t>(r) * G + ((r & 1) ? G - 1 - c : c);
-  if (k >= n * A.H) return 0;
-  const int64_t rank = A.head_major ? k / A.H : k % n;
-  hh = static_cast<int>(A.head_major ? k % A.H : k / n);
-  const int4 e = *reinterpret_cast<const int4*>(A.tables + 4 * rank);
-  bi = min(max(e.x, 0), A.b - 1);
-  qb = min(max(e.y, 0), nb - 1);
-  const int lo = max(e.z, 0), hi = min(e.w, A.s);
-  kb0 = lo / 128;
-  int end = hi > lo ? (hi + 127) / 128 : kb0;
-  if (A.causal) end = min(end, qb + 1);  // the workspace has no other tiles
-  nj = max(end - kb0, 0);
-  return 1;
-}
+// What every role needs to know of an item: a (query block, head) pair.
+struct alignas(16) OptDqItem {
+  int4 entry;  // sequence, query block, first key block, key blocks (-1: no more items)
+  int head;
+  int pad[3];
+};
+constexpr int kOptDqRing = 4;
 
 // Persistent, 192 threads: warp 0 loads per key block the dz^T tile (one bulk
 // copy of its swizzled image) and K_j into a 3-deep ring that runs on across
@@ -832,9 +1022,14 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t* full = bars + 0;       // [3]
   uint64_t* empty = bars + 3;      // [3]
   uint64_t* acc_full = bars + 6;   // [2]  an item's dQ is complete in accumulator a
-  uint64_t* acc_empty = bars + 8;  // [2]  the epilogue has read accumulator a (128 threads)
+  uint64_t* acc_empty = bars + 8;  // [2]  the epilogue has read accumulator a (4 warps)
   uint64_t* drain = bars + 10;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 11);
+  uint64_t* it_full = bars + 11;   // [kOptDqRing]
+  uint64_t* it_empty = bars + 15;  // [kOptDqRing] read by the MMA and epilogue warps (5)
+  uint64_t* steal_bar = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  void* response = bars + 22;  // 16 bytes, aligned as the stages are
+  OptDqItem* items = reinterpret_cast<OptDqItem*>(bars + 24);
   int* status = A.status;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -847,9 +1042,14 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&acc_empty[i], 4);
     }
     mbar_init(drain, 1);
+    mbar_init(steal_bar, 1);
+    for (int i = 0; i < kOptDqRing; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 5);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tm_qkv);
   }
@@ -863,14 +1063,41 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the dK/dV kernel (the tiles) has completed
 
-  int qb, bi, hh, kb0, nj;
   if (warp == 0) {
     if (lane == 0) {
       // -------------------------------------------------------- producer
       int gt = 0;  // tiles issued, across items
       bool ok = true;
-      for (int r = 0; ok && opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
-        for (int j = 0; j < nj; ++j, ++gt) {
+      OptItems steal(response, steal_bar, A.b * nb * H, A.steal);
+      int4 e_next = make_int4(0, 0, 0, 0);
+      int h_next = 0;
+      auto read_entry = [&]() {
+        int rank = 0;
+        if (steal.more) {
+          opt_item(steal.k, A.b * nb, H, A.head_group, rank, h_next);
+          e_next = *reinterpret_cast<const int4*>(A.tables + 4ll * rank);
+        }
+      };
+      read_entry();
+      for (int r = 0;; ++r) {
+        int4 cur = make_int4(0, 0, 0, -1);
+        const int hh = h_next;
+        if (steal.more) {
+          const int4 e = opt_checked(e_next, A.b, nb, status);
+          const int lo = max(e.z, 0), hi = min(e.w, s);
+          const int kb0 = lo / 128;
+          int end = hi > lo ? (hi + 127) / 128 : kb0;
+          if (A.causal) end = min(end, e.y + 1);  // the workspace has no other tiles
+          cur = make_int4(e.x, e.y, kb0, max(end - kb0, 0));
+        }
+        const int slot = r % kOptDqRing;
+        if (!mbar_wait(&it_empty[slot], ((r / kOptDqRing) & 1) ^ 1u, status, kSiteAttention)) break;
+        items[slot].entry = cur;
+        items[slot].head = hh;
+        mbar_arrive(&it_full[slot]);
+        if (cur.w < 0) break;
+        const int64_t hb = static_cast<int64_t>(cur.x) * H + hh;
+        for (int j = 0; j < cur.w; ++j, ++gt) {
           const int st = gt % C::kStages;
           if (!mbar_wait(&empty[st], ((gt / C::kStages) & 1) ^ 1u, status, kSiteAttention)) {
             ok = false;
@@ -879,14 +1106,16 @@ __global__ void __launch_bounds__(192, 1)
           uint8_t* dst = smem + st * C::kStage;
           mbar_arrive_expect_tx(&full[st], C::kStage);
           bulk_load(dst,
-                    A.ds_tiles + opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb,
-                                          kb0 + j) * kOptTileBytes,
+                    A.ds_tiles + opt_tile(A.causal, nb, hb, cur.y, cur.z + j) * kOptTileBytes,
                     static_cast<uint32_t>(kOptTileBytes), &full[st]);
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_3d(dst + kOptTileBytes + c * 16384, &tm_qkv, &full[st], a + hh * D + c * 64,
-                        (kb0 + j) * 128, bi);
+                        (cur.z + j) * 128, cur.x);
         }
+        if (!ok || !steal.next(status)) break;
+        read_entry();
       }
+      steal.finish(status);
       pdl_launch();  // every load of this CTA is issued
       for (int g = gt - 1; g >= 0 && g >= gt - C::kStages; --g)
         mbar_wait(&full[g % C::kStages], (g / C::kStages) & 1, status, kSiteAttention,
@@ -902,7 +1131,12 @@ __global__ void __launch_bounds__(192, 1)
     const uint64_t a_desc = smem_desc_sw128(smem_u32(smem), 16384, 1024);
     bool ok = true;
     int gt = 0;
-    for (int r = 0; ok && opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
+    for (int r = 0; ok; ++r) {
+      const int slot = r % kOptDqRing;
+      if (!mbar_wait_warp(&it_full[slot], (r / kOptDqRing) & 1, status, kSiteAttention)) break;
+      const int nj = __shfl_sync(0xffffffffu, items[slot].entry.w, 0);
+      if (leader) mbar_arrive(&it_empty[slot]);
+      if (nj < 0) break;
       const int acc = r & 1;
       // the epilogue of item r - 2 has read this accumulator
       if (!mbar_wait_warp(&acc_empty[acc], ((r >> 1) & 1) ^ 1u, status, kSiteAttention)) break;
@@ -940,32 +1174,29 @@ __global__ void __launch_bounds__(192, 1)
     const int quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float scale = rsqrtf(static_cast<float>(D));
-    for (int r = 0; opt_dq_item(r, A, nb, qb, bi, hh, kb0, nj); ++r) {
+    for (int r = 0;; ++r) {
+      const int slot = r % kOptDqRing;
+      if (!mbar_wait_warp(&it_full[slot], (r / kOptDqRing) & 1, status, kSiteAttention)) break;
+      const int4 e = items[slot].entry;
+      const int hh = items[slot].head;
+      mbar_arrive_warp(&it_empty[slot], lane);
+      if (e.w < 0) break;
+      const int bi = e.x, qb = e.y, nj = e.w;
       const int acc = r & 1;
-      const int row = qb * 128 + quarter * 32 + lane;  // this thread's query row
+      const int warp_row = qb * 128 + quarter * 32;
       if (!mbar_wait_warp(&acc_full[acc], (r >> 1) & 1, status, kSiteAttention)) break;
       tc_fence_after();
-      const int64_t base = (static_cast<int64_t>(bi) * s + row) * 3 * static_cast<int64_t>(a);
+      uint16_t* base = A.dqkv + (static_cast<int64_t>(bi) * s + warp_row) * 3 * a + hh * D;
+      const bool in_range = MC_DCHECK(warp_row >= 0 && hh * D + D <= a, status, kSiteAttention);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32] = {};
         if (nj > 0)
           tmem_ld_32x32b_x32(tmem + static_cast<uint32_t>(acc * 128) + lane_off + c * 32, v);
-        if (row < s && MC_DCHECK(row >= 0 && hh * D + c * 32 + 32 <= a, status, kSiteAttention)) {
-          uint4* dst = reinterpret_cast<uint4*>(A.dqkv + base + hh * D + c * 32);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 wv;
-            wv.x = pack_bf16x2(v[8 * k + 0] * scale, v[8 * k + 1] * scale);
-            wv.y = pack_bf16x2(v[8 * k + 2] * scale, v[8 * k + 3] * scale);
-            wv.z = pack_bf16x2(v[8 * k + 4] * scale, v[8 * k + 5] * scale);
-            wv.w = pack_bf16x2(v[8 * k + 6] * scale, v[8 * k + 7] * scale);
-            dst[k] = wv;
-          }
-        }
+        store_rows32(base + c * 32, 3ll * a, in_range ? s - warp_row : 0, v, scale, lane);
       }
       tc_fence_before();
-      mbar_arrive(&acc_empty[acc]);  // the accumulator may take the item after next
+      mbar_arrive_warp(&acc_empty[acc], lane);  // the accumulator may take the item after next
     }
   }
 
@@ -978,7 +1209,7 @@ __global__ void __launch_bounds__(192, 1)
 }
 
 // ---------------------------------------------------------------- launches
-dim3 opt_grid(const OptBwdArgs& A) {
+dim3 opt_dq_grid(const OptBwdArgs& A) {
   const unsigned n = static_cast<unsigned>(A.b) * static_cast<unsigned>((A.s + 127) / 128);
   return A.head_major ? dim3(static_cast<unsigned>(A.H), n, 1u)
                       : dim3(n, static_cast<unsigned>(A.H), 1u);
@@ -997,12 +1228,13 @@ int launch_bwd(const CUtensorMap& tq, const CUtensorMap& td, const OptBwdArgs& A
   static PerDeviceInit init_kv, init_q;
   auto kv = attn_opt_dkdv_kernel<D, CAP, BIAS>;
   if (opt_smem(init_kv, kv, OptBwdCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
-  launch_kernel(kv, opt_grid(A), dim3(kOptBwdThreads), OptBwdCfg<D>::kSmem, st, 1, tq, td, A);
+  launch_kernel(kv, dim3(static_cast<unsigned>(A.ctas)), dim3(kOptKvThreads), OptBwdCfg<D>::kSmem,
+                st, 1, tq, td, A);
   if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
   if (A.ds_tiles) return MC_OK;
   auto kq = attn_opt_dq_kernel<D, CAP, BIAS>;
   if (opt_smem(init_q, kq, OptDqCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
-  launch_kernel(kq, opt_grid(A), dim3(kOptBwdThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
+  launch_kernel(kq, opt_dq_grid(A), dim3(kOptBwdThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
 
@@ -1027,9 +1259,7 @@ int launch_bwd_d(const uint16_t* qkv, const uint16_t* dout, const OptBwdArgs& A,
   static PerDeviceInit init;
   auto kern = attn_opt_dq_gemm_kernel<D>;
   if (opt_smem(init, kern, OptDqGemmCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
-  const int64_t items = static_cast<int64_t>(A.b) * ((A.s + 127) / 128) * A.H;
-  const int grid = items < num_sms() ? static_cast<int>(items) : num_sms();
-  launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(192), OptDqGemmCfg<D>::kSmem, st, 1,
+  launch_kernel(kern, dim3(static_cast<unsigned>(A.ctas)), dim3(192), OptDqGemmCfg<D>::kSmem, st, 1,
                 tq, A);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
@@ -1059,6 +1289,10 @@ int launch_attention_opt_bwd(const uint16_t* qkv, const float* lse, const uint16
   A.s = s;
   A.H = H;
   A.head_major = attention_head_major(static_cast<int64_t>(b) * ((s + 127) / 128), H, 1) ? 1 : 0;
+  const OptGrid grid = opt_grid(b, s, H, d);
+  A.steal = grid.steal;
+  A.head_group = grid.head_group;
+  A.ctas = grid.ctas;
   A.causal = opt.causal ? 1 : 0;
   A.status = status;
   return d == 64 ? launch_bwd_d<64>(qkv, dout, A, st) : launch_bwd_d<128>(qkv, dout, A, st);

@@ -53,7 +53,7 @@ struct OptFwdCfg {
   static constexpr int kHalf = 128 * D * 2;        // 128 rows of K or V
   static constexpr int kVSlots = D == 64 ? 4 : 2;
   static constexpr int kXch = 2 * 2 * 128 * 4;     // [parity][half][row] floats
-  static constexpr int kBars = 40 * 8;
+  static constexpr int kBars = 38 * 8;  // and 16 bytes of work stealing
   // The dynamic shared memory starts 1024-byte aligned (checked at run time),
   // so no alignment slack is reserved: at D = 128 it would not fit.
   static constexpr int kUsed = kQTile + 2 * kKTile + kVSlots * kHalf + kXch +
@@ -73,6 +73,7 @@ struct OptFwdArgs {
   const float* slopes;
   float softcap;
   int b, s, H;
+  int steal, head_group;
   int* status;
 };
 
@@ -109,7 +110,9 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
   uint64_t* xbar = bars + 20;      // [4] per lane quarter: the halves' exchange (64 threads)
   uint64_t* it_full = bars + 24;   // [kOptRing]
   uint64_t* it_empty = bars + 28;  // [kOptRing] read by the MMA thread and the softmax (257)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
+  uint64_t* steal_bar = bars + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
+  void* response = bars + 34;  // 16 bytes, aligned as the items are
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = A.s, a = A.H * D;
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
     mbar_init(pv_done, 1);
     mbar_init(o_free, 256);
     mbar_init(drain, 1);
+    mbar_init(steal_bar, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 64);
     for (int i = 0; i < kOptRing; ++i) {
       mbar_init(&it_full[i], 1);
@@ -179,16 +183,18 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         // one's intervals early, and their table entries are read two ahead.
         int4 e_next = make_int4(0, 0, 0, 0);
         int h_next = 0;
-        bool more = true;
-        auto read_entry = [&](int r) {
+        OptItems steal(response, steal_bar, A.b * nb * A.H, A.steal);
+        auto read_entry = [&]() {
           int rank = 0;
-          more = opt_item(r, A.b * nb, A.H, rank, h_next);
-          if (more) e_next = *reinterpret_cast<const int4*>(A.tables + 4ll * rank);
+          if (steal.more) {
+            opt_item(steal.k, A.b * nb, A.H, A.head_group, rank, h_next);
+            e_next = *reinterpret_cast<const int4*>(A.tables + 4ll * rank);
+          }
         };
         auto announce = [&](int r, OptItem& it) -> bool {
           it.entry = make_int4(0, 0, 0, -1);
           it.head = h_next;
-          if (more) {
+          if (steal.more) {
             const int4 e = opt_checked(e_next, A.b, nb, status);
             const int k_lo = max(e.z, 0), k_hi = min(e.w, s);
             it.entry = make_int4(e.x, e.y, k_lo, k_hi > k_lo ? (k_hi - k_lo + 127) / 128 : 0);
@@ -199,19 +205,27 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           items[slot].entry = it.entry;
           items[slot].head = it.head;
           mbar_arrive(&it_full[slot]);
-          read_entry(r + 1);
           return true;
         };
         OptItem cur, next;
-        read_entry(0);
+        read_entry();
         ok = announce(0, cur);
+        // (an item's first loads are issued before the next item is asked about)
+        auto go_on = [&](int r) -> bool {
+          if (steal.more) {
+            if (!steal.next(status)) return false;
+            read_entry();
+          }
+          return announce(r + 1, next);
+        };
         for (int r = 0; ok && cur.entry.w >= 0; ++r, cur = next) {
           const int bi = cur.entry.x, k_lo = cur.entry.z, halves = cur.entry.w;
           const int hh = cur.head;
           // Announcing waits for an earlier item's softmax, which waits for its
           // last V: with empty items in between that V is not left pending.
           if (halves == 0) load_v();
-          if (!ok || !(ok = announce(r + 1, next))) break;
+          const bool early = r > 0 || halves == 0;  // (the first item's loads go first)
+          if (ok && early) ok = go_on(r);
           for (int j = 0; ok && 2 * j < halves; ++j, ++g) {
             if (j == 0) {
               if (!(ok = mbar_wait(q_empty, (q_n & 1) ^ 1u, status, kSiteAttention))) break;
@@ -227,6 +241,10 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
               for (int h = 0; h < nh; ++h)
                 tma_load_3d(sK[ks] + c * C::kChunkBytes + h * 16384, &tm, &k_full[ks],
                             a + hh * D + c * 64, k_lo + j * kOptKeys + h * 128, bi);
+            if (j == 0 && !early && !(ok = go_on(r))) {
+              ++g;
+              break;
+            }
             load_v();
             v_halves = nh;
             v_row = k_lo + j * kOptKeys;
@@ -235,6 +253,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           }
         }
         if (ok) load_v();
+        steal.finish(status);
         pdl_launch();  // every load of this CTA is issued
         // Copies still in flight must land before the CTA exits.
         if (q_n > 0) mbar_wait(q_full, (q_n - 1) & 1, status, kSiteAttention, 200000000ull, false);
@@ -436,11 +455,11 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       const ScoreConst sc =
           score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
       const CapPoly poly = cap_poly(sc.cap2);
-      fetch(r + 1);
-      if (!ok) break;
+      const bool early = r > 0 || halves == 0;
+      if (early) fetch(r + 1);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; 2 * j < halves; ++j, ++g) {
-        if (!mbar_wait_warp(s_full, g & 1, status, kSiteAttention)) {
+        if (!ok || !mbar_wait_warp(s_full, g & 1, status, kSiteAttention)) {
           ok = false;
           break;
         }
@@ -645,6 +664,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full);
+        if (j == 0 && !early) fetch(r + 1);
       }
       if (!ok) break;
       if (halves > 0) {
@@ -687,7 +707,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
 }
 
 template <int D, bool CAP, bool BIAS>
-int launch_fwd(const uint16_t* qkv, const OptFwdArgs& A, cudaStream_t st) {
+int launch_fwd(const uint16_t* qkv, const OptFwdArgs& A, int ctas, cudaStream_t st) {
   using C = OptFwdCfg<D>;
   const uint64_t a3 = 3ull * A.H * D;
   CUtensorMap tm;
@@ -701,18 +721,19 @@ int launch_fwd(const uint16_t* qkv, const OptFwdArgs& A, cudaStream_t st) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (attr != cudaSuccess) return MC_ERR_CUDA;
-  const int64_t items = static_cast<int64_t>(A.b) * ((A.s + 127) / 128) * A.H;
-  const int64_t ctas = num_sms();
-  launch_kernel(kern, dim3(static_cast<unsigned>(items < ctas ? items : ctas)),
-                dim3(kOptFwdThreads), C::kSmem, st, 1, tm, A);
+  launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(kOptFwdThreads), C::kSmem, st, 1, tm,
+                A);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
 
 template <int D>
-int launch_fwd_d(const uint16_t* qkv, const OptFwdArgs& A, cudaStream_t st) {
+int launch_fwd_d(const uint16_t* qkv, const OptFwdArgs& A, int ctas, cudaStream_t st) {
   const bool cap = A.softcap > 0.f, bias = A.slopes != nullptr;
-  if (cap) return bias ? launch_fwd<D, true, true>(qkv, A, st) : launch_fwd<D, true, false>(qkv, A, st);
-  return bias ? launch_fwd<D, false, true>(qkv, A, st) : launch_fwd<D, false, false>(qkv, A, st);
+  if (cap)
+    return bias ? launch_fwd<D, true, true>(qkv, A, ctas, st)
+                : launch_fwd<D, true, false>(qkv, A, ctas, st);
+  return bias ? launch_fwd<D, false, true>(qkv, A, ctas, st)
+              : launch_fwd<D, false, false>(qkv, A, ctas, st);
 }
 
 }  // namespace
@@ -731,8 +752,12 @@ int launch_attention_opt_fwd(const uint16_t* qkv, uint16_t* o, float* lse, int b
   A.b = b;
   A.s = s;
   A.H = H;
+  const OptGrid grid = opt_grid(b, s, H, d);
+  A.steal = grid.steal;
+  A.head_group = grid.head_group;
   A.status = status;
-  return d == 64 ? launch_fwd_d<64>(qkv, A, st) : launch_fwd_d<128>(qkv, A, st);
+  return d == 64 ? launch_fwd_d<64>(qkv, A, grid.ctas, st)
+                 : launch_fwd_d<128>(qkv, A, grid.ctas, st);
 }
 
 }  // namespace mc

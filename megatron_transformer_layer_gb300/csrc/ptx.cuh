@@ -82,6 +82,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One arrival for a converged warp, after what all its lanes did before: the
+// lanes' own arrivals on one barrier would be taken one after another.
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
                "r"(bytes)
@@ -284,6 +291,36 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- work stealing
+// Cluster launch control: a running CTA asks for the index of one of the
+// grid's CTAs that has not started, which then never does (its resources are
+// this CTA's).  The 16-byte response lands in shared memory and is signalled on
+// `bar` as transaction bytes.  One request at a time, none after a refused one.
+__device__ __forceinline__ void clc_request(void* response, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(smem_u32(response)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The response: true and the CTA's x index, or false when none was left.
+__device__ __forceinline__ bool clc_response(const void* response, int& cta_x) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  cta_x = static_cast<int>(x);
+  return got != 0;
 }
 
 // ---------------------------------------------------------------- registers
@@ -622,6 +659,23 @@ __device__ __forceinline__ void transpose_16b_x4(uint32_t (&w)[16], int lane) {
       w[4 * v + e] = b1 ? got : x;
       w[8 + 4 * v + e] = b1 ? y : got;
     }
+}
+
+// 32 columns of a warp's 32 rows (lane = row) as bf16, v * mul, to `base` (the
+// first row's columns, 16-byte aligned; rows `stride` elements apart); the
+// first `rows` rows are stored.
+__device__ __forceinline__ void store_rows32(uint16_t* base, int64_t stride, int rows,
+                                             const float (&v)[32], float mul, int lane) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * mul, v[2 * i + 1] * mul);
+  transpose_16b_x4(w, lane);
+  uint16_t* p = base + static_cast<int64_t>(lane & ~3) * stride + (lane & 3) * 8;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if ((lane & ~3) + k < rows)
+      *reinterpret_cast<uint4*>(p + k * stride) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
 }
 
 // 32 values of one row added to a running fp32 sum (the context-parallel
