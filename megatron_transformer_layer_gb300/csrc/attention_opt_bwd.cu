@@ -62,18 +62,46 @@ template <int D>
 struct OptBwdCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = 128 * D * 2;
-  // K, V, two (Q_i, dO_i) stages, the dz^T tile staged for its bulk store,
-  // lse / delta [2][128], the queries' key ranges relative to the block
-  // [2][128] (two bytes each), their edge flags [2][4], items, barriers.  The
-  // dynamic shared memory starts 1024-byte aligned (checked at run time).
-  static constexpr int kUsed = 6 * kTile + static_cast<int>(kOptTileBytes) + 4 * 128 * 4 +
-                               2 * 128 * 2 + 2 * 4 * 4 +
-                               kOptKvRing * static_cast<int>(sizeof(OptKvItem)) + 30 * 8;
+  // K, V, three Q_i and two dO_i stages (S^T_{i+1} runs ahead of the products
+  // of block i, which read Q_i and dO_i), lse / delta [2][128], the queries'
+  // key ranges relative to the block [2][128] (two bytes each), their edge
+  // flags [2][4], items, barriers.  The dynamic shared memory starts
+  // 1024-byte aligned (checked at run time).
+  static constexpr int kQ = 3, kdO = 2;
+  static constexpr int kUsed = (2 + kQ + kdO) * kTile + 4 * 128 * 4 + 2 * 128 * 2 + 2 * 4 * 4 +
+                               kOptKvRing * static_cast<int>(sizeof(OptKvItem)) + 34 * 8;
   // one CTA per SM: it takes all 512 TMEM columns
   static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kUsed <= 227 * 1024, "dkdv kernel shared memory");
 };
+
+// Bit i of lane j becomes bit j of lane i (a 32 x 32 transpose in five steps).
+__device__ __forceinline__ uint32_t bit_transpose(uint32_t x, int lane) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const uint32_t low = d == 16  ? 0x0000FFFFu
+                         : d == 8 ? 0x00FF00FFu
+                         : d == 4 ? 0x0F0F0F0Fu
+                         : d == 2 ? 0x33333333u
+                                  : 0x55555555u;
+    // lanes without bit d keep their low columns and take the partner's low
+    // ones as high; the others the reverse
+    const bool up = lane & d;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, x, d);
+    x = up ? (x & ~low) | ((got & ~low) >> d) : (x & low) | ((got & low) << d);
+  }
+  return x;
+}
+
+// Bits [first, end) of a word.
+__device__ __forceinline__ uint32_t bit_range(int first, int end) {
+  first = min(max(first, 0), 32);
+  end = min(max(end, 0), 32);
+  const uint32_t below_end = end == 32 ? 0xFFFFFFFFu : (1u << end) - 1u;
+  const uint32_t below_first = first == 32 ? 0xFFFFFFFFu : (1u << first) - 1u;
+  return below_end & ~below_first;
+}
 
 constexpr int kOptKvThreads = 384;
 // As in the forward: 128 x 72 + 256 x 216 = 384 x 168.
@@ -108,10 +136,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   }
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::kTile;
-  uint8_t* sQ = smem + 2 * C::kTile;   // [2]
-  uint8_t* sdO = smem + 4 * C::kTile;  // [2]
-  uint8_t* sDs = smem + 6 * C::kTile;  // dz^T tile image (swizzled), 32 KB
-  float* sL = reinterpret_cast<float*>(sDs + kOptTileBytes);  // [2][128] lse * log2(e)
+  uint8_t* sQ = smem + 2 * C::kTile;             // [kQ]
+  uint8_t* sdO = smem + (2 + C::kQ) * C::kTile;  // [kdO]
+  float* sL = reinterpret_cast<float*>(sdO + C::kdO * C::kTile);  // [2][128] lse * log2(e)
   float* sD = sL + 256;                                        // [2][128] delta
   OptKvItem* items = reinterpret_cast<OptKvItem*>(sD + 256);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kOptKvRing);
@@ -119,23 +146,23 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   uint64_t* k_empty = bars + 1;    // the item's last S^T
   uint64_t* v_full = bars + 2;
   uint64_t* v_empty = bars + 3;    // the item's last dP^T
-  uint64_t* st_full = bars + 4;    // [2]
-  uint64_t* st_empty = bars + 6;   // [2]
-  uint64_t* s_full = bars + 8;     // S^T_i in TMEM
-  uint64_t* s_free = bars + 9;     // compute warps hold S^T_i in registers
-  uint64_t* dp_full = bars + 10;   // dP^T_i in TMEM
-  uint64_t* p_full = bars + 11;    // P^T_i, dz^T_i in TMEM
-  uint64_t* acc_done = bars + 12;  // dV, dK products of block i complete
-  uint64_t* drain = bars + 13;
-  uint64_t* lse_ready = bars + 14;  // [2]
-  uint64_t* ds_full = bars + 16;    // the dz^T tile of block i is in sDs (8 warps)
-  uint64_t* ds_free = bars + 17;    // its bulk store has read sDs
-  uint64_t* it_full = bars + 18;    // [kOptKvRing]
-  uint64_t* it_empty = bars + 22;   // [kOptKvRing] read by the MMA warp and the compute warps (9)
-  uint64_t* steal_bar = bars + 26;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
-  void* response = bars + 28;  // 16 bytes, aligned as the items are
-  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 30);  // [2][128] first | end << 8
+  uint64_t* q_full = bars + 4;     // [kQ]
+  uint64_t* q_empty = bars + 7;    // [kQ]  after the products
+  uint64_t* do_full = bars + 10;   // [kdO]
+  uint64_t* do_empty = bars + 12;  // [kdO] after the products
+  uint64_t* s_full = bars + 14;    // S^T_i in TMEM
+  uint64_t* s_free = bars + 15;    // compute warps hold S^T_i in registers (8 warps)
+  uint64_t* dp_full = bars + 16;   // dP^T_i in TMEM
+  uint64_t* p_full = bars + 17;    // P^T_i, dz^T_i in TMEM (8 warps)
+  uint64_t* acc_done = bars + 18;  // dV, dK products of block i complete
+  uint64_t* drain = bars + 19;
+  uint64_t* lse_ready = bars + 20;  // [2] (8 warps)
+  uint64_t* it_full = bars + 22;    // [kOptKvRing]
+  uint64_t* it_empty = bars + 26;   // [kOptKvRing] read by the MMA and the compute warps (9)
+  uint64_t* steal_bar = bars + 30;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
+  void* response = bars + 32;  // 16 bytes, aligned as the items are
+  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 34);  // [2][128] first | end << 8
   int* sF = reinterpret_cast<int*>(sM + 256);             // [2][4] the 32 queries see the whole block
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,19 +173,21 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     mbar_init(k_empty, 1);
     mbar_init(v_full, 1);
     mbar_init(v_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&st_full[i], 1);
-      mbar_init(&st_empty[i], 1);
-      mbar_init(&lse_ready[i], 8);
+    for (int i = 0; i < C::kQ; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
     }
+    for (int i = 0; i < C::kdO; ++i) {
+      mbar_init(&do_full[i], 1);
+      mbar_init(&do_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&lse_ready[i], 8);
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
     mbar_init(dp_full, 1);
     mbar_init(p_full, 8);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
-    mbar_init(ds_full, 8);
-    mbar_init(ds_free, 1);
     mbar_init(steal_bar, 1);
     for (int i = 0; i < kOptKvRing; ++i) {
       mbar_init(&it_full[i], 1);
@@ -185,6 +214,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       if (lane == 0) {
         // -------------------------------------------------------- producer
         int g = 0, n = 0;  // query blocks and items (with blocks) loaded
+        int q_n = 0, do_n = 0;
         bool ok = true, v_loaded = true;
         int4 e_next = make_int4(0, 0, 0, 0);
         int h_next = 0;
@@ -237,30 +267,30 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
                 tma_load_3d(sK + c * 16384, &tm_qkv, k_full, ck + c * 64, r0, bi);
               v_loaded = false;
             }
-            const int st = g & 1, row = (cur.entry.z + i) * 128;
-            if (!(ok = mbar_wait(&st_empty[st], ((g >> 1) & 1) ^ 1u, status, kSiteAttention)))
+            const int row = (cur.entry.z + i) * 128;
+            const int qs = g % C::kQ, ds = g % C::kdO;
+            if (!(ok = mbar_wait(&q_empty[qs], ((g / C::kQ) & 1) ^ 1u, status, kSiteAttention)))
               break;
-            mbar_arrive_expect_tx(&st_full[st], 2 * C::kTile);
-            for (int c = 0; c < C::kChunks; ++c) {
-              tma_load_3d(sQ + st * C::kTile + c * 16384, &tm_qkv, &st_full[st], cq + c * 64, row,
+            mbar_arrive_expect_tx(&q_full[qs], C::kTile);
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(sQ + qs * C::kTile + c * 16384, &tm_qkv, &q_full[qs], cq + c * 64, row,
                           bi);
-              tma_load_3d(sdO + st * C::kTile + c * 16384, &tm_do, &st_full[st], hh * D + c * 64,
+            ++q_n;
+            if (!(ok = mbar_wait(&do_empty[ds], ((g / C::kdO) & 1) ^ 1u, status, kSiteAttention)))
+              break;
+            mbar_arrive_expect_tx(&do_full[ds], C::kTile);
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(sdO + ds * C::kTile + c * 16384, &tm_do, &do_full[ds], hh * D + c * 64,
                           row, bi);
-            }
+            ++do_n;
             if (i == 0) {
-              if (!(ok = mbar_wait(v_empty, (n & 1) ^ 1u, status, kSiteAttention))) {
-                ++g;
-                break;
-              }
+              if (!(ok = mbar_wait(v_empty, (n & 1) ^ 1u, status, kSiteAttention))) break;
               mbar_arrive_expect_tx(v_full, C::kTile);
               for (int c = 0; c < C::kChunks; ++c)
                 tma_load_3d(sV + c * 16384, &tm_qkv, v_full, cv + c * 64, r0, bi);
               v_loaded = true;
               ++n;
-              if (!early && !(ok = go_on(r))) {
-                ++g;
-                break;
-              }
+              if (!early && !(ok = go_on(r))) break;
             }
           }
         }
@@ -270,8 +300,12 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         const int kn = v_loaded ? n : n + 1;  // K tiles issued
         if (kn > 0) mbar_wait(k_full, (kn - 1) & 1, status, kSiteAttention, 200000000ull, false);
         if (n > 0) mbar_wait(v_full, (n - 1) & 1, status, kSiteAttention, 200000000ull, false);
-        for (int i = g - 1; i >= 0 && i >= g - 2; --i)
-          mbar_wait(&st_full[i & 1], (i >> 1) & 1, status, kSiteAttention, 200000000ull, false);
+        for (int i = q_n - 1; i >= 0 && i >= q_n - C::kQ; --i)
+          mbar_wait(&q_full[i % C::kQ], (i / C::kQ) & 1, status, kSiteAttention, 200000000ull,
+                    false);
+        for (int i = do_n - 1; i >= 0 && i >= do_n - C::kdO; --i)
+          mbar_wait(&do_full[i % C::kdO], (i / C::kdO) & 1, status, kSiteAttention, 200000000ull,
+                    false);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
@@ -294,8 +328,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       auto products = [&](int pg) -> bool {
         if (!mbar_wait_warp(p_full, pg & 1, status, kSiteAttention)) return false;
         tc_fence_after();
-        const uint64_t qd = smem_desc_add(qt_desc, (pg & 1) * C::kTile);
-        const uint64_t dod = smem_desc_add(dot_desc, (pg & 1) * C::kTile);
+        const int qs = pg % C::kQ, ds = pg % C::kdO;
+        const uint64_t qd = smem_desc_add(qt_desc, qs * C::kTile);
+        const uint64_t dod = smem_desc_add(dot_desc, ds * C::kTile);
         const uint32_t acc0 = pend_first ? 0u : 1u;
         if (leader) {
 #pragma unroll
@@ -306,7 +341,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
             umma_bf16_ts(tdV, tdP + pcol, smem_desc_add(dod, kk * 2048), kIdescAcc, acc);
             umma_bf16_ts(tdK, tdP + pcol + 8, smem_desc_add(qd, kk * 2048), kIdescAcc, acc);
           }
-          umma_commit(&st_empty[pg & 1]);
+          umma_commit(&q_empty[qs]);
+          umma_commit(&do_empty[ds]);
           umma_commit(acc_done);
         }
         __syncwarp();
@@ -325,7 +361,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           pend = false;
         }
         for (int i = 0; ok && i < count; ++i, ++g) {
-          const int st = g & 1;
+          const int qs = g % C::kQ, ds = g % C::kdO;
           if (i == 0) {
             // S^T_g before the products of block g - 1, unless those are ready
             // first (an item's first S^T waits for its K).
@@ -339,11 +375,11 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
             }
             if (!(ok = mbar_wait_warp(k_full, n & 1, status, kSiteAttention))) break;
           }
-          if (!(ok = mbar_wait_warp(&st_full[st], (g >> 1) & 1, status, kSiteAttention))) break;
+          if (!(ok = mbar_wait_warp(&q_full[qs], (g / C::kQ) & 1, status, kSiteAttention))) break;
           // tS was read into registers for block g - 1.
           if (g > 0 && !(ok = mbar_wait_warp(s_free, (g - 1) & 1, status, kSiteAttention))) break;
           tc_fence_after();
-          const uint64_t qd = smem_desc_add(q_desc, st * C::kTile);
+          const uint64_t qd = smem_desc_add(q_desc, qs * C::kTile);
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -359,10 +395,11 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           pend = true;
           pend_first = i == 0;
           if (i == 0 && !(ok = mbar_wait_warp(v_full, n & 1, status, kSiteAttention))) break;
+          if (!(ok = mbar_wait_warp(&do_full[ds], (g / C::kdO) & 1, status, kSiteAttention))) break;
           // dP^T_g overwrites the P^T / dz^T that the products above read.
           if (g > 0 && !(ok = mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteAttention))) break;
           tc_fence_after();
-          const uint64_t dod = smem_desc_add(do_desc, st * C::kTile);
+          const uint64_t dod = smem_desc_add(do_desc, ds * C::kTile);
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -394,23 +431,34 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t my_cols = lane_off + static_cast<uint32_t>(half * 64);
     bool ok = true;
-    // What query t of the next block brings, loaded one block ahead (half 0).
-    // Queries past the sequence see the whole block: their Q and dO are zeros.
-    float nl2 = 0.f, nd = 0.f;
-    int nrange = 128 << 8;
+    // What query t of the next block brings, loaded one block ahead (half 0)
+    // and first used when it is staged: an operation on it here would wait for
+    // the loads.  Queries past the sequence see the whole block: their Q and
+    // dO are zeros.
+    float q_lse = 0.f, q_delta = 0.f;
+    int q_lo = 0, q_hi = 0, q_r0 = 0;  // and the first key of its block
+    bool q_in = false;
     auto load_query = [&](int bi, int hh, int r0, int qn) {
-      nl2 = 0.f;
-      nd = 0.f;
-      nrange = 128 << 8;
-      if (qn < s) {
+      q_in = qn < s;
+      q_r0 = r0;
+      if (q_in) {
         const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s + qn;
         const int64_t brow = static_cast<int64_t>(bi) * s + qn;
-        nl2 = A.lse[hrow] * kOptLog2e;
-        nd = A.delta[hrow];
-        const int first = min(max(A.key_lo[brow] - r0, 0), 128);
-        const int end = min(max(min(A.key_hi[brow], s) - r0, 0), 128);
-        nrange = first | (end << 8);
+        q_lse = A.lse[hrow];
+        q_delta = A.delta[hrow];
+        q_lo = A.key_lo[brow];
+        q_hi = A.key_hi[brow];
       }
+    };
+    auto stage_query = [&](int st) {
+      const int first = min(max(q_lo - q_r0, 0), 128);
+      const int end = min(max(min(q_hi, s) - q_r0, 0), 128);
+      const int range = q_in ? first | (end << 8) : 128 << 8;
+      sL[st * 128 + t] = q_in ? q_lse * kOptLog2e : 0.f;
+      sD[st * 128 + t] = q_in ? q_delta : 0.f;
+      sM[st * 128 + t] = static_cast<uint16_t>(range);
+      const bool whole = __all_sync(0xffffffffu, range == (128 << 8));
+      if (lane == 0) sF[st * 4 + quarter] = whole ? 1 : 0;
     };
     float slope = 0.f, n_slope = 0.f;
     // waits for item r's announcement and loads its first block's queries
@@ -465,11 +513,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         const float* l2 = sL + (g & 1) * 128 + half * 64;
         const float* dl = sD + (g & 1) * 128 + half * 64;
         if (half == 0) {
-          sL[(g & 1) * 128 + t] = nl2;
-          sD[(g & 1) * 128 + t] = nd;
-          sM[(g & 1) * 128 + t] = static_cast<uint16_t>(nrange);
-          const bool whole = __all_sync(0xffffffffu, nrange == (128 << 8));
-          if (lane == 0) sF[(g & 1) * 4 + quarter] = whole ? 1 : 0;
+          stage_query(g & 1);
           if (i + 1 < count) load_query(bi, hh, r0, c0 + 128 + t);
         }
         if (r > 0 && i + 1 == count) look_ahead(r + 1);
@@ -487,7 +531,17 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         tc_fence_before();
         mbar_arrive_warp(s_free, lane);
         const bool edge = (sF[(g & 1) * 4 + 2 * half] & sF[(g & 1) * 4 + 2 * half + 1]) == 0;
-        const uint16_t* mrow = sM + (g & 1) * 128 + half * 64;
+        // bit e of vis: this key is visible to query e of the 64
+        uint32_t vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int range = sM[(g & 1) * 128 + half * 64 + 32 * c + lane];
+            vis[c] = bit_transpose(
+                bit_range((range & 255) - 32 * quarter, (range >> 8) - 32 * quarter), lane);
+          }
+        }
+        auto sees = [&](int e) { return ((vis[e >> 5] >> (e & 31)) & 1u) != 0; };
         // the warp's visible scores are far enough below the cap
         bool small = false;
         if constexpr (CAP) {
@@ -495,11 +549,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           if (edge) {
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
-              const uint32_t m2 = *reinterpret_cast<const uint32_t*>(mrow + e);
-              const bool v0 = t >= static_cast<int>(m2 & 255) && t < static_cast<int>((m2 >> 8) & 255);
-              const bool v1 = t >= static_cast<int>((m2 >> 16) & 255) && t < static_cast<int>(m2 >> 24);
-              hi = fmax3f(hi, v0 ? p[e] : -INFINITY, v1 ? p[e + 1] : -INFINITY);
-              low = fmin3f(low, v0 ? p[e] : INFINITY, v1 ? p[e + 1] : INFINITY);
+              hi = fmax3f(hi, sees(e) ? p[e] : -INFINITY, sees(e + 1) ? p[e + 1] : -INFINITY);
+              low = fmin3f(low, sees(e) ? p[e] : INFINITY, sees(e + 1) ? p[e + 1] : INFINITY);
             }
           } else {
             float hi1 = -INFINITY, low1 = INFINITY;
@@ -525,12 +576,6 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float4 lv = *reinterpret_cast<const float4*>(l2 + e);
-            uint32_t mm[2] = {0u, 0u};
-            if constexpr (EDGE) {
-              const uint2 w = *reinterpret_cast<const uint2*>(mrow + e);
-              mm[0] = w.x;
-              mm[1] = w.y;
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int k = e + 2 * h;
@@ -555,9 +600,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
               }
               float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
               if constexpr (EDGE) {
-                const int f0 = mm[h] & 255, e0 = (mm[h] >> 8) & 255;
-                const int f1 = (mm[h] >> 16) & 255, e1 = mm[h] >> 24;
-                const bool v0 = t >= f0 && t < e0, v1 = t >= f1 && t < e1;
+                const bool v0 = sees(k), v1 = sees(k + 1);
                 pv = make_float2(v0 ? pv.x : 0.f, v1 ? pv.y : 0.f);
                 if constexpr (CAP) th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
               }
@@ -604,76 +647,62 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         // dz^T of this block pair also goes to `ds_tiles` for the dQ product, as
         // the 128-byte-swizzled shared-memory image of an MN-major A operand:
         // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit of
-        // queries [8u, 8u + 8) at unit u ^ (t & 7); assembled in sDs, sent as
-        // one bulk store, whose predecessor must have read sDs first.
-        const bool store_ds = A.ds_tiles != nullptr;
-        uint8_t* ds_row = sDs + half * 16384 + t * 128;
-        if (store_ds && g > 0) {
-          if (threadIdx.x == 128) {
-            bulk_wait_read();
-            mbar_arrive(ds_free);
-          }
-          if (!mbar_wait_warp(ds_free, (g - 1) & 1, status, kSiteAttention)) {
-            ok = false;
-            break;
-          }
-        }
+        // queries [8u, 8u + 8) at unit u ^ (t & 7).  (The workspace of a causal
+        // mask has no tile above the diagonal.)
+        uint8_t* tile = nullptr;
+        if (A.ds_tiles != nullptr && check_index(!A.causal || kb <= qb0 + i, status, kSiteAttention))
+          tile = A.ds_tiles +
+                 opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb0 + i, kb) *
+                     kOptTileBytes +
+                 half * 16384 + quarter * 4096;
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          float dv[16];
-          tmem_ld_32x32b_x16(tdP + my_cols + gr * 16, dv);
-          uint32_t w[16];  // [P of the 16 queries | dz of the 16 queries]
+        for (int gp = 0; gp < 2; ++gp) {
+          float dv[32];
+          tmem_ld_32x32b_x32(tdP + my_cols + gp * 32, dv);
+          uint32_t z[16];  // dz of the 32 queries
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 dlv = *reinterpret_cast<const float4*>(dl + gr * 16 + e);
-            const float* pq = p + gr * 16 + e;
-            const float2 d0 = __fmul2_rn(make_float2(pq[0], pq[1]),
-                                         __fadd2_rn(make_float2(dv[e], dv[e + 1]),
-                                                    make_float2(-dlv.x, -dlv.y)));
-            const float2 d1 = __fmul2_rn(make_float2(pq[2], pq[3]),
-                                         __fadd2_rn(make_float2(dv[e + 2], dv[e + 3]),
-                                                    make_float2(-dlv.z, -dlv.w)));
-            if constexpr (CAP) {
-              w[e / 2] = pp[(gr * 16 + e) / 2];
-              w[e / 2 + 1] = pp[(gr * 16 + e) / 2 + 1];
-            } else {
-              w[e / 2] = pack_bf16x2(pq[0], pq[1]);
-              w[e / 2 + 1] = pack_bf16x2(pq[2], pq[3]);
-            }
-            w[8 + e / 2] = pack_bf16x2(d0.x, d0.y);
-            w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
-          }
-          if (store_ds) {
-            *reinterpret_cast<uint4*>(ds_row + (((2 * gr) ^ (t & 7)) << 4)) =
-                make_uint4(w[8], w[9], w[10], w[11]);
-            *reinterpret_cast<uint4*>(ds_row + (((2 * gr + 1) ^ (t & 7)) << 4)) =
-                make_uint4(w[12], w[13], w[14], w[15]);
-          }
-          // over this thread's own dP^T columns, already in registers
-          tmem_st_32x32b_x16(tdP + my_cols + gr * 16, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive_warp(p_full, lane);
-        if (store_ds) {
-          fence_proxy_async_smem();  // sDs writes visible to the bulk copy
-          mbar_arrive_warp(ds_full, lane);
-          if (warp == 4) {
-            // one thread stores the assembled tile
-            if (!mbar_wait_warp(ds_full, g & 1, status, kSiteAttention)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              const int qb = qb0 + i;
-              // the workspace of a causal mask has no tile above the diagonal
-              if (check_index(!A.causal || kb <= qb, status, kSiteAttention)) {
-                bulk_store(A.ds_tiles +
-                               opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb, kb) *
-                                   kOptTileBytes,
-                           sDs, static_cast<uint32_t>(kOptTileBytes));
-                bulk_commit();
+          for (int gr = 0; gr < 2; ++gr) {
+            uint32_t w[16];  // [P of 16 queries | their dz]
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const int at = gp * 32 + gr * 16 + e;
+              const float4 dlv = *reinterpret_cast<const float4*>(dl + at);
+              const float* dq = dv + gr * 16 + e;
+              const float2 d0 = __fmul2_rn(make_float2(p[at], p[at + 1]),
+                                           __fadd2_rn(make_float2(dq[0], dq[1]),
+                                                      make_float2(-dlv.x, -dlv.y)));
+              const float2 d1 = __fmul2_rn(make_float2(p[at + 2], p[at + 3]),
+                                           __fadd2_rn(make_float2(dq[2], dq[3]),
+                                                      make_float2(-dlv.z, -dlv.w)));
+              if constexpr (CAP) {
+                w[e / 2] = pp[at / 2];
+                w[e / 2 + 1] = pp[at / 2 + 1];
+              } else {
+                w[e / 2] = pack_bf16x2(p[at], p[at + 1]);
+                w[e / 2 + 1] = pack_bf16x2(p[at + 2], p[at + 3]);
               }
+              w[8 + e / 2] = pack_bf16x2(d0.x, d0.y);
+              w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[gr * 8 + e] = w[8 + e];
+            // over this thread's own dP^T columns, already in registers
+            tmem_st_32x32b_x16(tdP + my_cols + gp * 32 + gr * 16, w);
+          }
+          if (gp == 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(p_full, lane);
+          }
+          if (tile) {
+            // four lanes store 64 bytes of a row
+            transpose_16b_x4(z, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = (lane & ~3) + k;
+              const int unit = (4 * gp + (lane & 3)) ^ (row & 7);
+              *reinterpret_cast<uint4*>(tile + row * 128 + unit * 16) =
+                  make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
             }
           }
         }
@@ -694,8 +723,6 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       tc_fence_after();
       store_item(true, p_row, p_bi, p_head);
     }
-    // the tile stores must be complete (and done with sDs) before exit
-    if (A.ds_tiles && threadIdx.x == 128) bulk_wait_all();
   }
 
   tc_fence_before();
