@@ -21,20 +21,22 @@
 namespace mc {
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotMaxTable = 4096;  // (token, pair) entries of a block's cos / sin table (32 KB)
-constexpr int kRotMaxTokens = 32;   // tokens of a block
+constexpr int kRotWarps = 4;
+constexpr int kRotTurns = 8;    // turns of an item
+constexpr int kRotTable = 512;  // (token, pair) entries of a warp's cos / sin table (4 KB)
 
 struct RotaryArgs {
   int64_t tokens, ld_in, ld_out;
+  int64_t items;    // (token group, unit range) pairs, one warp each
   int heads, head_dim, pairs;
-  uint32_t div_nu, div_units_head, div_pairs;  // 2^32 / d rounded up, for divisions (fast_div)
-  int units;        // work units per token: heads * units_head
-  int units_head;   // pairs / VEC rotating units, then the vectors that are copied
-  int tok_block;    // tokens per block
-  int unit_block;   // units of each of them per block
+  int units;        // work units per token: the rotating ones of all heads, then the copied
+  int rot_units;    // rotating units of a head
+  int copy_units;   // copied vectors of a head
+  int tok_item;     // tokens of an item
+  int unit_item;    // units of each of them
+  int ranges;       // unit ranges per token
   int inverse;
-  int copy_rest;    // out of place: the unrotated dimensions are copied
+  uint32_t div_unit_item, div_rot, div_copy, div_pairs;  // 2^32 / d rounded up (fast_div)
   uint8_t axis[kRotaryMaxPairs];
 };
 
@@ -94,155 +96,174 @@ __device__ __forceinline__ uint64_t turns_fixed(float f) {
   return bits >> 31 ? 0 - r : r;
 }
 
-// A unit is VEC pairs of one head (two vectors of VEC elements: the halves of
-// the pairs, or 2 VEC adjacent elements) or one copied vector.  A block takes
-// unit_block units of each of tok_block tokens, up to UPT per thread; their
-// loads are issued before the cos / sin table is formed, so one DRAM round
-// trip covers both.
-template <typename T, int VEC, bool ADJACENT, int UPT>
-__global__ void __launch_bounds__(kRotThreads, UPT > 1 ? 3 : 4)
+// A unit is a vector of VEC / 2 adjacent pairs, or two vectors of VEC pairs'
+// halves (VEC = 1: always two), or one copied vector.  A warp takes items of
+// unit_item units of each of tok_item tokens, one per lane and turn.  The first
+// turn's loads are issued before the item's cos / sin table is formed, so one
+// DRAM round trip covers both; the turns per position of every pair are formed
+// once per block.  What keeps the loads coming is the number of warps: two
+// units per lane and turn, or the next turn's loads ahead of this one's work,
+// cost registers and were slower (60 and 64 us against 52 us over 4096 tokens
+// of 128 heads of 128).
+template <typename T, int VEC, bool ADJACENT>
+__global__ void __launch_bounds__(kRotWarps * 32)
     rotary_kernel(const T* in, T* out, const int32_t* __restrict__ positions,
                   const float* __restrict__ inv_freq, const __grid_constant__ RotaryArgs A,
                   int* status) {
   using V = RotVec<T, VEC>;
-  // cos and sin, [tok_block][pairs] each
-  extern __shared__ __align__(16) float table[];
-  float* const t_cos = table;
-  float* const t_sin = table + A.tok_block * A.pairs;
+  using F = RotVec<float, (ADJACENT && VEC > 1) ? VEC / 2 : VEC>;
+  __shared__ uint64_t turns[kRotaryMaxPairs];
+  __shared__ __align__(16) float table[kRotWarps][2][kRotTable];
   pdl_wait();  // the previous kernel on the stream has completed
   pdl_launch();
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * A.tok_block;
-  const int ntok = static_cast<int>(min(static_cast<int64_t>(A.tok_block), A.tokens - t0));
-  const int u0 = static_cast<int>(blockIdx.y) * A.unit_block;
-  const int nu = min(A.unit_block, A.units - u0);
-  const int total = ntok * nu;
-  const int rot_units = A.pairs / VEC;
-
-  V a[UPT], b[UPT];
-  int tok[UPT], pair[UPT];  // pair < 0: nothing, or a copied vector
-  int off[UPT];             // of the unit's first vector within its row
-#pragma unroll
-  for (int k = 0; k < UPT; ++k) {
-    const int e = static_cast<int>(threadIdx.x) + k * kRotThreads;
-    pair[k] = -1;
-    off[k] = -1;
-    tok[k] = 0;
-    if (e < total) {
-      const int tk = nu == A.unit_block ? fast_div(e, A.div_nu) : e / nu;
-      const int u = u0 + (e - tk * nu);
-      const int h = fast_div(u, A.div_units_head);
-      const int w = u - h * A.units_head;
-      tok[k] = tk;
-      const T* row = in + (t0 + tk) * A.ld_in;
-      const int base = h * A.head_dim;
-      if (w < rot_units) {
-        pair[k] = w * VEC;
-        off[k] = base + (ADJACENT ? 2 * w * VEC : w * VEC);
-        a[k] = *reinterpret_cast<const V*>(row + off[k]);
-        b[k] = *reinterpret_cast<const V*>(row + off[k] + (ADJACENT ? VEC : A.pairs));
-      } else if (A.copy_rest) {
-        off[k] = base + 2 * A.pairs + (w - rot_units) * VEC;
-        a[k] = *reinterpret_cast<const V*>(row + off[k]);
-      }
-    }
-  }
-
-  for (int i = threadIdx.x; i < ntok * A.pairs; i += kRotThreads) {
-    const int tk = fast_div(i, A.div_pairs), p = i - tk * A.pairs;
-    const uint64_t f = turns_fixed(inv_freq[p]);
-    const int64_t pos = positions[A.axis[p] * A.tokens + t0 + tk];
-    const uint64_t w = static_cast<uint64_t>(A.inverse ? -pos : pos) * f;
-    const float x = static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>((w + 0x80000000ull) >> 32)));
-    float s, c;
-    sincospif(x * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-    t_cos[i] = c;
-    t_sin[i] = s;
-  }
+  for (int p = threadIdx.x; p < A.pairs; p += kRotWarps * 32) turns[p] = turns_fixed(inv_freq[p]);
   __syncthreads();
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  float* const t_cos = table[warp][0];
+  float* const t_sin = table[warp][1];
+  constexpr bool kTwo = !ADJACENT || VEC == 1;           // a unit has two vectors
+  constexpr int kPairs = kTwo ? VEC : VEC / 2;           // and that many pairs
+  const int second = ADJACENT ? 1 : A.pairs;             // from its first vector to its second
+  const int rotating = A.heads * A.rot_units;            // units before the copied ones
 
-  int held = -1;  // the table place whose VEC entries are in cs / sn
-  RotVec<float, VEC> cs, sn;
-#pragma unroll
-  for (int k = 0; k < UPT; ++k) {
-    if (off[k] < 0) continue;
-    T* row = out + (t0 + tok[k]) * A.ld_out;
-    const int rest = pair[k] >= 0 ? (ADJACENT ? VEC : A.pairs) : 0;
-    if (!MC_DCHECK(t0 + tok[k] < A.tokens &&
-                       off[k] + rest + VEC <= A.heads * A.head_dim,
-                   status, kSiteRotary))
-      continue;
-    if (pair[k] >= 0) {
-      const int at = tok[k] * A.pairs + pair[k];
-      if (at != held) {
-        held = at;
-        cs = *reinterpret_cast<const RotVec<float, VEC>*>(t_cos + at);
-        sn = *reinterpret_cast<const RotVec<float, VEC>*>(t_sin + at);
-      }
-      V ya, yb;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float2 r = make_float2(cs.e[j], sn.e[j]);
-        float u, v;
-        if constexpr (ADJACENT) {  // pair j: elements 2j, 2j + 1 of a | b
-          u = to_f32(2 * j < VEC ? a[k].e[(2 * j) % VEC] : b[k].e[(2 * j) % VEC]);
-          v = to_f32(2 * j + 1 < VEC ? a[k].e[(2 * j + 1) % VEC] : b[k].e[(2 * j + 1) % VEC]);
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRotWarps + warp; item < A.items;
+       item += static_cast<int64_t>(gridDim.x) * kRotWarps) {
+    const int64_t group = item / A.ranges;
+    const int64_t t0 = group * A.tok_item;
+    const int ntok = static_cast<int>(min(static_cast<int64_t>(A.tok_item), A.tokens - t0));
+    const int u0 = static_cast<int>(item - group * A.ranges) * A.unit_item;
+    const int nu = min(A.unit_item, A.units - u0);
+    const int total = ntok * nu;
+    const T* const in0 = in + t0 * A.ld_in;
+    T* const out0 = out + t0 * A.ld_out;
+    struct Unit {
+      V a, b;
+      int tok, off, at;  // off < 0: nothing; at < 0: a copied vector
+    };
+    auto load = [&](int e) {
+      Unit x;
+      x.off = x.at = -1;
+      x.tok = 0;
+      if (e < total) {
+        const int tk = nu == A.unit_item ? fast_div(e, A.div_unit_item) : e / nu;
+        const int u = u0 + (e - tk * nu);
+        x.tok = tk;
+        const T* row = in0 + tk * A.ld_in;
+        if (u < rotating) {
+          const int h = fast_div(u, A.div_rot);
+          const int p = (u - h * A.rot_units) * kPairs;
+          x.at = tk * A.pairs + p;
+          x.off = h * A.head_dim + (ADJACENT ? 2 * p : p);
+          x.a = *reinterpret_cast<const V*>(row + x.off);
+          if constexpr (kTwo) x.b = *reinterpret_cast<const V*>(row + x.off + second);
         } else {
-          u = to_f32(a[k].e[j]);
-          v = to_f32(b[k].e[j]);
-        }
-        const T nu_ = from_f32<T>(u * r.x - v * r.y), nv_ = from_f32<T>(u * r.y + v * r.x);
-        if constexpr (ADJACENT) {
-          if (2 * j < VEC) ya.e[(2 * j) % VEC] = nu_; else yb.e[(2 * j) % VEC] = nu_;
-          if (2 * j + 1 < VEC) ya.e[(2 * j + 1) % VEC] = nv_; else yb.e[(2 * j + 1) % VEC] = nv_;
-        } else {
-          ya.e[j] = nu_;
-          yb.e[j] = nv_;
+          const int h = fast_div(u - rotating, A.div_copy);
+          x.off = h * A.head_dim + 2 * A.pairs + (u - rotating - h * A.copy_units) * VEC;
+          x.a = *reinterpret_cast<const V*>(row + x.off);
         }
       }
-      *reinterpret_cast<V*>(row + off[k]) = ya;
-      *reinterpret_cast<V*>(row + off[k] + rest) = yb;
-    } else {
-      *reinterpret_cast<V*>(row + off[k]) = a[k];
+      return x;
+    };
+    Unit cur = load(lane);
+    __syncwarp();  // the table of the item before has been read
+    for (int i = lane; i < ntok * A.pairs; i += 32) {
+      const int tk = fast_div(i, A.div_pairs), p = i - tk * A.pairs;
+      const int64_t pos = positions[A.axis[p] * A.tokens + t0 + tk];
+      const uint64_t w = static_cast<uint64_t>(A.inverse ? -pos : pos) * turns[p];
+      // the nearest 2^-32 of a turn, in half turns
+      const int32_t x = static_cast<int32_t>(static_cast<uint32_t>((w + 0x80000000ull) >> 32));
+      float s, c;
+      sincospif(static_cast<float>(x) * 4.656612873077393e-10f, &s, &c);
+      t_cos[i] = c;
+      t_sin[i] = s;
+    }
+    __syncwarp();
+    int held = -1;  // the table place whose entries are in cs / sn
+    F cs, sn;
+    for (int e = lane; e - lane < total; e += 32) {
+      T* row = out0 + cur.tok * A.ld_out;
+      if (cur.off >= 0 &&
+          MC_DCHECK(t0 + cur.tok < A.tokens &&
+                        cur.off + (kTwo && cur.at >= 0 ? second : 0) + VEC <= A.heads * A.head_dim,
+                    status, kSiteRotary)) {
+        if (cur.at >= 0) {
+          if (cur.at != held) {
+            held = cur.at;
+            cs = *reinterpret_cast<const F*>(t_cos + held);
+            sn = *reinterpret_cast<const F*>(t_sin + held);
+          }
+          V ya, yb;
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            const float u = to_f32(kTwo ? cur.a.e[j] : cur.a.e[2 * j]);
+            const float v = to_f32(kTwo ? cur.b.e[j] : cur.a.e[2 * j + 1]);
+            const T yu = from_f32<T>(u * cs.e[j] - v * sn.e[j]);
+            const T yv = from_f32<T>(u * sn.e[j] + v * cs.e[j]);
+            if constexpr (kTwo) {
+              ya.e[j] = yu;
+              yb.e[j] = yv;
+            } else {
+              ya.e[2 * j] = yu;
+              ya.e[2 * j + 1] = yv;
+            }
+          }
+          *reinterpret_cast<V*>(row + cur.off) = ya;
+          if constexpr (kTwo) *reinterpret_cast<V*>(row + cur.off + second) = yb;
+        } else {
+          *reinterpret_cast<V*>(row + cur.off) = cur.a;
+        }
+      }
+      cur = load(e + 32);
     }
   }
 }
 
-template <typename T, int VEC, bool ADJACENT, int UPT>
+template <typename T, int VEC, bool ADJACENT>
 int rotary_launch(const T* in, T* out, const int32_t* positions, const float* inv_freq,
-                  const RotaryArgs& A, int64_t gx, int64_t gy, int* status, cudaStream_t st) {
-  launch_kernel(rotary_kernel<T, VEC, ADJACENT, UPT>,
-                dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(kRotThreads),
-                2 * sizeof(float) * A.tok_block * A.pairs, st, 1, in, out, positions, inv_freq, A,
-                status);
+                  const RotaryArgs& A, int* status, cudaStream_t st) {
+  auto kern = rotary_kernel<T, VEC, ADJACENT>;
+  // at most as many blocks as are resident at once
+  static PerDeviceInit init;
+  long long resident = 0;
+  const cudaError_t e = once_per_device(init, [&](long long* value) {
+    int per_sm = 0;
+    const cudaError_t r =
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRotWarps * 32, 0);
+    *value = static_cast<long long>(per_sm < 1 ? 1 : per_sm) * num_sms();
+    return r;
+  }, &resident);
+  if (e != cudaSuccess) return MC_ERR_CUDA;
+  const int64_t blocks = (A.items + kRotWarps - 1) / kRotWarps;
+  launch_kernel(kern, dim3(static_cast<unsigned>(blocks < resident ? blocks : resident)),
+                dim3(kRotWarps * 32), 0, st, 1, in, out, positions, inv_freq, A, status);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
 
 template <typename T, int VEC, bool ADJACENT>
 int rotary_plan(const T* in, T* out, const int32_t* positions, const float* inv_freq, RotaryArgs A,
                 int* status, cudaStream_t st) {
-  const int rest = A.copy_rest ? (A.head_dim - 2 * A.pairs) / VEC : 0;
-  A.units_head = A.pairs / VEC + rest;
-  const int64_t units = static_cast<int64_t>(A.heads) * A.units_head;  // <= 2^22
+  A.rot_units = ADJACENT && VEC > 1 ? 2 * A.pairs / VEC : A.pairs / VEC;
+  A.copy_units = in != out ? (A.head_dim - 2 * A.pairs) / VEC : 0;
+  const int64_t units =
+      static_cast<int64_t>(A.heads) * (A.rot_units + A.copy_units);  // <= 2^22
   A.units = static_cast<int>(units);
-  // Four units per thread keep enough loads in flight; few units in all take
-  // one per thread, so that more SMs share the call.
-  const bool small = units * A.tokens <= 4ll * kRotThreads * num_sms();
-  const int block_units = small ? kRotThreads : 4 * kRotThreads;
-  A.unit_block = A.units < block_units ? A.units : block_units;
-  int tb = block_units / A.unit_block;
-  if (tb > kRotMaxTokens) tb = kRotMaxTokens;
-  if (tb > kRotMaxTable / A.pairs) tb = kRotMaxTable / A.pairs;
-  if (tb > A.tokens) tb = static_cast<int>(A.tokens);
-  A.tok_block = tb;
+  // Units of an item: enough that forming its table does not show, or one turn
+  // where the call is too short to fill the SMs otherwise.
+  const bool small = units * A.tokens <= 1024ll * num_sms();
+  const int item_units = small ? 32 : 32 * kRotTurns;
+  A.unit_item = A.units < item_units ? A.units : item_units;
+  int tk = item_units / A.unit_item;
+  if (tk > kRotTable / A.pairs) tk = kRotTable / A.pairs;
+  if (tk > A.tokens) tk = static_cast<int>(A.tokens);
+  A.tok_item = tk;
+  A.ranges = (A.units + A.unit_item - 1) / A.unit_item;
+  A.items = (A.tokens + tk - 1) / tk * A.ranges;
   auto magic = [](int d) { return d == 1 ? 0u : static_cast<uint32_t>((0x100000000ull + d - 1) / d); };
-  A.div_nu = magic(A.unit_block);
-  A.div_units_head = magic(A.units_head);
+  A.div_unit_item = magic(A.unit_item);
+  A.div_rot = magic(A.rot_units);
+  A.div_copy = magic(A.copy_units > 0 ? A.copy_units : 1);
   A.div_pairs = magic(A.pairs);
-  const int64_t gx = (A.tokens + tb - 1) / tb;
-  const int64_t gy = (A.units + A.unit_block - 1) / A.unit_block;
-  if (gx > 0x7fffffff) return MC_ERR_UNSUPPORTED;
-  return small ? rotary_launch<T, VEC, ADJACENT, 1>(in, out, positions, inv_freq, A, gx, gy, status, st)
-               : rotary_launch<T, VEC, ADJACENT, 4>(in, out, positions, inv_freq, A, gx, gy, status, st);
+  return rotary_launch<T, VEC, ADJACENT>(in, out, positions, inv_freq, A, status, st);
 }
 
 template <typename T>
@@ -255,7 +276,7 @@ int rotary_typed(const void* in_, void* out_, const int32_t* positions, const fl
   // addresses are whole multiples of.
   auto fits = [&](int vec) {
     const uintptr_t bytes = sizeof(T) * static_cast<uintptr_t>(vec);
-    return A.pairs % vec == 0 && A.head_dim % vec == 0 && A.ld_in % vec == 0 &&
+    return (adjacent ? 2 * A.pairs : A.pairs) % vec == 0 && A.head_dim % vec == 0 && A.ld_in % vec == 0 &&
            A.ld_out % vec == 0 && reinterpret_cast<uintptr_t>(in) % bytes == 0 &&
            reinterpret_cast<uintptr_t>(out) % bytes == 0;
   };
@@ -311,7 +332,6 @@ int launch_rotary(const void* in, void* out, bool bf16, int64_t tokens, int head
   A.head_dim = head_dim;
   A.pairs = spec->rot_dim / 2;
   A.inverse = inverse ? 1 : 0;
-  A.copy_rest = in != out ? 1 : 0;
   rotary_axes(spec, A.axis);
   const bool adjacent = (spec->flags & MC_ROTARY_ADJACENT_PAIRS) != 0;
   return bf16 ? rotary_typed<__nv_bfloat16>(in, out, positions, inv_freq, A, adjacent, status, st)
