@@ -62,14 +62,15 @@ template <int D>
 struct OptBwdCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = 128 * D * 2;
-  // K, V, three Q_i and two dO_i stages (S^T_{i+1} runs ahead of the products
-  // of block i, which read Q_i and dO_i), lse / delta [2][128], the queries'
-  // key ranges relative to the block [2][128] (two bytes each), their edge
-  // flags [2][4], items, barriers.  The dynamic shared memory starts
-  // 1024-byte aligned (checked at run time).
-  static constexpr int kQ = 3, kdO = 2;
-  static constexpr int kUsed = (2 + kQ + kdO) * kTile + 4 * 128 * 4 + 2 * 128 * 2 + 2 * 4 * 4 +
-                               kOptKvRing * static_cast<int>(sizeof(OptKvItem)) + 34 * 8;
+  // K, V, the Q_i and dO_i stages (apart, Q_i first: S^T_{i+1} runs ahead of
+  // the products of block i), the dz^T tile for its bulk store, lse / delta
+  // [2][128], the queries' key ranges relative to the block [2][128] (two
+  // bytes each), their edge flags [2][4], items, barriers.  The dynamic
+  // shared memory starts 1024-byte aligned (checked at run time).
+  static constexpr int kQ = D == 64 ? 3 : 2, kdO = 2;
+  static constexpr int kUsed = (2 + kQ + kdO) * kTile + static_cast<int>(kOptTileBytes) +
+                               4 * 128 * 4 + 2 * 128 * 2 + 2 * 4 * 4 +
+                               kOptKvRing * static_cast<int>(sizeof(OptKvItem)) + 36 * 8;
   // one CTA per SM: it takes all 512 TMEM columns
   static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
   static constexpr uint32_t kTmemCols = 512;
@@ -109,7 +110,7 @@ constexpr int kOptKvRegsIo = 72, kOptKvRegsCompute = 216;
 
 // Persistent: one CTA per SM walks the (key block, head) items, each against
 // the query blocks that see it (blocks i, counted across items).  384 threads:
-// warp 0 loads, warp 1 issues, warps 4..11 compute.
+// warp 0 loads, warp 1 issues, warp 2 stores dz^T tiles, warps 4..11 compute.
 // TMEM: S^T [0, 128), dP^T [128, 256), dV [256, 256 + D), dK [384, 384 + D).
 // Per query block i:
 //   MMA      S^T_i = K Q_i^T (as soon as the compute warps hold S^T_{i-1} in
@@ -138,7 +139,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   uint8_t* sV = smem + C::kTile;
   uint8_t* sQ = smem + 2 * C::kTile;             // [kQ]
   uint8_t* sdO = smem + (2 + C::kQ) * C::kTile;  // [kdO]
-  float* sL = reinterpret_cast<float*>(sdO + C::kdO * C::kTile);  // [2][128] lse * log2(e)
+  uint8_t* sDs = sdO + C::kdO * C::kTile;  // dz^T tile image (swizzled), 32 KB
+  float* sL = reinterpret_cast<float*>(sDs + kOptTileBytes);  // [2][128] lse * log2(e)
   float* sD = sL + 256;                                        // [2][128] delta
   OptKvItem* items = reinterpret_cast<OptKvItem*>(sD + 256);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kOptKvRing);
@@ -156,13 +158,15 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   uint64_t* p_full = bars + 17;    // P^T_i, dz^T_i in TMEM (8 warps)
   uint64_t* acc_done = bars + 18;  // dV, dK products of block i complete
   uint64_t* drain = bars + 19;
-  uint64_t* lse_ready = bars + 20;  // [2] (8 warps)
+  uint64_t* lse_ready = bars + 20;  // [2] (4 warps)
   uint64_t* it_full = bars + 22;    // [kOptKvRing]
-  uint64_t* it_empty = bars + 26;   // [kOptKvRing] read by the MMA and the compute warps (9)
+  uint64_t* it_empty = bars + 26;   // [kOptKvRing] read by MMA, tile and compute warps (10)
   uint64_t* steal_bar = bars + 30;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   void* response = bars + 32;  // 16 bytes, aligned as the items are
-  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 34);  // [2][128] first | end << 8
+  uint64_t* ds_full = bars + 34;  // the dz^T tile of block i is in sDs (8 warps)
+  uint64_t* ds_free = bars + 35;  // its bulk store has read sDs
+  uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 36);  // [2][128] first | end << 8
   int* sF = reinterpret_cast<int*>(sM + 256);             // [2][4] the 32 queries see the whole block
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -181,7 +185,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       mbar_init(&do_full[i], 1);
       mbar_init(&do_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&lse_ready[i], 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&lse_ready[i], 4);
+    mbar_init(ds_full, 8);
+    mbar_init(ds_free, 1);
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
     mbar_init(dp_full, 1);
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     mbar_init(steal_bar, 1);
     for (int i = 0; i < kOptKvRing; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 9);
+      mbar_init(&it_empty[i], 10);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_qkv);
@@ -420,6 +426,37 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
       }
       __syncwarp();
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- tile stores
+      // dz^T of a block pair goes to `ds_tiles` for the dQ product, as one bulk
+      // store of the image the compute warps assembled.
+      if (lane == 0) {
+        int g = 0;
+        bool ok = true;
+        for (int r = 0; ok; ++r) {
+          const int slot = r % kOptKvRing;
+          if (!mbar_wait(&it_full[slot], (r / kOptKvRing) & 1, status, kSiteAttention)) break;
+          const int4 e = items[slot].entry;
+          const int hh = items[slot].head;
+          mbar_arrive(&it_empty[slot]);
+          if (e.w < 0) break;
+          if (!A.ds_tiles) continue;
+          const int64_t hb = static_cast<int64_t>(e.x) * H + hh;
+          for (int i = 0; i < e.w; ++i, ++g) {
+            if (!(ok = mbar_wait(ds_full, g & 1, status, kSiteAttention))) break;
+            const int qb = e.z + i;
+            // the workspace of a causal mask has no tile above the diagonal
+            if (check_index(!A.causal || e.y <= qb, status, kSiteAttention)) {
+              bulk_store(A.ds_tiles + opt_tile(A.causal, nb, hb, qb, e.y) * kOptTileBytes, sDs,
+                         static_cast<uint32_t>(kOptTileBytes));
+              bulk_commit();
+              bulk_wait_read();
+            }
+            mbar_arrive(ds_free);
+          }
+        }
+        bulk_wait_all();  // complete before the CTA exits
+      }
     }
   } else {
     // ---------------------------------------------------------- compute
@@ -450,7 +487,10 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         q_hi = A.key_hi[brow];
       }
     };
+    bool have = false;  // loaded and not yet staged
     auto stage_query = [&](int st) {
+      have = false;
+      if (half != 0) return;
       const int first = min(max(q_lo - q_r0, 0), 128);
       const int end = min(max(min(q_hi, s) - q_r0, 0), 128);
       const int range = q_in ? first | (end << 8) : 128 << 8;
@@ -459,6 +499,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       sM[st * 128 + t] = static_cast<uint16_t>(range);
       const bool whole = __all_sync(0xffffffffu, range == (128 << 8));
       if (lane == 0) sF[st * 4 + quarter] = whole ? 1 : 0;
+      mbar_arrive_warp(&lse_ready[st], lane);
     };
     float slope = 0.f, n_slope = 0.f;
     // waits for item r's announcement and loads its first block's queries
@@ -469,7 +510,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         return;
       }
       const int4 e = items[slot].entry;
-      if (e.w > 0) {
+      have = e.w > 0;
+      if (have) {
         if (half == 0) load_query(e.x, items[slot].head, e.y * 128, e.z * 128 + t);
         if constexpr (BIAS) n_slope = A.slopes[items[slot].head];
       }
@@ -497,12 +539,13 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       }
     };
     look_ahead(0);
+    if (have) stage_query(0);
     int g = 0;
     for (int r = 0; ok; ++r) {
       const OptKvItem& it = items[r % kOptKvRing];
       const int count = it.entry.w;
       if (count < 0) break;
-      const int bi = it.entry.x, r0 = it.entry.y * 128, qb0 = it.entry.z, kb = it.entry.y;
+      const int bi = it.entry.x, r0 = it.entry.y * 128, qb0 = it.entry.z;
       const int hh = it.head;
       slope = n_slope;
       const ScoreConst sc =
@@ -512,13 +555,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         const int c0 = (qb0 + i) * 128;  // first query of this block
         const float* l2 = sL + (g & 1) * 128 + half * 64;
         const float* dl = sD + (g & 1) * 128 + half * 64;
-        if (half == 0) {
-          stage_query(g & 1);
-          if (i + 1 < count) load_query(bi, hh, r0, c0 + 128 + t);
-        }
-        if (r > 0 && i + 1 == count) look_ahead(r + 1);
-        mbar_arrive_warp(&lse_ready[g & 1], lane);
-        if (!ok || !mbar_wait_warp(&lse_ready[g & 1], (g >> 1) & 1, status, kSiteAttention) ||
+        if (!mbar_wait_warp(&lse_ready[g & 1], (g >> 1) & 1, status, kSiteAttention) ||
             !mbar_wait_warp(s_full, g & 1, status, kSiteAttention)) {
           ok = false;
           break;
@@ -530,6 +567,13 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive_warp(s_free, lane);
+        // the next block's queries: loaded here, staged behind this block's work
+        if (i + 1 < count) {
+          have = true;
+          if (half == 0) load_query(bi, hh, r0, c0 + 128 + t);
+        } else {
+          look_ahead(r + 1);
+        }
         const bool edge = (sF[(g & 1) * 4 + 2 * half] & sF[(g & 1) * 4 + 2 * half + 1]) == 0;
         // bit e of vis: this key is visible to query e of the 64
         uint32_t vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
@@ -644,22 +688,11 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           break;
         }
         tc_fence_after();
-        // dz^T of this block pair also goes to `ds_tiles` for the dQ product, as
-        // the 128-byte-swizzled shared-memory image of an MN-major A operand:
-        // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit of
-        // queries [8u, 8u + 8) at unit u ^ (t & 7).  (The workspace of a causal
-        // mask has no tile above the diagonal.)
-        uint8_t* tile = nullptr;
-        if (A.ds_tiles != nullptr && check_index(!A.causal || kb <= qb0 + i, status, kSiteAttention))
-          tile = A.ds_tiles +
-                 opt_tile(A.causal, nb, static_cast<int64_t>(bi) * H + hh, qb0 + i, kb) *
-                     kOptTileBytes +
-                 half * 16384 + quarter * 4096;
+        uint32_t z[32];  // dz of the 64 queries
 #pragma unroll
         for (int gp = 0; gp < 2; ++gp) {
           float dv[32];
           tmem_ld_32x32b_x32(tdP + my_cols + gp * 32, dv);
-          uint32_t z[16];  // dz of the 32 queries
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
             uint32_t w[16];  // [P of 16 queries | their dz]
@@ -685,30 +718,34 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
               w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[gr * 8 + e] = w[8 + e];
+            for (int e = 0; e < 8; ++e) z[gp * 16 + gr * 8 + e] = w[8 + e];
             // over this thread's own dP^T columns, already in registers
             tmem_st_32x32b_x16(tdP + my_cols + gp * 32 + gr * 16, w);
           }
-          if (gp == 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive_warp(p_full, lane);
-          }
-          if (tile) {
-            // four lanes store 64 bytes of a row
-            transpose_16b_x4(z, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = (lane & ~3) + k;
-              const int unit = (4 * gp + (lane & 3)) ^ (row & 7);
-              *reinterpret_cast<uint4*>(tile + row * 128 + unit * 16) =
-                  make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
-            }
-          }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(p_full, lane);
+        if (A.ds_tiles) {
+          // The 128-byte-swizzled shared-memory image of an MN-major A operand:
+          // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit
+          // of queries [8u, 8u + 8) at unit u ^ (t & 7); the store of the
+          // block before must have read sDs first.
+          if (g > 0 && !mbar_wait_warp(ds_free, (g - 1) & 1, status, kSiteAttention)) {
+            ok = false;
+            break;
+          }
+          uint8_t* ds_row = sDs + half * 16384 + t * 128;
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(ds_row + ((u ^ (t & 7)) << 4)) =
+                make_uint4(z[4 * u], z[4 * u + 1], z[4 * u + 2], z[4 * u + 3]);
+          fence_proxy_async_smem();  // visible to the bulk copy
+          mbar_arrive_warp(ds_full, lane);
+        }
+        if (have) stage_query((g + 1) & 1);
       }
       if (!ok) break;
-      if (r == 0 || count == 0) look_ahead(r + 1);
       if (count > 0) {
         p_row = r0;
         p_bi = bi;
@@ -716,6 +753,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         pending = true;
       } else {
         store_item(false, r0, bi, hh);
+        look_ahead(r + 1);
+        if (have) stage_query(g & 1);
       }
       mbar_arrive_warp(&it_empty[r % kOptKvRing], lane);
     }
