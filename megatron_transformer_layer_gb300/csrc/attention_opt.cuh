@@ -48,19 +48,27 @@ struct ScoreConst {
 // that far below their cap; a warp with one that is not takes the quotient form.
 constexpr float kCapSmall = 0.46875f;
 
-// p(t^2), times `scale`.
+// scale * tanh(arg x) = x (k0 + k1 x^2 + k2 x^4 + k3 x^6) for raw scores x: the
+// powers of `arg` are in the coefficients.
 struct CapPoly {
   float k0, k1, k2, k3;
 };
-__device__ __forceinline__ CapPoly cap_poly(float scale) {
-  return {0.9999985694885254f * scale, -0.3332448899745941f * scale, 0.13184478878974915f * scale,
-          -0.04449363797903061f * scale};
+__device__ __forceinline__ CapPoly cap_poly(float scale, float arg) {
+  const float a2 = arg * arg;
+  const float a1 = scale * arg, a3 = a1 * a2, a5 = a3 * a2;
+  return {0.9999985694885254f * a1, -0.3332448899745941f * a3, 0.13184478878974915f * a5,
+          -0.04449363797903061f * (a5 * a2)};
 }
-__device__ __forceinline__ float2 cap_small(float2 t, const CapPoly& c) {
-  const float2 u = __fmul2_rn(t, t);
+// The factor of x, from u = x^2.
+__device__ __forceinline__ float2 cap_small(float2 u, const CapPoly& c) {
   float2 p = __ffma2_rn(make_float2(c.k3, c.k3), u, make_float2(c.k2, c.k2));
   p = __ffma2_rn(p, u, make_float2(c.k1, c.k1));
   return __ffma2_rn(p, u, make_float2(c.k0, c.k0));
+}
+// Raw scores up to this size (absolute) are small; below caps of about 10^5
+// arg^7 is a normal number, above them none is.
+__device__ __forceinline__ float cap_small_limit(float arg) {
+  return arg > 1e-5f ? kCapSmall / arg : -1.f;
 }
 
 template <bool CAP, bool BIAS>

@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       // in uniform registers; one lane issues.
       constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+      constexpr int kLead = 6;
       const bool leader = elect_one();
       const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), 16, 1024);
@@ -339,15 +340,19 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         const uint64_t dod = smem_desc_add(dot_desc, ds * C::kTile);
         const uint32_t acc0 = pend_first ? 0u : 1u;
         if (leader) {
+          // 16 queries = group kk: P at columns 16 kk, dz at 16 kk + 8.  dK goes
+          // ahead, kLead groups of dV behind, so that Q_i is released for the
+          // load of Q_{i+2} before dV is done.
 #pragma unroll
-          for (int kk = 0; kk < 128 / 16; ++kk) {
-            // 16 queries = group kk: P at 16 kk, dz at 16 kk + 8
-            const uint32_t pcol = static_cast<uint32_t>(kk * 16);
-            const uint32_t acc = kk > 0 ? 1u : acc0;
-            umma_bf16_ts(tdV, tdP + pcol, smem_desc_add(dod, kk * 2048), kIdescAcc, acc);
-            umma_bf16_ts(tdK, tdP + pcol + 8, smem_desc_add(qd, kk * 2048), kIdescAcc, acc);
+          for (int kk = 0; kk < 8 + kLead; ++kk) {
+            if (kk < 8)
+              umma_bf16_ts(tdK, tdP + 16 * kk + 8, smem_desc_add(qd, kk * 2048), kIdescAcc,
+                           kk > 0 ? 1u : acc0);
+            if (kk == 7) umma_commit(&q_empty[qs]);
+            if (kk >= kLead)
+              umma_bf16_ts(tdV, tdP + 16 * (kk - kLead), smem_desc_add(dod, (kk - kLead) * 2048),
+                           kIdescAcc, kk > kLead ? 1u : acc0);
           }
-          umma_commit(&q_empty[qs]);
           umma_commit(&do_empty[ds]);
           umma_commit(acc_done);
         }
@@ -550,7 +555,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       slope = n_slope;
       const ScoreConst sc =
           score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
-      const CapPoly poly = cap_poly(1.f);
+      const CapPoly poly = cap_poly(1.f, sc.arg);
+      const float cap_limit = cap_small_limit(sc.arg);
+      const float cap_limit2 = cap_limit > 0.f ? cap_limit * cap_limit : -1.f;
       for (int i = 0; i < count; ++i, ++g) {
         const int c0 = (qb0 + i) * 128;  // first query of this block
         const float* l2 = sL + (g & 1) * 128 + half * 64;
@@ -565,8 +572,10 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
         tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
         tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive_warp(s_free, lane);
+        if constexpr (!CAP) {  // (a cap may need S^T once more)
+          tc_fence_before();
+          mbar_arrive_warp(s_free, lane);
+        }
         // the next block's queries: loaded here, staged behind this block's work
         if (i + 1 < count) {
           have = true;
@@ -586,34 +595,11 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           }
         }
         auto sees = [&](int e) { return ((vis[e >> 5] >> (e & 31)) & 1u) != 0; };
-        // the warp's visible scores are far enough below the cap
-        bool small = false;
-        if constexpr (CAP) {
-          float hi = -INFINITY, low = INFINITY;
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              hi = fmax3f(hi, sees(e) ? p[e] : -INFINITY, sees(e + 1) ? p[e + 1] : -INFINITY);
-              low = fmin3f(low, sees(e) ? p[e] : INFINITY, sees(e + 1) ? p[e + 1] : INFINITY);
-            }
-          } else {
-            float hi1 = -INFINITY, low1 = INFINITY;
-#pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-              hi = fmax3f(hi, p[e], p[e + 1]);
-              low = fmin3f(low, p[e], p[e + 1]);
-              hi1 = fmax3f(hi1, p[e + 2], p[e + 3]);
-              low1 = fmin3f(low1, p[e + 2], p[e + 3]);
-            }
-            hi = fmaxf(hi, hi1);
-            low = fminf(low, low1);
-          }
-          small = __all_sync(0xffffffffu, fmaxf(hi, -low) * sc.arg <= kCapSmall);
-        }
         // P (bf16 pairs in pp with a cap, else still in p), and in p what dP -
         // delta is multiplied by: P, with a cap P (1 - tanh^2).
         uint32_t pp[CAP ? 32 : 1];
         const float base = sc.slope2 * static_cast<float>(c0 + half * 64 - (r0 + t));
+        float u_max = 0.f;  // the largest square of a visible raw score
         auto weights = [&](auto edge_c, auto small_c) {
           constexpr bool EDGE = decltype(edge_c)::value;
           [[maybe_unused]] constexpr bool SMALL = decltype(small_c)::value;
@@ -633,8 +619,12 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
               [[maybe_unused]] float2 th;  // tanh
               if constexpr (CAP) {
                 if constexpr (SMALL) {
-                  const float2 arg = __fmul2_rn(x, make_float2(sc.arg, sc.arg));
-                  th = __fmul2_rn(arg, cap_small(arg, poly));
+                  const float2 u = __fmul2_rn(x, x);
+                  if constexpr (EDGE)
+                    u_max = fmax3f(u_max, sees(k) ? u.x : 0.f, sees(k + 1) ? u.y : 0.f);
+                  else
+                    u_max = fmax3f(u_max, u.x, u.y);
+                  th = __fmul2_rn(x, cap_small(u, poly));
                 } else {
                   th = __ffma2_rn(cap_r(x, sc.mul), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
                 }
@@ -658,20 +648,21 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
             }
           }
         };
+        if (edge)
+          weights(BoolC<true>{}, BoolC<true>{});
+        else
+          weights(BoolC<false>{}, BoolC<true>{});
         if constexpr (CAP) {
-          if (small) {
-            if (edge)
-              weights(BoolC<true>{}, BoolC<true>{});
-            else
-              weights(BoolC<false>{}, BoolC<true>{});
-          } else {
+          // a visible score of the warp is not far enough below the cap (what is
+          // masked must not decide how it is formed): the quotient form
+          if (!__all_sync(0xffffffffu, u_max <= cap_limit2)) {
+            tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
+            tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
+            tmem_ld_wait();
             weights(BoolC<true>{}, BoolC<false>{});
           }
-        } else {
-          if (edge)
-            weights(BoolC<true>{}, BoolC<false>{});
-          else
-            weights(BoolC<false>{}, BoolC<false>{});
+          tc_fence_before();
+          mbar_arrive_warp(s_free, lane);
         }
         if (pending) {
           if (!mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteAttention)) {

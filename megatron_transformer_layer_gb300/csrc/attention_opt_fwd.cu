@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       const int row_lo = lo, row_hi = q < s ? min(hi, s) : hi;
       const ScoreConst sc =
           score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
-      const CapPoly poly = cap_poly(sc.cap2);
+      const CapPoly poly = cap_poly(sc.cap2, sc.arg);
+      const float cap_limit = cap_small_limit(sc.arg);
       const bool early = r > 0 || halves == 0;
       if (early) fetch(r + 1);
       float m = -INFINITY, l = 0.f;
@@ -503,9 +504,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         // The visible scores of the warp's rows are far enough below the cap
         // (masked ones must not decide how the cap is formed).
         auto below_cap = [&](float high) {
-          return __all_sync(0xffffffffu, fmaxf(high, -low) * sc.arg <= kCapSmall);
+          return __all_sync(0xffffffffu, fmaxf(high, -low) <= cap_limit);
         };
-        const float2 arg2 = make_float2(sc.arg, sc.arg);
         const float2 m2cap2 = make_float2(-2.f * sc.cap2, -2.f * sc.cap2);
         if constexpr (BIAS) {
           const float base = sc.slope2 * static_cast<float>(key0 - q);
@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             if (below_cap(high)) {
 #pragma unroll
               for (int i = 0; i < 64; ++i) {
-                const float2 t = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), arg2);
-                const float2 y = __fmul2_rn(t, cap_small(t, poly));
+                const float2 xi = make_float2(x[2 * i], x[2 * i + 1]);
+                const float2 y = __fmul2_rn(xi, cap_small(__fmul2_rn(xi, xi), poly));
                 x[2 * i] = y.x;
                 x[2 * i + 1] = y.y;
               }
@@ -602,8 +602,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
               y = __fadd2_rn(xi, negm2);
             } else {
               if constexpr (kForm == 2) {
-                const float2 t = __fmul2_rn(xi, arg2);
-                y = __ffma2_rn(t, cap_small(t, poly), negm2);
+                y = __ffma2_rn(xi, cap_small(__fmul2_rn(xi, xi), poly), negm2);
               } else {
                 y = __ffma2_rn(cap_r(xi, sc.mul), m2cap2, off2);
               }
