@@ -21,7 +21,6 @@
 namespace mc {
 namespace {
 
-constexpr int kOptBwdThreads = 320;  // the dQ kernel: producer, MMA, 8 compute warps
 constexpr int64_t kOptTileBytes = 128 * 128 * 2;  // one bf16 dz^T tile (128 keys x 128 queries)
 
 struct OptBwdArgs {
@@ -105,8 +104,8 @@ __device__ __forceinline__ uint32_t bit_range(int first, int end) {
 }
 
 constexpr int kOptKvThreads = 384;
-// As in the forward: 128 x 72 + 256 x 216 = 384 x 168.
-constexpr int kOptKvRegsIo = 72, kOptKvRegsCompute = 216;
+// As in the forward: 128 x 56 + 256 x 224 = 384 x 168.
+constexpr int kOptKvRegsIo = 56, kOptKvRegsCompute = 224;
 
 // Persistent: one CTA per SM walks the (key block, head) items, each against
 // the query blocks that see it (blocks i, counted across items).  384 threads:
@@ -596,8 +595,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         }
         auto sees = [&](int e) { return ((vis[e >> 5] >> (e & 31)) & 1u) != 0; };
         // P (bf16 pairs in pp with a cap, else still in p), and in p what dP -
-        // delta is multiplied by: P, with a cap P (1 - tanh^2).
-        uint32_t pp[CAP ? 32 : 1];
+        // delta is multiplied by: P, with a cap P (1 - tanh^2).  pp ends up with
+        // dz, pair for pair.
+        uint32_t pp[32];
         const float base = sc.slope2 * static_cast<float>(c0 + half * 64 - (r0 + t));
         float u_max = 0.f;  // the largest square of a visible raw score
         auto weights = [&](auto edge_c, auto small_c) {
@@ -679,7 +679,6 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t z[32];  // dz of the 64 queries
 #pragma unroll
         for (int gp = 0; gp < 2; ++gp) {
           float dv[32];
@@ -709,7 +708,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
               w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[gp * 16 + gr * 8 + e] = w[8 + e];
+            for (int e = 0; e < 8; ++e) pp[gp * 16 + gr * 8 + e] = w[8 + e];
             // over this thread's own dP^T columns, already in registers
             tmem_st_32x32b_x16(tdP + my_cols + gp * 32 + gr * 16, w);
           }
@@ -730,7 +729,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             *reinterpret_cast<uint4*>(ds_row + ((u ^ (t & 7)) << 4)) =
-                make_uint4(z[4 * u], z[4 * u + 1], z[4 * u + 2], z[4 * u + 3]);
+                make_uint4(pp[4 * u], pp[4 * u + 1], pp[4 * u + 2], pp[4 * u + 3]);
           fence_proxy_async_smem();  // visible to the bulk copy
           mbar_arrive_warp(ds_full, lane);
         }
@@ -781,7 +780,7 @@ struct OptDqCfg {
 // follows when dz_j is in TMEM (ds_full), and its completion (ds_free) lets
 // dz_{j+1} be written.
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kOptBwdThreads, 1)
+__global__ void __launch_bounds__(kOptKvThreads, 1)
     attn_opt_dq_kernel(const __grid_constant__ CUtensorMap tm_qkv,
                        const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ OptBwdArgs A) {
@@ -848,99 +847,103 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
   const int k_lo = max(entry.z, 0), k_hi = min(entry.w, s);
   const int count = ok_entry && k_hi > k_lo ? (k_hi - k_lo + 127) / 128 : 0;
 
-  if (warp == 0) {
-    if (lane == 0 && count > 0) {
-      // -------------------------------------------------------- producer
-      mbar_arrive_expect_tx(r_full, 2 * C::kTile);
-      for (int c = 0; c < C::kChunks; ++c) {
-        tma_load_3d(sQ + c * 16384, &tm_qkv, r_full, hh * D + c * 64, q0, bi);
-        tma_load_3d(sdO + c * 16384, &tm_do, r_full, hh * D + c * 64, q0, bi);
+  if (warp < 4) {
+    setmaxnreg_dec<kOptKvRegsIo>();
+    if (warp == 0) {
+      if (lane == 0 && count > 0) {
+        // -------------------------------------------------------- producer
+        mbar_arrive_expect_tx(r_full, 2 * C::kTile);
+        for (int c = 0; c < C::kChunks; ++c) {
+          tma_load_3d(sQ + c * 16384, &tm_qkv, r_full, hh * D + c * 64, q0, bi);
+          tma_load_3d(sdO + c * 16384, &tm_do, r_full, hh * D + c * 64, q0, bi);
+        }
+        int k_issued = 0, v_issued = 0;
+        for (int j = 0; j < count; ++j) {
+          const int ks = j % 3, kph = (j / 3) & 1, vs = j & 1, vph = (j >> 1) & 1;
+          if (!mbar_wait(&k_empty[ks], kph ^ 1u, status, kSiteAttention)) break;
+          mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(sK[ks] + c * 16384, &tm_qkv, &k_full[ks], a + hh * D + c * 64,
+                        k_lo + j * 128, bi);
+          ++k_issued;
+          if (!mbar_wait(&v_empty[vs], vph ^ 1u, status, kSiteAttention)) break;
+          mbar_arrive_expect_tx(&v_full[vs], C::kTile);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(sV[vs] + c * 16384, &tm_qkv, &v_full[vs], 2 * a + hh * D + c * 64,
+                        k_lo + j * 128, bi);
+          ++v_issued;
+        }
+        pdl_launch();  // every load of this CTA is issued
+        mbar_wait(r_full, 0, status, kSiteAttention, 200000000ull, false);
+        for (int j = k_issued - 1; j >= 0 && j >= k_issued - 3; --j)
+          mbar_wait(&k_full[j % 3], (j / 3) & 1, status, kSiteAttention, 200000000ull, false);
+        for (int j = v_issued - 1; j >= 0 && j >= v_issued - 2; --j)
+          mbar_wait(&v_full[j & 1], (j >> 1) & 1, status, kSiteAttention, 200000000ull, false);
       }
-      int k_issued = 0, v_issued = 0;
-      for (int j = 0; j < count; ++j) {
-        const int ks = j % 3, kph = (j / 3) & 1, vs = j & 1, vph = (j >> 1) & 1;
-        if (!mbar_wait(&k_empty[ks], kph ^ 1u, status, kSiteAttention)) break;
-        mbar_arrive_expect_tx(&k_full[ks], C::kTile);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d(sK[ks] + c * 16384, &tm_qkv, &k_full[ks], a + hh * D + c * 64,
-                      k_lo + j * 128, bi);
-        ++k_issued;
-        if (!mbar_wait(&v_empty[vs], vph ^ 1u, status, kSiteAttention)) break;
-        mbar_arrive_expect_tx(&v_full[vs], C::kTile);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d(sV[vs] + c * 16384, &tm_qkv, &v_full[vs], 2 * a + hh * D + c * 64,
-                      k_lo + j * 128, bi);
-        ++v_issued;
-      }
-      pdl_launch();  // every load of this CTA is issued
-      mbar_wait(r_full, 0, status, kSiteAttention, 200000000ull, false);
-      for (int j = k_issued - 1; j >= 0 && j >= k_issued - 3; --j)
-        mbar_wait(&k_full[j % 3], (j / 3) & 1, status, kSiteAttention, 200000000ull, false);
-      for (int j = v_issued - 1; j >= 0 && j >= v_issued - 2; --j)
-        mbar_wait(&v_full[j & 1], (j >> 1) & 1, status, kSiteAttention, 200000000ull, false);
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    // (converged, as in the dK/dV kernel)
-    constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
-    const bool leader = elect_one();
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t do_desc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
-    const uint64_t k_desc = smem_desc_sw128(smem_u32(sK[0]), 16, 1024);
-    const uint64_t kt_desc = smem_desc_sw128(smem_u32(sK[0]), 16384, 1024);
-    const uint64_t v_desc = smem_desc_sw128(smem_u32(sV[0]), 16, 1024);
-    bool ok = count > 0 && mbar_wait_warp(r_full, 0, status, kSiteAttention);
-    for (int j = 0; ok && j <= count; ++j) {
-      if (j < count) {
-        const int ks = j % 3, vs = j & 1;
-        if (!mbar_wait_warp(&k_full[ks], (j / 3) & 1, status, kSiteAttention)) break;
-        if (!mbar_wait_warp(&v_full[vs], (j >> 1) & 1, status, kSiteAttention)) break;
-        // S / dP of block j - 1 are in the compute warps' registers.
-        if (j > 0 && !mbar_wait_warp(s_free, (j - 1) & 1, status, kSiteAttention)) break;
-        tc_fence_after();
-        const uint64_t kd = smem_desc_add(k_desc, ks * C::kTile);
-        const uint64_t vd = smem_desc_add(v_desc, vs * C::kTile);
-        if (leader) {
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      // (converged, as in the dK/dV kernel)
+      constexpr uint32_t kIdescSq = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, false, true);
+      const bool leader = elect_one();
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t do_desc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sK[0]), 16, 1024);
+      const uint64_t kt_desc = smem_desc_sw128(smem_u32(sK[0]), 16384, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sV[0]), 16, 1024);
+      bool ok = count > 0 && mbar_wait_warp(r_full, 0, status, kSiteAttention);
+      for (int j = 0; ok && j <= count; ++j) {
+        if (j < count) {
+          const int ks = j % 3, vs = j & 1;
+          if (!mbar_wait_warp(&k_full[ks], (j / 3) & 1, status, kSiteAttention)) break;
+          if (!mbar_wait_warp(&v_full[vs], (j >> 1) & 1, status, kSiteAttention)) break;
+          // S / dP of block j - 1 are in the compute warps' registers.
+          if (j > 0 && !mbar_wait_warp(s_free, (j - 1) & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint64_t kd = smem_desc_add(k_desc, ks * C::kTile);
+          const uint64_t vd = smem_desc_add(v_desc, vs * C::kTile);
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tS, smem_desc_add(q_desc, off), smem_desc_add(kd, off), kIdescSq,
-                      kk > 0 ? 1u : 0u);
-            umma_bf16(tdP, smem_desc_add(do_desc, off), smem_desc_add(vd, off), kIdescSq,
-                      kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              umma_bf16(tS, smem_desc_add(q_desc, off), smem_desc_add(kd, off), kIdescSq,
+                        kk > 0 ? 1u : 0u);
+              umma_bf16(tdP, smem_desc_add(do_desc, off), smem_desc_add(vd, off), kIdescSq,
+                        kk > 0 ? 1u : 0u);
+            }
+            umma_commit(s_full);
+            umma_commit(&v_empty[vs]);  // V_j is done once dP_j is
           }
-          umma_commit(s_full);
-          umma_commit(&v_empty[vs]);  // V_j is done once dP_j is
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (j > 0) {
-        const int pj = j - 1, pks = pj % 3;
-        if (!mbar_wait_warp(ds_full, pj & 1, status, kSiteAttention)) break;
-        tc_fence_after();
-        const uint64_t kd = smem_desc_add(kt_desc, pks * C::kTile);
-        const uint32_t acc0 = pj > 0 ? 1u : 0u;
-        if (leader) {
+        if (j > 0) {
+          const int pj = j - 1, pks = pj % 3;
+          if (!mbar_wait_warp(ds_full, pj & 1, status, kSiteAttention)) break;
+          tc_fence_after();
+          const uint64_t kd = smem_desc_add(kt_desc, pks * C::kTile);
+          const uint32_t acc0 = pj > 0 ? 1u : 0u;
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 128 / 16; ++kk)
-            umma_bf16_ts(tdQ, tdS + kk * 8, smem_desc_add(kd, kk * 2048), kIdescAcc,
-                         kk > 0 ? 1u : acc0);
-          umma_commit(&k_empty[pks]);
-          umma_commit(ds_free);
+            for (int kk = 0; kk < 128 / 16; ++kk)
+              umma_bf16_ts(tdQ, tdS + kk * 8, smem_desc_add(kd, kk * 2048), kIdescAcc,
+                           kk > 0 ? 1u : acc0);
+            umma_commit(&k_empty[pks]);
+            umma_commit(ds_free);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
+      if (leader) {
+        umma_commit(drain);
+        mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
+      }
+      __syncwarp();
     }
-    if (leader) {
-      umma_commit(drain);
-      mbar_wait(drain, 0, status, kSiteAttention, 200000000ull, false);
-    }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- compute
+    setmaxnreg_inc<kOptKvRegsCompute>();
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;   // 64 of the block's 128 key columns
+    const int half = (warp - 4) >> 2;   // 64 of the block's 128 key columns
     const int r = q0 + quarter * 32 + lane;  // this thread's query row
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const ScoreConst sc =
@@ -954,7 +957,9 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
       lo = A.key_lo[static_cast<int64_t>(bi) * s + r];
       hi = min(A.key_hi[static_cast<int64_t>(bi) * s + r], s);
     }
-    const float add0 = (CAP ? sc.cap2 : 0.f) - my_l2;
+    const CapPoly poly = cap_poly(1.f, sc.arg);
+    const float cap_limit = cap_small_limit(sc.arg);
+    const float cap_limit2 = cap_limit > 0.f ? cap_limit * cap_limit : -1.f;
     bool ok = true;
     for (int j = 0; j < count; ++j) {
       if (!mbar_wait_warp(s_full, j & 1, status, kSiteAttention)) {
@@ -963,47 +968,73 @@ __global__ void __launch_bounds__(kOptBwdThreads, 1)
       }
       tc_fence_after();
       float sv[64], dv[64];
-      tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 64, sv);
-      tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 64 + 32, sv + 32);
-      tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64, dv);
-      tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64 + 32, dv + 32);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive_warp(s_free, lane);
+      auto load = [&]() {
+        tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 64, sv);
+        tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 64 + 32, sv + 32);
+        tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64, dv);
+        tmem_ld_32x32b_x32_nowait(tdP + lane_off + half * 64 + 32, dv + 32);
+        tmem_ld_wait();
+      };
+      load();
+      if constexpr (!CAP) {  // (a cap may need S and dP once more)
+        tc_fence_before();
+        mbar_arrive_warp(s_free, lane);
+      }
       const int c0 = k_lo + j * 128 + half * 64;
       const bool edge = __any_sync(0xffffffffu, lo > c0 || hi < c0 + 64);
       const int first = lo - c0, end = hi - c0;
       uint32_t dw[32];
       const float2 nd2 = make_float2(-my_d, -my_d);
-      const float base = static_cast<float>(c0 - r);
+      const float base = sc.slope2 * static_cast<float>(c0 - r);
+      float u_max = 0.f;  // the largest square of a visible raw score
+      auto gradients = [&](auto edge_c, auto small_c) {
+        constexpr bool EDGE = decltype(edge_c)::value;
+        [[maybe_unused]] constexpr bool SMALL = decltype(small_c)::value;
 #pragma unroll
-      for (int e = 0; e < 64; e += 2) {
-        float2 add = make_float2(add0, add0);
-        if constexpr (BIAS) {
-          add.x = fmaf(-sc.slope2, fabsf(base + e), add.x);
-          add.y = fmaf(-sc.slope2, fabsf(base + (e + 1)), add.y);
-        }
-        const float2 x = make_float2(sv[e], sv[e + 1]);
-        float2 y;
-        [[maybe_unused]] float2 rr;
-        if constexpr (CAP) {
-          rr = cap_r(x, sc.mul);
-          y = __ffma2_rn(rr, make_float2(-2.f * sc.cap2, -2.f * sc.cap2), add);
-        } else {
-          y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
-        }
-        float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-        if (edge) {
-          const bool v0 = e >= first && e < end, v1 = e + 1 >= first && e + 1 < end;
+        for (int e = 0; e < 64; e += 2) {
+          float2 add = make_float2(-my_l2, -my_l2);
+          if constexpr (BIAS) {
+            add.x -= fabsf(fmaf(sc.slope2, static_cast<float>(e), base));
+            add.y -= fabsf(fmaf(sc.slope2, static_cast<float>(e + 1), base));
+          }
+          const float2 x = make_float2(sv[e], sv[e + 1]);
+          const bool v0 = !EDGE || (e >= first && e < end);
+          const bool v1 = !EDGE || (e + 1 >= first && e + 1 < end);
+          float2 y;
+          [[maybe_unused]] float2 th;
+          if constexpr (CAP) {
+            if constexpr (SMALL) {
+              const float2 u = __fmul2_rn(x, x);
+              u_max = fmax3f(u_max, v0 ? u.x : 0.f, v1 ? u.y : 0.f);
+              th = __fmul2_rn(x, cap_small(u, poly));
+            } else {
+              th = __ffma2_rn(cap_r(x, sc.mul), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
+            }
+            th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
+            y = __ffma2_rn(th, make_float2(sc.cap2, sc.cap2), add);
+          } else {
+            y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
+          }
+          float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
           pv = make_float2(v0 ? pv.x : 0.f, v1 ? pv.y : 0.f);
-          if constexpr (CAP) rr = make_float2(v0 ? rr.x : 0.f, v1 ? rr.y : 0.f);
+          if constexpr (CAP)
+            pv = __fmul2_rn(pv, __ffma2_rn(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f)));
+          const float2 ds = __fmul2_rn(pv, __fadd2_rn(make_float2(dv[e], dv[e + 1]), nd2));
+          dw[e / 2] = pack_bf16x2(ds.x, ds.y);
         }
-        if constexpr (CAP) {
-          const float2 r4 = __fmul2_rn(rr, make_float2(4.f, 4.f));
-          pv = __fmul2_rn(pv, __ffma2_rn(make_float2(-r4.x, -r4.y), rr, r4));
+      };
+      if (edge)
+        gradients(BoolC<true>{}, BoolC<true>{});
+      else
+        gradients(BoolC<false>{}, BoolC<true>{});
+      if constexpr (CAP) {
+        // as in the dK/dV kernel: the quotient form where a score needs it
+        if (!__all_sync(0xffffffffu, u_max <= cap_limit2)) {
+          load();
+          gradients(BoolC<true>{}, BoolC<false>{});
         }
-        const float2 ds = __fmul2_rn(pv, __fadd2_rn(make_float2(dv[e], dv[e + 1]), nd2));
-        dw[e / 2] = pack_bf16x2(ds.x, ds.y);
+        tc_fence_before();
+        mbar_arrive_warp(s_free, lane);
       }
       // dz_{j-1} must have been consumed by its dQ product.
       if (j > 0 && !mbar_wait_warp(ds_free, (j - 1) & 1, status, kSiteAttention)) {
@@ -1291,7 +1322,7 @@ int launch_bwd(const CUtensorMap& tq, const CUtensorMap& td, const OptBwdArgs& A
   if (A.ds_tiles) return MC_OK;
   auto kq = attn_opt_dq_kernel<D, CAP, BIAS>;
   if (opt_smem(init_q, kq, OptDqCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
-  launch_kernel(kq, opt_dq_grid(A), dim3(kOptBwdThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
+  launch_kernel(kq, opt_dq_grid(A), dim3(kOptKvThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
 
