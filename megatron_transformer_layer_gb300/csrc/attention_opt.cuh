@@ -192,6 +192,15 @@ struct OptItems {
   }
 };
 
+// Bits [first, end) of a word.
+__device__ __forceinline__ uint32_t bit_range(int first, int end) {
+  first = min(max(first, 0), 32);
+  end = min(max(end, 0), 32);
+  const uint32_t below_end = end == 32 ? 0xFFFFFFFFu : (1u << end) - 1u;
+  const uint32_t below_first = first == 32 ? 0xFFFFFFFFu : (1u << first) - 1u;
+  return below_end & ~below_first;
+}
+
 // A table entry that is not one of this shape is reported and taken as an
 // empty one of block 0.
 __device__ __forceinline__ int4 opt_checked(int4 e, int b, int nb, int* status) {

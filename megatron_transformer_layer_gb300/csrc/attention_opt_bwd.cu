@@ -94,15 +94,6 @@ __device__ __forceinline__ uint32_t bit_transpose(uint32_t x, int lane) {
   return x;
 }
 
-// Bits [first, end) of a word.
-__device__ __forceinline__ uint32_t bit_range(int first, int end) {
-  first = min(max(first, 0), 32);
-  end = min(max(end, 0), 32);
-  const uint32_t below_end = end == 32 ? 0xFFFFFFFFu : (1u << end) - 1u;
-  const uint32_t below_first = first == 32 ? 0xFFFFFFFFu : (1u << first) - 1u;
-  return below_end & ~below_first;
-}
-
 constexpr int kOptKvThreads = 384;
 // As in the forward: 128 x 56 + 256 x 224 = 384 x 168.
 constexpr int kOptKvRegsIo = 56, kOptKvRegsCompute = 224;
@@ -982,7 +973,12 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       }
       const int c0 = k_lo + j * 128 + half * 64;
       const bool edge = __any_sync(0xffffffffu, lo > c0 || hi < c0 + 64);
-      const int first = lo - c0, end = hi - c0;
+      // bit e of vis: this query sees key e of the 64
+      uint32_t vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (edge) {
+        vis[0] = bit_range(lo - c0, hi - c0);
+        vis[1] = bit_range(lo - c0 - 32, hi - c0 - 32);
+      }
       uint32_t dw[32];
       const float2 nd2 = make_float2(-my_d, -my_d);
       const float base = sc.slope2 * static_cast<float>(c0 - r);
@@ -998,8 +994,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
             add.y -= fabsf(fmaf(sc.slope2, static_cast<float>(e + 1), base));
           }
           const float2 x = make_float2(sv[e], sv[e + 1]);
-          const bool v0 = !EDGE || (e >= first && e < end);
-          const bool v1 = !EDGE || (e + 1 >= first && e + 1 < end);
+          const bool v0 = !EDGE || ((vis[e >> 5] >> (e & 31)) & 1u);
+          const bool v1 = !EDGE || ((vis[e >> 5] >> ((e + 1) & 31)) & 1u);
           float2 y;
           [[maybe_unused]] float2 th;
           if constexpr (CAP) {
@@ -1163,6 +1159,7 @@ __global__ void __launch_bounds__(192, 1)
         int rank = 0;
         if (steal.more) {
           opt_item(steal.k, A.b * nb, H, A.head_group, rank, h_next);
+          h_next = H - 1 - h_next;  // the heads whose tiles were written last are still in L2
           e_next = *reinterpret_cast<const int4*>(A.tables + 4ll * rank);
         }
       };

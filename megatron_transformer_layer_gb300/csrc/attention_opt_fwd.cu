@@ -477,9 +477,14 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         //      its second half, whose S is an older one)
         const int first = row_lo - key0;
         const int end = 2 * j + half < halves ? row_hi - key0 : 0;
-        const bool cut_end = __any_sync(0xffffffffu, end < 128);
-        const bool cut_first = __any_sync(0xffffffffu, first > 0);
-        const bool cut = cut_end || cut_first;
+        const bool cut = __any_sync(0xffffffffu, end < 128 || first > 0);
+        // bit i of vis: key i is visible
+        uint32_t vis[4] = {};
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) vis[c] = bit_range(first - 32 * c, end - 32 * c);
+        }
+        auto sees = [&](int i) { return ((vis[i >> 5] >> (i & 31)) & 1u) != 0; };
         // With a bias the scores are formed here, in log2 units.  Without one
         // they stay raw until the exponent: the scale is positive and the cap
         // monotone, so the raw maximum gives the row's.
@@ -489,8 +494,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           if (cut) {
 #pragma unroll
             for (int i = 0; i < 128; i += 2) {
-              low = fminf(low, i >= first && i < end ? x[i] : INFINITY);
-              lo1 = fminf(lo1, i + 1 >= first && i + 1 < end ? x[i + 1] : INFINITY);
+              low = fminf(low, sees(i) ? x[i] : INFINITY);
+              lo1 = fminf(lo1, sees(i + 1) ? x[i + 1] : INFINITY);
             }
           } else {
 #pragma unroll
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             if (cut) {
 #pragma unroll
               for (int i = 0; i < 128; ++i)
-                high = fmaxf(high, i >= first && i < end ? x[i] : -INFINITY);
+                high = fmaxf(high, sees(i) ? x[i] : -INFINITY);
             } else {
 #pragma unroll
               for (int i = 0; i < 128; i += 2) high = fmax3f(high, x[i], x[i + 1]);
@@ -543,13 +548,9 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             x[i] = z - fabsf(fmaf(sc.slope2, static_cast<float>(i), base));
           }
         }
-        if (cut_end) {
+        if (cut) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i < end ? x[i] : -INFINITY;
-        }
-        if (cut_first) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i >= first ? x[i] : -INFINITY;
+          for (int i = 0; i < 128; ++i) x[i] = sees(i) ? x[i] : -INFINITY;
         }
         // ---- row maximum: four chains of three-input maxima, then a tree
         float mc[4] = {x[0], x[1], x[2], x[3]};
@@ -609,8 +610,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             }
             float2 pv = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             if constexpr (CUT)  // (the cap of -infinity is not -infinity)
-              pv = make_float2(2 * i >= first && 2 * i < end ? pv.x : 0.f,
-                               2 * i + 1 >= first && 2 * i + 1 < end ? pv.y : 0.f);
+              pv = make_float2(sees(2 * i) ? pv.x : 0.f, sees(2 * i + 1) ? pv.y : 0.f);
             sm2[i & 3] = __fadd2_rn(sm2[i & 3], pv);
             x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));
           }
@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             else
               exponentials(IntC<2>{}, BoolC<false>{});
           } else {
+            if (!cut) vis[0] = vis[1] = vis[2] = vis[3] = 0xFFFFFFFFu;
             exponentials(IntC<3>{}, BoolC<true>{});
           }
         } else {
