@@ -268,6 +268,12 @@ __device__ __forceinline__ uint32_t mapa_shared(const void* p, uint32_t rank) {
   return r;
 }
 
+// An 8-byte store to a shared::cluster address.
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, int2 v) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y)
+               : "memory");
+}
+
 // Arrive on an mbarrier given by its shared::cluster address (this CTA's or
 // another CTA's of the cluster).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {

@@ -8,6 +8,7 @@ where a result is stored.
 """
 from __future__ import annotations
 
+import bisect
 import math
 
 import numpy as np
@@ -71,10 +72,9 @@ def document_intervals(offsets, prefix, causal, window, b, s):
     for bi in range(b):
         for i in range(s):
             t = bi * s + i
-            owner = [k for k in range(n) if offsets[k] <= t < offsets[k + 1]]
-            if not owner:
+            k = bisect.bisect_right(offsets, t) - 1  # the last document that starts at or before t
+            if not 0 <= k < n:
                 continue
-            k = owner[0]
             pre = prefix[k] if prefix is not None else 0
             if pre < 0:
                 continue

@@ -163,6 +163,21 @@ def test_mask_tables_of_many_blocks():
     assert k[0] == (0, 0, 0, nb) and k[nb + 3] == (1, 3, 3, nb)
 
 
+@pytest.mark.parametrize("b,s,docs", [(7, 5000, 9000), (1, 40000, 33), (300, 257, 1500)])
+def test_mask_tables_over_several_turns(b, s, docs):
+    """More blocks than a cluster forms at once, and searches of several rounds."""
+    g = torch.Generator().manual_seed(docs)
+    cuts = torch.randint(0, b * s - 4, (docs - 1,), generator=g).sort().values.tolist()
+    off = [0] + cuts + [b * s - 5]
+    pre = torch.randint(-1, 40, (docs,), generator=g).tolist()
+    lo, hi, tab = make_documents(off, pre, True, 900, b, s)
+    rlo, rhi = O.document_intervals(off, pre, True, 900, b, s)
+    assert lo.cpu().tolist() == rlo.tolist() and hi.cpu().tolist() == rhi.tolist()
+    q, k = table_lists(tab)
+    rq, rk = O.tables(rlo, rhi)
+    assert q == rq and k == rk
+
+
 # ------------------------------------------------------------------ attention
 def random_intervals(b, s, seed):
     """Intervals with no order, some empty, some past the sequence's ends."""
