@@ -553,8 +553,8 @@ int mc_attention_mask_intervals(int32_t micro_batch, int32_t seq_len, const int3
 /* What mc_attention_forward_opt / _backward_opt compute beyond plain causal
  * attention.  With z = q k / sqrt(d):
  *   softcap > 0:     z <- softcap * tanh(z / softcap)
- *   slopes != NULL:  z <- z - slopes[head] * |query - key| (fp32 [heads];
- *                    constants: they get no gradient)
+ *   slopes != NULL:  z <- z - slopes[head] * |query - key| (fp32 [heads], of
+ *                    either sign; constants: they get no gradient)
  * then the softmax over the keys of the query's interval.  causal != 0 states
  * that no interval reaches past its own query (key_hi[i] <= i + 1), which
  * halves the backward's workspace; an interval that does is then reported as
@@ -564,15 +564,16 @@ typedef struct mc_attention_options {
   const int32_t* key_hi;
   const int32_t* tables; /* made from key_lo / key_hi for the same shape */
   const float* slopes;   /* or NULL */
-  float softcap;         /* 0: none */
+  float softcap;         /* 0: none; else 2^-16 .. 2^16 */
   int32_t causal;
 } mc_attention_options;
 
 /* mc_attention_forward over an interval mask: same layouts, types and errors
  * (lse is -infinity for a row that sees nothing).  MC_ERR_ARGUMENT for a
- * negative or non-finite softcap.  Values in rows that a query does not see
- * have no influence as long as they are finite: a NaN or infinity in K or V
- * can reach the other queries of blocks that hold it. */
+ * softcap that is neither 0 nor in its range.  Values in rows that a query
+ * does not see have no influence as long as they are finite: a NaN or infinity
+ * in K or V can reach the other queries of blocks that hold it, and in the
+ * backward pass one in Q or dO the other keys. */
 int mc_attention_forward_opt(const uint16_t* qkv, uint16_t* o, float* lse, int32_t micro_batch,
                              int32_t seq_len, int32_t heads, int32_t head_dim,
                              const mc_attention_options* options, int* status, void* stream);

@@ -3,8 +3,6 @@
 // attention_opt_bwd.cu; the delta = rowsum(dO O) pre-pass is attention.cu's.
 #include <cuda_runtime.h>
 
-#include <cmath>
-
 #include "mc_layer_internal.h"
 
 namespace mc {
@@ -38,7 +36,9 @@ int check_attention_options(const mc_attention_options* opt) {
   if (!aligned(opt->key_lo, 4) || !aligned(opt->key_hi, 4) || !aligned(opt->tables, 16) ||
       !aligned(opt->slopes, 4))
     return MC_ERR_ALIGN;
-  if (!std::isfinite(opt->softcap) || opt->softcap < 0.f) return MC_ERR_ARGUMENT;
+  // (the range in which the cap's forms hold in 32 bits)
+  if (!(opt->softcap == 0.f || (opt->softcap >= 0x1p-16f && opt->softcap <= 0x1p16f)))
+    return MC_ERR_ARGUMENT;
   return MC_OK;
 }
 

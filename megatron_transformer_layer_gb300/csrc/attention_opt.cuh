@@ -65,11 +65,10 @@ __device__ __forceinline__ float2 cap_small(float2 u, const CapPoly& c) {
   p = __ffma2_rn(p, u, make_float2(c.k1, c.k1));
   return __ffma2_rn(p, u, make_float2(c.k0, c.k0));
 }
-// Raw scores up to this size (absolute) are small; below caps of about 10^5
-// arg^7 is a normal number, above them none is.
-__device__ __forceinline__ float cap_small_limit(float arg) {
-  return arg > 1e-5f ? kCapSmall / arg : -1.f;
-}
+// Raw scores up to this size (absolute) are small.  Caps are 2^-16 .. 2^16
+// (checked at the entry points): 1 / (sqrt(d) c) is 1.3e-6 .. 8192, so that the
+// coefficients, log2(e) / sqrt(d) times up to its sixth power, are normal.
+__device__ __forceinline__ float cap_small_limit(float arg) { return kCapSmall / arg; }
 
 template <bool CAP, bool BIAS>
 __device__ __forceinline__ ScoreConst score_const(float rsqrt_d, float softcap, float slope) {
@@ -93,6 +92,44 @@ __device__ __forceinline__ float2 cap_r(float2 x, float mul) {
   const float2 t = __fmul2_rn(x, make_float2(mul, mul));
   const float2 e = __fadd2_rn(make_float2(fast_exp2(t.x), fast_exp2(t.y)), make_float2(1.f, 1.f));
   return make_float2(fast_rcp(e.x), fast_rcp(e.y));
+}
+
+// x[i] <- x[i] mul - slope2 |d0 + i|, i < N, d0 an integer.  `side` > 0: no
+// d0 + i of the warp is negative, < 0: none is positive (all blocks but those
+// on the diagonal), so that the distance needs no absolute value and two scores
+// share an instruction: the distances of 8 scores relative to their first are
+// formed once.
+template <int N>
+__device__ __forceinline__ void bias_scores(float* x, float mul, float slope2, float d0, int side) {
+  const float2 mul2 = make_float2(mul, mul);
+  if (side != 0) {
+    const float s2 = side > 0 ? -slope2 : slope2;
+    const float base = s2 * d0;
+    float2 off[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) off[k] = make_float2(s2 * (2 * k), s2 * (2 * k + 1));
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      const float b = fmaf(s2, static_cast<float>(i), base);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float* xi = x + i + 2 * k;
+        const float2 y = __ffma2_rn(make_float2(xi[0], xi[1]), mul2,
+                                    __fadd2_rn(off[k], make_float2(b, b)));
+        xi[0] = y.x;
+        xi[1] = y.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      x[i] = fmaf(x[i], mul, -slope2 * fabsf(d0 + static_cast<float>(i)));
+  }
+}
+
+// The `side` of bias_scores for rows [a, a + na) minus rows [b, b + nb).
+__device__ __forceinline__ int side_of(int a, int na, int b, int nb) {
+  return a >= b + nb - 1 ? 1 : a + na - 1 <= b ? -1 : 0;
 }
 
 // The table entry of this CTA (in dispatch order) and its head: `tables` has

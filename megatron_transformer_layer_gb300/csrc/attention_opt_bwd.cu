@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
       const CapPoly poly = cap_poly(1.f, sc.arg);
       const float cap_limit = cap_small_limit(sc.arg);
-      const float cap_limit2 = cap_limit > 0.f ? cap_limit * cap_limit : -1.f;
+      const float cap_limit2 = cap_limit * cap_limit;
       for (int i = 0; i < count; ++i, ++g) {
         const int c0 = (qb0 + i) * 128;  // first query of this block
         const float* l2 = sL + (g & 1) * 128 + half * 64;
@@ -589,7 +589,11 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         // delta is multiplied by: P, with a cap P (1 - tanh^2).  pp ends up with
         // dz, pair for pair.
         uint32_t pp[32];
-        const float base = sc.slope2 * static_cast<float>(c0 + half * 64 - (r0 + t));
+        const float d0 = static_cast<float>(c0 + half * 64 - (r0 + t));  // query - key
+        // (in log2 units from here on, if there is no cap to form first)
+        if constexpr (BIAS && !CAP)
+          bias_scores<64>(p, sc.mul, sc.slope2, d0,
+                          side_of(c0 + half * 64, 64, r0 + quarter * 32, 32));
         float u_max = 0.f;  // the largest square of a visible raw score
         auto weights = [&](auto edge_c, auto small_c) {
           constexpr bool EDGE = decltype(edge_c)::value;
@@ -601,9 +605,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
             for (int h = 0; h < 2; ++h) {
               const int k = e + 2 * h;
               float2 add = h == 0 ? make_float2(-lv.x, -lv.y) : make_float2(-lv.z, -lv.w);
-              if constexpr (BIAS) {
-                add.x -= fabsf(fmaf(sc.slope2, static_cast<float>(k), base));
-                add.y -= fabsf(fmaf(sc.slope2, static_cast<float>(k + 1), base));
+              if constexpr (BIAS && CAP) {
+                add.x = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(k)), add.x);
+                add.y = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(k + 1)), add.y);
               }
               const float2 x = make_float2(p[k], p[k + 1]);
               float2 y;
@@ -620,6 +624,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
                   th = __ffma2_rn(cap_r(x, sc.mul), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
                 }
                 y = __ffma2_rn(th, make_float2(sc.cap2, sc.cap2), add);
+              } else if constexpr (BIAS) {
+                y = __fadd2_rn(x, add);
               } else {
                 y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
               }
@@ -950,7 +956,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     }
     const CapPoly poly = cap_poly(1.f, sc.arg);
     const float cap_limit = cap_small_limit(sc.arg);
-    const float cap_limit2 = cap_limit > 0.f ? cap_limit * cap_limit : -1.f;
+    const float cap_limit2 = cap_limit * cap_limit;
     bool ok = true;
     for (int j = 0; j < count; ++j) {
       if (!mbar_wait_warp(s_full, j & 1, status, kSiteAttention)) {
@@ -981,7 +987,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       }
       uint32_t dw[32];
       const float2 nd2 = make_float2(-my_d, -my_d);
-      const float base = sc.slope2 * static_cast<float>(c0 - r);
+      const float d0 = static_cast<float>(c0 - r);  // key - query
+      if constexpr (BIAS && !CAP)
+        bias_scores<64>(sv, sc.mul, sc.slope2, d0, side_of(c0, 64, q0 + quarter * 32, 32));
       float u_max = 0.f;  // the largest square of a visible raw score
       auto gradients = [&](auto edge_c, auto small_c) {
         constexpr bool EDGE = decltype(edge_c)::value;
@@ -989,9 +997,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
           float2 add = make_float2(-my_l2, -my_l2);
-          if constexpr (BIAS) {
-            add.x -= fabsf(fmaf(sc.slope2, static_cast<float>(e), base));
-            add.y -= fabsf(fmaf(sc.slope2, static_cast<float>(e + 1), base));
+          if constexpr (BIAS && CAP) {
+            add.x = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(e)), add.x);
+            add.y = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(e + 1)), add.y);
           }
           const float2 x = make_float2(sv[e], sv[e + 1]);
           const bool v0 = !EDGE || ((vis[e >> 5] >> (e & 31)) & 1u);
@@ -1008,6 +1016,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
             }
             th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
             y = __ffma2_rn(th, make_float2(sc.cap2, sc.cap2), add);
+          } else if constexpr (BIAS) {
+            y = __fadd2_rn(x, add);
           } else {
             y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
           }

@@ -513,7 +513,6 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         };
         const float2 m2cap2 = make_float2(-2.f * sc.cap2, -2.f * sc.cap2);
         if constexpr (BIAS) {
-          const float base = sc.slope2 * static_cast<float>(key0 - q);
           if constexpr (CAP) {
             float high = -INFINITY;
             if (cut) {
@@ -542,11 +541,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
               }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const float z = CAP ? x[i] : x[i] * sc.mul;
-            x[i] = z - fabsf(fmaf(sc.slope2, static_cast<float>(i), base));
-          }
+          bias_scores<128>(x, CAP ? 1.f : sc.mul, sc.slope2, static_cast<float>(key0 - q),
+                           side_of(key0, 128, q - lane, 32));
         }
         if (cut) {
 #pragma unroll

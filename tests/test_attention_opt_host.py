@@ -207,6 +207,17 @@ def test_attention_backward_refusals(change, code):
                                        a["ws_bytes"]) == code
 
 
+@pytest.mark.parametrize("cap,code", [
+    (-1.0, L.MC_ERR_ARGUMENT), (float("nan"), L.MC_ERR_ARGUMENT),
+    (float("inf"), L.MC_ERR_ARGUMENT), (1e5, L.MC_ERR_ARGUMENT), (1e-6, L.MC_ERR_ARGUMENT),
+    (2.0 ** 16, L.MC_ERR_NULLPTR), (2.0 ** -16, L.MC_ERR_NULLPTR), (0.0, L.MC_ERR_NULLPTR)])
+def test_softcap_range(cap, code):
+    """Caps in range get as far as the check of the other pointers."""
+    opt = L.make_attention_options(P, P, P, softcap=cap)
+    assert L.mc_attention_forward_opt(None, P, P, 1, 4, 2, 64, opt) == code
+    assert L.mc_attention_backward_opt(None, P, P, P, P, P, 1, 4, 2, 64, opt) == code
+
+
 def test_null_options():
     assert L.mc_attention_forward_opt(P, P, P, 1, 4, 2, 64, None) == L.MC_ERR_NULLPTR
     assert L.mc_attention_backward_opt(P, P, P, P, P, P, 1, 4, 2, 64, None) == L.MC_ERR_NULLPTR

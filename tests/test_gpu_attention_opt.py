@@ -355,6 +355,26 @@ def test_attention_large_scores_and_steep_bias():
     p.check()
 
 
+@pytest.mark.parametrize("kind", ["causal", "window", "whole"])
+@pytest.mark.parametrize("cap,d", [(0.0, 128), (0.0, 64), (5.0, 64)])
+def test_attention_slopes_of_both_signs(kind, cap, d):
+    p = Problem(kind, 1, 430, 3, d, cap, True)
+    p.slopes = [-0.125, 0.0, 0.25]  # negative: far keys count more
+    p.sl.copy_(torch.tensor(p.slopes))
+    p.check()
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -16, 0.01, 5000.0, 2.0 ** 16])
+def test_attention_smallest_and_largest_caps(cap):
+    p = Problem("documents", 1, 333, 2, 64, cap, qstd=2.0)
+    p.qkv[:, 200:, :128] = 0  # scores of 0 too
+    if cap == 2.0 ** 16:
+        # c tanh(z / c) is z - z^3 / (3 c^2): for |z| < 40 that is z to within 5e-6, below the
+        # tolerance without a cap (which has no term in c)
+        p.cap = 0.0
+    p.check()
+
+
 def test_matches_plain_causal_attention():
     p = Problem("causal", 2, 777, 4, 128)
     o, lse = p.forward()
