@@ -591,9 +591,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         uint32_t pp[32];
         const float d0 = static_cast<float>(c0 + half * 64 - (r0 + t));  // query - key
         // (in log2 units from here on, if there is no cap to form first)
-        if constexpr (BIAS && !CAP)
-          bias_scores<64>(p, sc.mul, sc.slope2, d0,
-                          side_of(c0 + half * 64, 64, r0 + quarter * 32, 32));
+        if constexpr (BIAS && !CAP) bias_scores<64>(p, sc.mul, sc.slope2, d0);
         float u_max = 0.f;  // the largest square of a visible raw score
         auto weights = [&](auto edge_c, auto small_c) {
           constexpr bool EDGE = decltype(edge_c)::value;
@@ -988,8 +986,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       uint32_t dw[32];
       const float2 nd2 = make_float2(-my_d, -my_d);
       const float d0 = static_cast<float>(c0 - r);  // key - query
-      if constexpr (BIAS && !CAP)
-        bias_scores<64>(sv, sc.mul, sc.slope2, d0, side_of(c0, 64, q0 + quarter * 32, 32));
+      if constexpr (BIAS && !CAP) bias_scores<64>(sv, sc.mul, sc.slope2, d0);
       float u_max = 0.f;  // the largest square of a visible raw score
       auto gradients = [&](auto edge_c, auto small_c) {
         constexpr bool EDGE = decltype(edge_c)::value;

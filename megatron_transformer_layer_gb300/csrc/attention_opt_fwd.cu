@@ -541,8 +541,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
               }
             }
           }
-          bias_scores<128>(x, CAP ? 1.f : sc.mul, sc.slope2, static_cast<float>(key0 - q),
-                           side_of(key0, 128, q - lane, 32));
+          bias_scores<128>(x, CAP ? 1.f : sc.mul, sc.slope2, static_cast<float>(key0 - q));
         }
         if (cut) {
 #pragma unroll
