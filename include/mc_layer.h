@@ -498,8 +498,10 @@ typedef struct mc_rotary_spec {
  * heads = 2 H, ld = 3a.  positions: int32 [axes, tokens], any value (angles
  * are formed in 64 bits); inv_freq: fp32 [rot_dim / 2], finite.  out == in
  * (with the same stride) turns in place; otherwise they must not overlap.
- * rot_dim <= 512, heads * head_dim <= 2^22.  Vectors of 16 bytes are used where rot_dim / 2, head_dim,
- * the strides and the addresses are multiples of them, else smaller ones. */
+ * rot_dim <= 512, head_dim <= 1024, heads * head_dim <= 2^22 (else
+ * MC_ERR_UNSUPPORTED).  Vectors of 16 bytes are used where rot_dim / 2,
+ * head_dim, the strides and the addresses are multiples of them, else smaller
+ * ones. */
 int mc_rotary_forward(const void* in, void* out, int32_t is_bf16, int64_t tokens, int32_t heads,
                       int32_t head_dim, int64_t ld_in, int64_t ld_out, const int32_t* positions,
                       const float* inv_freq, const mc_rotary_spec* spec, int* status,

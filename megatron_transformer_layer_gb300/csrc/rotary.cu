@@ -315,8 +315,8 @@ int launch_rotary(const void* in, void* out, bool bf16, int64_t tokens, int head
   if (rc != MC_OK) return rc;
   if (tokens < 1 || heads < 1) return MC_ERR_SHAPE;
   const int64_t width = static_cast<int64_t>(heads) * head_dim;
-  // (2^22 units of at most 512 per head: within fast_div)
-  if (width > (1 << 22)) return MC_ERR_UNSUPPORTED;
+  // fast_div: fewer than 2^22 units, at most 2^10 of them of one head
+  if (width > (1 << 22) || head_dim > 1024) return MC_ERR_UNSUPPORTED;
   if (ld_in < width || ld_out < width) return MC_ERR_SHAPE;
   if (!in || !out || !positions || !inv_freq) return MC_ERR_NULLPTR;
   const uintptr_t size = bf16 ? 2 : 4;

@@ -119,6 +119,9 @@ ROTARY = dict(x=P, out=P, bf16=1, tokens=4, heads=2, d=64, ld_in=128, ld_out=128
     (dict(pos=P + 2), L.MC_ERR_ALIGN),
     (dict(ld_out=160), L.MC_ERR_ARGUMENT),       # in place with another stride
     (dict(d=1024, ld_in=4096, ld_out=4096, spec=spec(514)), L.MC_ERR_UNSUPPORTED),
+    (dict(d=1026, ld_in=4096, ld_out=4096), L.MC_ERR_UNSUPPORTED),
+    (dict(heads=1, d=3000000, ld_in=1 << 22, ld_out=1 << 22), L.MC_ERR_UNSUPPORTED),
+    (dict(heads=65537, ld_in=1 << 23, ld_out=1 << 23), L.MC_ERR_UNSUPPORTED),
 ])
 def test_rotary_refusals(change, code):
     a = dict(ROTARY, spec=spec())

@@ -43,6 +43,7 @@ def i32(x):
     (2, 2, 512, 512, [256], False, False, torch.bfloat16, 0),
     (70, 64, 128, 128, None, False, False, torch.bfloat16, 4096),
     (600, 7, 64, 32, [0, 16], False, False, torch.bfloat16, 0),
+    (3, 4096, 1024, 2, None, False, False, torch.bfloat16, 1),    # the most units in a row
 ])
 @pytest.mark.parametrize("inverse", [False, True])
 def test_rotary(tokens, heads, d, rot, sections, adjacent, dealt, dtype, extra, inverse):
