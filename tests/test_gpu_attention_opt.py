@@ -43,6 +43,9 @@ def i32(x):
     (2, 2, 512, 512, [256], False, False, torch.bfloat16, 0),
     (70, 64, 128, 128, None, False, False, torch.bfloat16, 4096),
     (600, 7, 64, 32, [0, 16], False, False, torch.bfloat16, 0),
+    (11, 3, 64, 24, None, True, False, torch.bfloat16, 0),        # vectors that do not pair up
+    (6, 2, 72, 48, None, False, False, torch.bfloat16, 0),
+    (6, 2, 72, 64, [20, 12], True, True, torch.float32, 0),
     (3, 4096, 1024, 2, None, False, False, torch.bfloat16, 1),    # the most units in a row
 ])
 @pytest.mark.parametrize("inverse", [False, True])
