@@ -94,13 +94,14 @@ __device__ __forceinline__ uint32_t bit_transpose(uint32_t x, int lane) {
   return x;
 }
 
-constexpr int kOptKvThreads = 384;
-// As in the forward: 128 x 56 + 256 x 224 = 384 x 168.
-constexpr int kOptKvRegsIo = 56, kOptKvRegsCompute = 224;
+constexpr int kOptKvThreads = 640;
+// 128 x 56 + 512 x 104 of the launch's 640 x 96 registers.
+constexpr int kOptKvRegsIo = 56, kOptKvRegsCompute = 104;
+constexpr int kOptKvWarps = 16;  // compute warps
 
 // Persistent: one CTA per SM walks the (key block, head) items, each against
-// the query blocks that see it (blocks i, counted across items).  384 threads:
-// warp 0 loads, warp 1 issues, warp 2 stores dz^T tiles, warps 4..11 compute.
+// the query blocks that see it (blocks i, counted across items).  640 threads:
+// warp 0 loads, warp 1 issues, warp 2 stores dz^T tiles, warps 4..19 compute.
 // TMEM: S^T [0, 128), dP^T [128, 256), dV [256, 256 + D), dK [384, 384 + D).
 // Per query block i:
 //   MMA      S^T_i = K Q_i^T (as soon as the compute warps hold S^T_{i-1} in
@@ -108,11 +109,22 @@ constexpr int kOptKvRegsIo = 56, kOptKvRegsCompute = 224;
 //            then (those done) dP^T_i = V dO_i^T.
 //   compute  P^T (and the cap's derivative) from S^T_i while the products
 //            above run, then dz^T from dP^T_i.
-// A compute thread owns one key row and 64 query columns: the 16 queries of
+// A compute thread owns one key row and 32 query columns: the 16 queries of
 // group g (dP^T columns [16g, 16g + 16)) leave P at columns [16g, 16g + 8) and
 // dz at [16g + 8, 16g + 16), over columns that the thread itself has read.
 // An item's dV and dK are stored during the next item's first block: its
 // S^T and weights run meanwhile, as do the loads of its K and V.
+//
+// Bound by the chain products -> dP^T -> dz^T -> products, about 4200 clocks of
+// which the tensor cores work 3100, and by HBM where documents are short (the
+// dz^T tiles).  Sixteen compute warps against eight of 64 columns: 452 against
+// 476 us for a capped backward over 8192 tokens and 16 heads, 22.1 against 23.1
+// us for 4 x 509 tokens and 12 heads, 263 against 266 us for 4096 packed tokens
+// of 64 heads, but 722 against 712 us for the same without a mask but the causal
+// one.  Shorter chains were slower in all: P^T over S^T's columns with dz^T
+// read from shared memory, so that dP^T runs ahead (776 us, 757 with dK issued
+// earlier), P^T over dP^T's as soon as that is in registers (824 us), dV and dK
+// through the tile's buffer and TMA (722 us with eight warps).
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kOptKvThreads, 1)
     attn_opt_dkdv_kernel(const __grid_constant__ CUtensorMap tm_qkv,
@@ -143,18 +155,18 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   uint64_t* do_full = bars + 10;   // [kdO]
   uint64_t* do_empty = bars + 12;  // [kdO] after the products
   uint64_t* s_full = bars + 14;    // S^T_i in TMEM
-  uint64_t* s_free = bars + 15;    // compute warps hold S^T_i in registers (8 warps)
+  uint64_t* s_free = bars + 15;    // compute warps hold S^T_i in registers (16 warps)
   uint64_t* dp_full = bars + 16;   // dP^T_i in TMEM
-  uint64_t* p_full = bars + 17;    // P^T_i, dz^T_i in TMEM (8 warps)
+  uint64_t* p_full = bars + 17;    // P^T_i, dz^T_i in TMEM (16 warps)
   uint64_t* acc_done = bars + 18;  // dV, dK products of block i complete
   uint64_t* drain = bars + 19;
   uint64_t* lse_ready = bars + 20;  // [2] (4 warps)
   uint64_t* it_full = bars + 22;    // [kOptKvRing]
-  uint64_t* it_empty = bars + 26;   // [kOptKvRing] read by MMA, tile and compute warps (10)
+  uint64_t* it_empty = bars + 26;   // [kOptKvRing] read by MMA, tile and compute warps (18)
   uint64_t* steal_bar = bars + 30;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   void* response = bars + 32;  // 16 bytes, aligned as the items are
-  uint64_t* ds_full = bars + 34;  // the dz^T tile of block i is in sDs (8 warps)
+  uint64_t* ds_full = bars + 34;  // the dz^T tile of block i is in sDs (16 warps)
   uint64_t* ds_free = bars + 35;  // its bulk store has read sDs
   uint16_t* sM = reinterpret_cast<uint16_t*>(bars + 36);  // [2][128] first | end << 8
   int* sF = reinterpret_cast<int*>(sM + 256);             // [2][4] the 32 queries see the whole block
@@ -176,18 +188,18 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       mbar_init(&do_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&lse_ready[i], 4);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, kOptKvWarps);
     mbar_init(ds_free, 1);
     mbar_init(s_full, 1);
-    mbar_init(s_free, 8);
+    mbar_init(s_free, kOptKvWarps);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 8);
+    mbar_init(p_full, kOptKvWarps);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     mbar_init(steal_bar, 1);
     for (int i = 0; i < kOptKvRing; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 10);
+      mbar_init(&it_empty[i], 2 + kOptKvWarps);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_qkv);
@@ -456,14 +468,14 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   } else {
     // ---------------------------------------------------------- compute
     setmaxnreg_inc<kOptKvRegsCompute>();
-    // Two warps per TMEM lane quarter; `half` picks 64 of the 128 query columns.
+    // Four warps per TMEM lane quarter; `grp` picks 32 of the 128 query columns.
     const int quarter = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int grp = (warp - 4) >> 2;
     const int t = quarter * 32 + lane;  // key row within the block
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t my_cols = lane_off + static_cast<uint32_t>(half * 64);
+    const uint32_t my_cols = lane_off + static_cast<uint32_t>(grp * 32);
     bool ok = true;
-    // What query t of the next block brings, loaded one block ahead (half 0)
+    // What query t of the next block brings, loaded one block ahead (group 0)
     // and first used when it is staged: an operation on it here would wait for
     // the loads.  Queries past the sequence see the whole block: their Q and
     // dO are zeros.
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     bool have = false;  // loaded and not yet staged
     auto stage_query = [&](int st) {
       have = false;
-      if (half != 0) return;
+      if (grp != 0) return;
       const int first = min(max(q_lo - q_r0, 0), 128);
       const int end = min(max(min(q_hi, s) - q_r0, 0), 128);
       const int range = q_in ? first | (end << 8) : 128 << 8;
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       const int4 e = items[slot].entry;
       have = e.w > 0;
       if (have) {
-        if (half == 0) load_query(e.x, items[slot].head, e.y * 128, e.z * 128 + t);
+        if (grp == 0) load_query(e.x, items[slot].head, e.y * 128, e.z * 128 + t);
         if constexpr (BIAS) n_slope = A.slopes[items[slot].head];
       }
     };
@@ -517,20 +529,19 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     int p_row = 0, p_bi = 0, p_head = 0;
     auto store_item = [&](bool from_tmem, int row0, int bi, int hh) {
       const int warp_row = row0 + quarter * 32;
+      // 32 columns of dV (w = 0: V's columns of dqkv) and dK (1: scaled by
+      // 1/sqrt(d)) a warp, or of one of them (d = 64)
 #pragma unroll 1
-      for (int w = 0; w < 2; ++w) {
-        // w = 0: dV (V's columns of dqkv), w = 1: dK scaled by 1/sqrt(d)
+      for (int task = grp; task < D / 16; task += 4) {
+        const int w = task / (D / 32), c = task % (D / 32);
         const float mul = w == 0 ? 1.f : rsqrtf(static_cast<float>(D));
         const int col = (w == 0 ? 2 * a : a) + hh * D;
         uint16_t* base = A.dqkv + (static_cast<int64_t>(bi) * s + warp_row) * 3 * a + col;
         const bool in_range = MC_DCHECK(warp_row >= 0 && bi >= 0 && bi < A.b && col + D <= 3 * a,
                                         status, kSiteAttention);
-#pragma unroll 1
-        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
-          float v[32] = {};
-          if (from_tmem) tmem_ld_32x32b_x32((w == 0 ? tdV : tdK) + lane_off + c * 32, v);
-          store_rows32(base + c * 32, 3ll * a, in_range ? s - warp_row : 0, v, mul, lane);
-        }
+        float v[32] = {};
+        if (from_tmem) tmem_ld_32x32b_x32((w == 0 ? tdV : tdK) + lane_off + c * 32, v);
+        store_rows32(base + c * 32, 3ll * a, in_range ? s - warp_row : 0, v, mul, lane);
       }
     };
     look_ahead(0);
@@ -550,18 +561,16 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       const float cap_limit2 = cap_limit * cap_limit;
       for (int i = 0; i < count; ++i, ++g) {
         const int c0 = (qb0 + i) * 128;  // first query of this block
-        const float* l2 = sL + (g & 1) * 128 + half * 64;
-        const float* dl = sD + (g & 1) * 128 + half * 64;
+        const float* l2 = sL + (g & 1) * 128 + grp * 32;
+        const float* dl = sD + (g & 1) * 128 + grp * 32;
         if (!mbar_wait_warp(&lse_ready[g & 1], (g >> 1) & 1, status, kSiteAttention) ||
             !mbar_wait_warp(s_full, g & 1, status, kSiteAttention)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float p[64];
-        tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
-        tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
-        tmem_ld_wait();
+        float p[32];
+        tmem_ld_32x32b_x32(tS + my_cols, p);
         if constexpr (!CAP) {  // (a cap may need S^T once more)
           tc_fence_before();
           mbar_arrive_warp(s_free, lane);
@@ -569,35 +578,32 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         // the next block's queries: loaded here, staged behind this block's work
         if (i + 1 < count) {
           have = true;
-          if (half == 0) load_query(bi, hh, r0, c0 + 128 + t);
+          if (grp == 0) load_query(bi, hh, r0, c0 + 128 + t);
         } else {
           look_ahead(r + 1);
         }
-        const bool edge = (sF[(g & 1) * 4 + 2 * half] & sF[(g & 1) * 4 + 2 * half + 1]) == 0;
-        // bit e of vis: this key is visible to query e of the 64
-        uint32_t vis[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        const bool edge = sF[(g & 1) * 4 + grp] == 0;
+        // bit e of vis: this key is visible to query e of the 32
+        uint32_t vis = 0xFFFFFFFFu;
         if (edge) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int range = sM[(g & 1) * 128 + half * 64 + 32 * c + lane];
-            vis[c] = bit_transpose(
-                bit_range((range & 255) - 32 * quarter, (range >> 8) - 32 * quarter), lane);
-          }
+          const int range = sM[(g & 1) * 128 + grp * 32 + lane];
+          vis = bit_transpose(
+              bit_range((range & 255) - 32 * quarter, (range >> 8) - 32 * quarter), lane);
         }
-        auto sees = [&](int e) { return ((vis[e >> 5] >> (e & 31)) & 1u) != 0; };
+        auto sees = [&](int e) { return ((vis >> e) & 1u) != 0; };
         // P (bf16 pairs in pp with a cap, else still in p), and in p what dP -
         // delta is multiplied by: P, with a cap P (1 - tanh^2).  pp ends up with
         // dz, pair for pair.
-        uint32_t pp[32];
-        const float d0 = static_cast<float>(c0 + half * 64 - (r0 + t));  // query - key
+        uint32_t pp[16];
+        const float d0 = static_cast<float>(c0 + grp * 32 - (r0 + t));  // query - key
         // (in log2 units from here on, if there is no cap to form first)
-        if constexpr (BIAS && !CAP) bias_scores<64>(p, sc.mul, sc.slope2, d0);
+        if constexpr (BIAS && !CAP) bias_scores<32>(p, sc.mul, sc.slope2, d0);
         float u_max = 0.f;  // the largest square of a visible raw score
         auto weights = [&](auto edge_c, auto small_c) {
           constexpr bool EDGE = decltype(edge_c)::value;
           [[maybe_unused]] constexpr bool SMALL = decltype(small_c)::value;
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
+          for (int e = 0; e < 32; e += 4) {
             const float4 lv = *reinterpret_cast<const float4*>(l2 + e);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -651,9 +657,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           // a visible score of the warp is not far enough below the cap (what is
           // masked must not decide how it is formed): the quotient form
           if (!__all_sync(0xffffffffu, u_max <= cap_limit2)) {
-            tmem_ld_32x32b_x32_nowait(tS + my_cols, p);
-            tmem_ld_32x32b_x32_nowait(tS + my_cols + 32, p + 32);
-            tmem_ld_wait();
+            tmem_ld_32x32b_x32(tS + my_cols, p);
             weights(BoolC<true>{}, BoolC<false>{});
           }
           tc_fence_before();
@@ -674,16 +678,15 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
           break;
         }
         tc_fence_after();
-#pragma unroll
-        for (int gp = 0; gp < 2; ++gp) {
+        {
           float dv[32];
-          tmem_ld_32x32b_x32(tdP + my_cols + gp * 32, dv);
+          tmem_ld_32x32b_x32(tdP + my_cols, dv);
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
             uint32_t w[16];  // [P of 16 queries | their dz]
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const int at = gp * 32 + gr * 16 + e;
+              const int at = gr * 16 + e;
               const float4 dlv = *reinterpret_cast<const float4*>(dl + at);
               const float* dq = dv + gr * 16 + e;
               const float2 d0 = __fmul2_rn(make_float2(p[at], p[at + 1]),
@@ -703,9 +706,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
               w[8 + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) pp[gp * 16 + gr * 8 + e] = w[8 + e];
+            for (int e = 0; e < 8; ++e) pp[gr * 8 + e] = w[8 + e];
             // over this thread's own dP^T columns, already in registers
-            tmem_st_32x32b_x16(tdP + my_cols + gp * 32 + gr * 16, w);
+            tmem_st_32x32b_x16(tdP + my_cols + gr * 16, w);
           }
         }
         tmem_st_wait();
@@ -713,17 +716,17 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         mbar_arrive_warp(p_full, lane);
         if (A.ds_tiles) {
           // The 128-byte-swizzled shared-memory image of an MN-major A operand:
-          // query chunk `half` at 16 KB, key row t at 128 B, the 16-byte unit
+          // 64-query chunks 16 KB apart, key row t at 128 B, the 16-byte unit
           // of queries [8u, 8u + 8) at unit u ^ (t & 7); the store of the
           // block before must have read sDs first.
           if (g > 0 && !mbar_wait_warp(ds_free, (g - 1) & 1, status, kSiteAttention)) {
             ok = false;
             break;
           }
-          uint8_t* ds_row = sDs + half * 16384 + t * 128;
+          uint8_t* ds_row = sDs + (grp >> 1) * 16384 + t * 128;
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4*>(ds_row + ((u ^ (t & 7)) << 4)) =
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(ds_row + (((u + 4 * (grp & 1)) ^ (t & 7)) << 4)) =
                 make_uint4(pp[4 * u], pp[4 * u + 1], pp[4 * u + 2], pp[4 * u + 3]);
           fence_proxy_async_smem();  // visible to the bulk copy
           mbar_arrive_warp(ds_full, lane);
@@ -758,6 +761,10 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
 }
 
 // ---------------------------------------------------------------- dQ, scores formed again
+constexpr int kOptDqThreads = 384;
+// As in the forward: 128 x 56 + 256 x 224 = 384 x 168.
+constexpr int kOptDqRegsIo = 56, kOptDqRegsCompute = 224;
+
 template <int D>
 struct OptDqCfg {
   static constexpr int kChunks = D / 64;
@@ -775,7 +782,7 @@ struct OptDqCfg {
 // follows when dz_j is in TMEM (ds_full), and its completion (ds_free) lets
 // dz_{j+1} be written.
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kOptKvThreads, 1)
+__global__ void __launch_bounds__(kOptDqThreads, 1)
     attn_opt_dq_kernel(const __grid_constant__ CUtensorMap tm_qkv,
                        const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ OptBwdArgs A) {
@@ -843,7 +850,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
   const int count = ok_entry && k_hi > k_lo ? (k_hi - k_lo + 127) / 128 : 0;
 
   if (warp < 4) {
-    setmaxnreg_dec<kOptKvRegsIo>();
+    setmaxnreg_dec<kOptDqRegsIo>();
     if (warp == 0) {
       if (lane == 0 && count > 0) {
         // -------------------------------------------------------- producer
@@ -936,7 +943,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- compute
-    setmaxnreg_inc<kOptKvRegsCompute>();
+    setmaxnreg_inc<kOptDqRegsCompute>();
     const int quarter = warp & 3;
     const int half = (warp - 4) >> 2;   // 64 of the block's 128 key columns
     const int r = q0 + quarter * 32 + lane;  // this thread's query row
@@ -1326,7 +1333,7 @@ int launch_bwd(const CUtensorMap& tq, const CUtensorMap& td, const OptBwdArgs& A
   if (A.ds_tiles) return MC_OK;
   auto kq = attn_opt_dq_kernel<D, CAP, BIAS>;
   if (opt_smem(init_q, kq, OptDqCfg<D>::kSmem) != cudaSuccess) return MC_ERR_CUDA;
-  launch_kernel(kq, opt_dq_grid(A), dim3(kOptKvThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
+  launch_kernel(kq, opt_dq_grid(A), dim3(kOptDqThreads), OptDqCfg<D>::kSmem, st, 1, tq, td, A);
   return cudaGetLastError() == cudaSuccess ? MC_OK : MC_ERR_CUDA;
 }
 
