@@ -780,7 +780,9 @@ struct OptDqCfg {
 // The compute warps read S_j and dP_j into registers and release them at once
 // (s_free), so S_{j+1} and dP_{j+1} run while dz_j is formed; dQ += dz_j K_j
 // follows when dz_j is in TMEM (ds_full), and its completion (ds_free) lets
-// dz_{j+1} be written.
+// dz_{j+1} be written.  Three products per block pair where the tiles need one:
+// with the dK/dV kernel 297 us against 263 us for 4096 packed tokens of 64
+// heads, 563 against 452 us for 8192 capped ones of 16; it needs no workspace.
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kOptDqThreads, 1)
     attn_opt_dq_kernel(const __grid_constant__ CUtensorMap tm_qkv,
@@ -1107,7 +1109,9 @@ constexpr int kOptDqRing = 4;
 // Persistent, 192 threads: warp 0 loads per key block the dz^T tile (one bulk
 // copy of its swizzled image) and K_j into a 3-deep ring that runs on across
 // items, warp 1 issues dQ += dz_j K_j (items alternate accumulators), warps
-// 2..5 write dQ / sqrt(d) of the item before.
+// 2..5 write dQ / sqrt(d) of the item before.  Bound by HBM: 4096 packed tokens
+// of 64 heads move 423 MB in 68 us (6.2 TB/s), a causal mask over them 1.38 GB
+// in 200 us (6.9 TB/s: what the dK/dV kernel wrote last is still in L2).
 template <int D>
 __global__ void __launch_bounds__(192, 1)
     attn_opt_dq_gemm_kernel(const __grid_constant__ CUtensorMap tm_qkv,
