@@ -94,6 +94,23 @@ def test_rotary_there_and_back():
     assert float((z - x).abs().max()) < 8 * 2.0 ** -20
 
 
+def test_rotary_offsets_past_32_bits():
+    """Rows whose elements lie beyond 2^31: the last ones against the oracle."""
+    tokens, ld = 70000, 32768
+    x = torch.zeros(tokens, ld, dtype=torch.bfloat16, device=DEV)
+    x[-3:, :256] = bf16(gen(8), 3, 256)
+    pos, freq = i32(np.arange(tokens)[None]), torch.rand(64, generator=gen(9))
+    want = O.rotary(to_f64(x[-3:, :256]).reshape(3, 2, 128), pos[:, -3:].cpu().numpy(),
+                    freq.numpy(), 128, [64]).reshape(3, -1)
+    tol = 2.0 ** -8 * np.abs(want) + np.abs(to_f64(x[-3:, :256])).max() * 2.0 ** -20
+    st = status()
+    assert L.mc_rotary_forward(x, x, tokens, 2, 128, ld, ld, pos, freq.to(DEV),
+                               L.make_rotary_spec(128), st) == 0
+    check_status(st)
+    assert (np.abs(to_f64(x[-3:, :256]) - want) <= tol).all()
+    assert not x[-3:, 256:].any() and not x[:-3].any()
+
+
 # ------------------------------------------------------------------ masks
 def make_documents(off, pre, causal, window, b, s):
     n = 2 * b * ((s + 127) // 128)
@@ -443,6 +460,108 @@ def test_tables_of_another_shape_are_reported():
     assert L.mc_attention_forward_opt(p.qkv, p.o, p.lse, 1, 400, 2, 64, p.opt, st) == 0
     torch.cuda.synchronize()
     assert int(st[0]) == L.MC_ERR_DEVICE_BOUNDS
+
+
+def windowed_tail_matches(qkv, o, dqkv, dout, lo, hi, H, d, window, n=320):
+    """The last rows of the last head of the last sequence, which only depend on
+    the n tokens that end it."""
+    a, b, s = H * d, qkv.shape[0], qkv.shape[1]
+    part = lambda x, k: x[b - 1:, s - n:, k * a + (H - 1) * d:k * a + H * d]  # noqa: E731
+    sub = to_f64(torch.cat([part(qkv, k) for k in range(3)], dim=2))
+    slo, shi = ((v[b - 1:, s - n:].cpu().numpy() - (s - n)).clip(0, n) for v in (lo, hi))
+    want, _, tol, _ = O.attention_forward(sub, slo, shi, 1, d)
+    assert (np.abs(to_f64(part(o, 0)) - want) <= tol)[:, window:].all()
+    want, tol, _ = O.attention_backward(sub, to_f64(part(dout, 0)), slo, shi, 1, d)
+    got = to_f64(torch.cat([part(dqkv, k) for k in range(3)], dim=2))
+    assert (np.abs(got - want) <= tol)[:, window:].all()
+
+
+@pytest.mark.parametrize("b,s,H,d,tiles", [(1, 100000, 64, 128, False), (2, 50000, 64, 128, False),
+                                           (1, 16500, 18, 64, True)])
+def test_attention_offsets_past_32_bits(b, s, H, d, tiles):
+    """Elements beyond 2^31 in Q | K | V, or tiles beyond 2^32 bytes."""
+    a, window = H * d, 64
+    qkv, dqkv = (torch.empty(b, s, 3 * a, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    o, dout = (torch.empty(b, s, a, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    torch.manual_seed(s)
+    qkv.normal_()
+    dout.normal_()
+    lse, delta = (torch.empty(b * H * s, device=DEV) for _ in range(2))
+    lo, hi, tab = make_documents([0, b * s - s // 2, b * s], None, True, window, b, s)
+    opt = L.make_attention_options(lo, hi, tab)
+    n = L.mc_attention_backward_opt_ws_bytes(b, s, H, d, opt) if tiles else 0
+    assert not tiles or n > 2 ** 32
+    ws, st = torch.empty(n, dtype=torch.uint8, device=DEV) if tiles else None, status()
+    assert L.mc_attention_forward_opt(qkv, o, lse, b, s, H, d, opt, st) == 0
+    assert L.mc_attention_backward_opt(qkv, o, lse, dout, dqkv, delta, b, s, H, d, opt, ws, n,
+                                       st) == 0
+    check_status(st)
+    windowed_tail_matches(qkv, o, dqkv, dout, lo, hi, H, d, window)
+
+
+def test_two_streams_at_once_give_the_same_bits():
+    """Grids of more items than start at once, whose CTAs take items as they come."""
+    ps = [Problem("documents", 1, 2500, 40, 128, 30.0, seed=1),
+          Problem("window", 2, 1100, 40, 64, bias=True, seed=2)]
+    n = [L.mc_attention_backward_opt_ws_bytes(p.b, p.s, p.H, p.d, p.opt) for p in ps]
+    ws = [torch.empty(x, dtype=torch.uint8, device=DEV) for x in n]
+    out = [torch.empty_like(p.qkv) for p in ps]
+    st = [status(), status()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def call(i, stream):
+        p = ps[i]
+        assert L.mc_attention_forward_opt(p.qkv, p.o, p.lse, p.b, p.s, p.H, p.d, p.opt, st[i],
+                                          stream) == 0
+        assert L.mc_attention_backward_opt(p.qkv, p.o, p.lse, p.dout, out[i], p.delta, p.b, p.s,
+                                           p.H, p.d, p.opt, ws[i], n[i], st[i], stream) == 0
+
+    for i in range(2):
+        call(i, None)
+    torch.cuda.synchronize()
+    alone = [(p.o.clone(), p.lse.clone(), x.clone()) for p, x in zip(ps, out)]
+    for p, x in zip(ps, out):
+        p.o.zero_(), p.lse.zero_(), x.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_status(st[i])
+        p = ps[i]
+        rows = p.b * p.s
+        assert torch.equal(p.o[:rows], alone[i][0][:rows])
+        assert torch.equal(p.lse[:-1], alone[i][1][:-1]) and torch.equal(out[i], alone[i][2])
+
+
+def test_two_graphs_share_a_workspace():
+    ps = [Problem("documents", 1, 700, 4, 64, seed=1), Problem("prefix", 2, 300, 3, 128, seed=2)]
+    n = [L.mc_attention_backward_opt_ws_bytes(p.b, p.s, p.H, p.d, p.opt) for p in ps]
+    ws = torch.empty(max(n), dtype=torch.uint8, device=DEV)
+    out, graphs, alone = [torch.empty_like(p.qkv) for p in ps], [], []
+    stream = torch.cuda.Stream()
+    for i, p in enumerate(ps):
+        def call(i=i, p=p):
+            assert L.mc_attention_forward_opt(p.qkv, p.o, p.lse, p.b, p.s, p.H, p.d, p.opt, None,
+                                              stream) == 0
+            assert L.mc_attention_backward_opt(p.qkv, p.o, p.lse, p.dout, out[i], p.delta, p.b, p.s,
+                                               p.H, p.d, p.opt, ws, n[i], None, stream) == 0
+        with torch.cuda.stream(stream):
+            call()
+        torch.cuda.synchronize()
+        alone.append(out[i].clone())
+        out[i].zero_()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            call()
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 0, 1):
+        out[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[i], alone[i])
 
 
 def test_on_a_stream_and_in_a_graph():
