@@ -72,11 +72,12 @@ class mc_layer_grads(ctypes.Structure):  # noqa: N801
 MC_ROTARY_MAX_AXES = 4
 MC_ROTARY_ADJACENT_PAIRS = 1
 MC_ROTARY_DEAL_AXES = 2
+_RotarySections = ctypes.c_int32 * MC_ROTARY_MAX_AXES
 
 
 class mc_rotary_spec(ctypes.Structure):  # noqa: N801
     _fields_ = [("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
-                ("sections", ctypes.c_int32 * MC_ROTARY_MAX_AXES), ("flags", ctypes.c_uint32)]
+                ("sections", _RotarySections), ("flags", ctypes.c_uint32)]
 
 
 class mc_attention_options(ctypes.Structure):  # noqa: N801
@@ -387,13 +388,13 @@ def _ref(struct):
 def make_rotary_spec(rot_dim, sections=None, interleaved_pairs=False, interleaved_axes=False):
     """`sections`: pairs of each axis (default: one axis).  `interleaved_pairs`:
     pairs are neighbours (2p, 2p + 1); `interleaved_axes`: axes dealt in turn."""
-    sections = [rot_dim // 2] if sections is None else [int(x) for x in sections]
+    if sections is None:
+        sections = (rot_dim // 2,)
     if not 1 <= len(sections) <= MC_ROTARY_MAX_AXES:
         raise ValueError(f"1 to {MC_ROTARY_MAX_AXES} axes, got {len(sections)}")
     flags = (MC_ROTARY_ADJACENT_PAIRS if interleaved_pairs else 0) | \
         (MC_ROTARY_DEAL_AXES if interleaved_axes else 0)
-    return mc_rotary_spec(rot_dim, len(sections), (ctypes.c_int32 * MC_ROTARY_MAX_AXES)(*sections),
-                          flags)
+    return mc_rotary_spec(rot_dim, len(sections), _RotarySections(*sections), flags)
 
 
 def make_layer_rotary(spec, positions, inv_freq):
