@@ -18,9 +18,9 @@
 // TMEM: S [0, 256), O [256, 256 + D), P [384, 512) (bf16 pairs, 256 keys).
 //
 // Bound by the products (2870 clocks per block at D = 128) where nothing is
-// capped or biased: causal over 16,384 tokens and 16 heads 707 us, 0.82 of the
-// measured matrix rate.  A cap's or bias's multiply-adds exceed them: 1046 and
-// 877 us.  Over short documents (4096 tokens, 64 heads, 88 us, 3.0 TB/s) the
+// capped or biased: causal over 16,384 tokens and 16 heads 703 us, 0.82 of the
+// measured matrix rate.  A cap's or bias's multiply-adds exceed them: 1022 and
+// 890 us.  Over short documents (4096 tokens, 64 heads, 88 us, 3.0 TB/s) the
 // partly masked blocks, the wait for an item's first S and the stores, 32 bytes
 // per clock and SM, show.  128-key blocks in two CTAs per SM and softmax warps
 // that take two passes were slower, as were sixteen softmax warps of 64 scores
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
   uint64_t* v_full = bars + 6;     // [4] per half-tile slot (VS used)
   uint64_t* v_empty = bars + 10;   // [4]  after the half's PV steps
   uint64_t* s_full = bars + 14;    // S in TMEM
-  uint64_t* s_free = bars + 15;    // the softmax holds S in registers (256 threads)
+  uint64_t* s_free = bars + 15;    // the softmax holds S in registers (256 threads, 8 warps)
   uint64_t* p_full = bars + 16;    // P in TMEM (256 threads)
   uint64_t* pv_done = bars + 17;   // O += P V complete
   uint64_t* o_free = bars + 18;    // the item's O is in registers (256 threads)
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 256);
+    mbar_init(s_free, CAP ? 8 : 256);
     mbar_init(p_full, 256);
     mbar_init(pv_done, 1);
     mbar_init(o_free, 256);
@@ -380,12 +380,13 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
     // barrier); slots alternate by phase so a fast peer never overwrites a
     // value the other has not read.
     int xphase = 0;
-    auto exchange = [&](float v) -> float {
-      float* slot = xch + (xphase & 1) * 256;
-      slot[half * 128 + row] = v;
+    auto offer = [&](float v) {
+      xch[(xphase & 1) * 256 + half * 128 + row] = v;
       mbar_arrive(&xbar[quarter]);
+    };
+    auto take = [&]() -> float {
       if (!mbar_wait(&xbar[quarter], xphase & 1, status, kSiteAttention)) ok = false;
-      const float peer = slot[(half ^ 1) * 128 + row];
+      const float peer = xch[(xphase & 1) * 256 + (half ^ 1) * 128 + row];
       ++xphase;
       return peer;
     };
@@ -480,7 +481,13 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 128 + 32 * c, x + 32 * c);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(s_free);
+        // One arrival per warp leaves a capped softmax more issue slots (1022
+        // against 1040 us over 16,384 tokens), but a warp's own barrier costs
+        // the others as much or more (712 against 703 us).
+        if constexpr (CAP)
+          mbar_arrive_warp(s_free, lane);
+        else
+          mbar_arrive(s_free);
         const int key0 = k_lo + j * kOptKeys + half * 128;
         // ---- keys [first, end) of this half are visible (the last block may lack
         //      its second half, whose S is an older one)
@@ -497,9 +504,11 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
         // With a bias the scores are formed here, in log2 units.  Without one
         // they stay raw until the exponent: the scale is positive and the cap
         // monotone, so the raw maximum gives the row's.
-        float low = INFINITY;  // a cap needs the lowest visible score too
-        if constexpr (CAP) {
-          float lo1 = INFINITY;
+        // A cap needs the lowest visible score too: whether the warp's visible
+        // scores are far enough below it (masked ones must not decide how the
+        // cap is formed).
+        auto below_cap = [&](float high) {
+          float low = INFINITY, lo1 = INFINITY;
           if (cut) {
 #pragma unroll
             for (int i = 0; i < 128; i += 2) {
@@ -513,12 +522,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
               lo1 = fmin3f(lo1, x[i + 2], x[i + 3]);
             }
           }
-          low = fminf(low, lo1);
-        }
-        // The visible scores of the warp's rows are far enough below the cap
-        // (masked ones must not decide how the cap is formed).
-        auto below_cap = [&](float high) {
-          return __all_sync(0xffffffffu, fmaxf(high, -low) <= cap_limit);
+          return __all_sync(0xffffffffu, fmaxf(high, -fminf(low, lo1)) <= cap_limit);
         };
         const float2 m2cap2 = make_float2(-2.f * sc.cap2, -2.f * sc.cap2);
         if constexpr (BIAS) {
@@ -561,8 +565,9 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
 #pragma unroll
         for (int p = 0; p < 62; ++p) mc[p & 3] = fmax3f(mc[p & 3], x[4 + 2 * p], x[5 + 2 * p]);
         float mx = fmaxf(fmax3f(mc[0], mc[1], mc[2]), mc[3]);
-        const bool small = CAP && !BIAS && below_cap(mx);
-        mx = fmaxf(mx, exchange(mx));
+        offer(mx);
+        const bool small = CAP && !BIAS && below_cap(mx);  // while the other half's is awaited
+        mx = fmaxf(mx, take());
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -672,7 +677,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       }
       if (!ok) break;
       if (halves > 0) {
-        l += exchange(l);  // both halves' sums, taken against the same maximum
+        offer(l);
+        l += take();  // both halves' sums, taken against the same maximum
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
