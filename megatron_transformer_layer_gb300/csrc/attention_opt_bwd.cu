@@ -124,7 +124,8 @@ constexpr int kOptKvWarps = 16;  // compute warps
 // one.  Shorter chains were slower in all: P^T over S^T's columns with dz^T
 // read from shared memory, so that dP^T runs ahead (776 us, 757 with dK issued
 // earlier), P^T over dP^T's as soon as that is in registers (824 us), dV and dK
-// through the tile's buffer and TMA (722 us with eight warps).
+// through the tile's buffer and TMA (722 us with eight warps), the queries' lse,
+// delta and masks staged by a warp of their own (753 us).
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kOptKvThreads, 1)
     attn_opt_dkdv_kernel(const __grid_constant__ CUtensorMap tm_qkv,
