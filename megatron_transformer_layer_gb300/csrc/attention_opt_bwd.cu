@@ -115,17 +115,18 @@ constexpr int kOptKvWarps = 16;  // compute warps
 // An item's dV and dK are stored during the next item's first block: its
 // S^T and weights run meanwhile, as do the loads of its K and V.
 //
-// Bound by the chain products -> dP^T -> dz^T -> products, about 4200 clocks of
-// which the tensor cores work 3100, and by HBM where documents are short (the
-// dz^T tiles).  Sixteen compute warps against eight of 64 columns: 452 against
-// 476 us for a capped backward over 8192 tokens and 16 heads, 22.1 against 23.1
-// us for 4 x 509 tokens and 12 heads, 263 against 266 us for 4096 packed tokens
-// of 64 heads, but 722 against 712 us for the same without a mask but the causal
-// one.  Shorter chains were slower in all: P^T over S^T's columns with dz^T
-// read from shared memory, so that dP^T runs ahead (776 us, 757 with dK issued
-// earlier), P^T over dP^T's as soon as that is in registers (824 us), dV and dK
-// through the tile's buffer and TMA (722 us with eight warps), the queries' lse,
-// delta and masks staged by a warp of their own (753 us).
+// A block takes about 4200 clocks, its four products 3100, which share the
+// shared memory with the loads and the tile's way out (192 + 64 + 64 KB); where
+// documents are short HBM counts too (the dz^T tiles). Sixteen compute warps
+// against eight of 64 columns: 452 against 476 us for a capped backward over
+// 8192 tokens and 16 heads, 22.1 against 23.1 us for 4 x 509 tokens and 12
+// heads, 263 against 266 us for 4096 packed tokens of 64 heads, but 722 against
+// 712 us for the same without a mask but the causal one. Shorter chains from one
+// block's products to the next were slower in all: P^T over S^T's columns with
+// dz^T read from shared memory, so that dP^T runs ahead (776 us, 757 with dK
+// issued earlier), P^T over dP^T's as soon as that is in registers (824 us), dV
+// and dK through the tile's buffer and TMA (722 us with eight warps), the
+// queries' lse, delta and masks staged by a warp of their own (753 us).
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kOptKvThreads, 1)
     attn_opt_dkdv_kernel(const __grid_constant__ CUtensorMap tm_qkv,

@@ -103,11 +103,11 @@ __device__ __forceinline__ uint64_t turns_fixed(float f) {
 }
 
 // A unit is two vectors: of VEC pairs' halves, of VEC / 2 adjacent pairs each
-// (VEC > 1), or copied ones; one where a head's do not pair up. A warp takes items of
-// unit_item units of each of tok_item tokens, one per lane and turn.  The first
-// turn's loads are issued before the item's cos / sin table is formed, so one
-// DRAM round trip covers both; the turns per position of every pair are formed
-// once per block.  What keeps the loads coming is the number of warps: two
+// (VEC > 1), or copied ones; one where a head's do not pair up. A warp takes
+// items of unit_item units of each of tok_item tokens, one per lane and turn.
+// The first turn's loads are issued before the item's cos / sin table is formed,
+// so one DRAM round trip covers both; the turns per position of every pair are
+// formed once per block. What keeps the loads coming is the number of warps: two
 // units per lane and turn, or the next turn's loads ahead of this one's work,
 // cost registers and were slower (60 and 64 us against 52), as was holding the
 // kernel to the registers of 8 blocks per SM (54.6).
