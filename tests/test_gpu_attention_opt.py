@@ -322,6 +322,11 @@ def test_attention_one_row_and_many_sequences(kind):
     Problem(kind, 19, 11, 1, 128).check()
 
 
+def test_attention_thousands_of_short_sequences():
+    """More table entries than are sorted, a few rows in each block."""
+    Problem("any", 4500, 3, 2, 64, 5.0, True).check(tiles=(True,))
+
+
 def test_attention_many_blocks():
     """More CTAs than four waves: the grid goes head after head."""
     Problem("window", 6, 1200, 12, 64).check()
