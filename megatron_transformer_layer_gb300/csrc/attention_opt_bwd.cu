@@ -479,8 +479,10 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     bool ok = true;
     // What query t of the next block brings, loaded one block ahead (group 0)
     // and first used when it is staged: an operation on it here would wait for
-    // the loads.  Queries past the sequence see the whole block: their Q and
-    // dO are zeros.
+    // the loads.  Queries past the sequence see the whole block, so that they do
+    // not make it an edge, with a log-sum-exp of infinity: P = exp(z - lse) is 0
+    // whatever the bias (a negative slope's grows with the distance, and an
+    // infinite P would not be cancelled by their dO of zeros).
     float q_lse = 0.f, q_delta = 0.f;
     int q_lo = 0, q_hi = 0, q_r0 = 0;  // and the first key of its block
     bool q_in = false;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
       const int first = min(max(q_lo - q_r0, 0), 128);
       const int end = min(max(min(q_hi, s) - q_r0, 0), 128);
       const int range = q_in ? first | (end << 8) : 128 << 8;
-      sL[st * 128 + t] = q_in ? q_lse * kOptLog2e : 0.f;
+      sL[st * 128 + t] = q_in ? q_lse * kOptLog2e : INFINITY;
       sD[st * 128 + t] = q_in ? q_delta : 0.f;
       sM[st * 128 + t] = static_cast<uint16_t>(range);
       const bool whole = __all_sync(0xffffffffu, range == (128 << 8));
