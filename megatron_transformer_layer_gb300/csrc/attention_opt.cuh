@@ -36,7 +36,7 @@ struct ScoreConst {
   float mul;     // no cap: log2(e) / sqrt(d); cap: 2 log2(e) / (sqrt(d) c)
   float arg;     // cap: 1 / (sqrt(d) c), the tanh's argument per raw score
   float cap2;    // c log2(e)
-  float slope2;  // slope log2(e)
+  float slope;   // the bias per distance: slope sqrt(d) for raw scores, with a cap slope log2(e)
 };
 
 // For |t| <= kCapSmall, tanh(t) = t p(t^2) with the cubic p of least largest
@@ -76,13 +76,13 @@ __device__ __forceinline__ ScoreConst score_const(float rsqrt_d, float softcap, 
   c.mul = rsqrt_d * kOptLog2e;
   c.arg = 0.f;
   c.cap2 = 0.f;
-  c.slope2 = 0.f;
+  c.slope = 0.f;
   if constexpr (CAP) {
     c.arg = rsqrt_d / softcap;
     c.mul = 2.f * kOptLog2e * c.arg;
     c.cap2 = softcap * kOptLog2e;
   }
-  if constexpr (BIAS) c.slope2 = slope * kOptLog2e;
+  if constexpr (BIAS) c.slope = CAP ? slope * kOptLog2e : slope / rsqrt_d;
   return c;
 }
 
@@ -94,24 +94,17 @@ __device__ __forceinline__ float2 cap_r(float2 x, float mul) {
   return make_float2(fast_rcp(e.x), fast_rcp(e.y));
 }
 
-// x[i] <- x[i] mul - slope2 |d0 + i|, i < N: two multiply-adds per score for
-// either sign of the slope, which all rows share.  (One formula for both, the
-// sign a factor, takes a third: a causal forward over 16,384 tokens and 16
-// heads 939 us against 877 us.  Where all distances of a block have one sign,
-// packed multiply-adds of two scores need fewer, but the longer code took 37.7
-// us against 35.9 us for 4 x 1037 tokens and 16 heads, and 860 us for the other.)
+// x[i] <- x[i] - slope |d0 + i|, i < N, for either sign of the slope.  The
+// distance is exact (below 2^24), so the bias has one rounding of its own size;
+// |slope i + slope d0|, the second product formed once, is off by a rounding of
+// 127 slopes next to the query itself (1e-5 of a log-sum-exp for a slope of 2)
+// and was no faster: a causal forward over 16,384 tokens and 16 heads 884 us
+// against 867 us, 4 x 1037 tokens the same.  Products with an absolute value
+// taken off them, one branch per sign, took 987 us, packed 1006 us.
 template <int N>
-__device__ __forceinline__ void bias_scores(float* x, float mul, float slope2, float d0) {
-  const float base = slope2 * d0;
-  if (slope2 >= 0.f) {
+__device__ __forceinline__ void bias_scores(float* x, float slope, float d0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      x[i] = fmaf(x[i], mul, -fabsf(fmaf(slope2, static_cast<float>(i), base)));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      x[i] = fmaf(x[i], mul, fabsf(fmaf(slope2, static_cast<float>(i), base)));
-  }
+  for (int i = 0; i < N; ++i) x[i] = fmaf(-slope, fabsf(d0 + static_cast<float>(i)), x[i]);
 }
 
 // The table entry of this CTA (in dispatch order) and its head: `tables` has

@@ -600,8 +600,7 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
         // dz, pair for pair.
         uint32_t pp[16];
         const float d0 = static_cast<float>(c0 + grp * 32 - (r0 + t));  // query - key
-        // (in log2 units from here on, if there is no cap to form first)
-        if constexpr (BIAS && !CAP) bias_scores<32>(p, sc.mul, sc.slope2, d0);
+        if constexpr (BIAS && !CAP) bias_scores<32>(p, sc.slope, d0);
         float u_max = 0.f;  // the largest square of a visible raw score
         auto weights = [&](auto edge_c, auto small_c) {
           constexpr bool EDGE = decltype(edge_c)::value;
@@ -614,8 +613,8 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
               const int k = e + 2 * h;
               float2 add = h == 0 ? make_float2(-lv.x, -lv.y) : make_float2(-lv.z, -lv.w);
               if constexpr (BIAS && CAP) {
-                add.x = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(k)), add.x);
-                add.y = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(k + 1)), add.y);
+                add.x = fmaf(-sc.slope, fabsf(d0 + static_cast<float>(k)), add.x);
+                add.y = fmaf(-sc.slope, fabsf(d0 + static_cast<float>(k + 1)), add.y);
               }
               const float2 x = make_float2(p[k], p[k + 1]);
               float2 y;
@@ -632,8 +631,6 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
                   th = __ffma2_rn(cap_r(x, sc.mul), make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
                 }
                 y = __ffma2_rn(th, make_float2(sc.cap2, sc.cap2), add);
-              } else if constexpr (BIAS) {
-                y = __fadd2_rn(x, add);
               } else {
                 y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
               }
@@ -999,7 +996,7 @@ __global__ void __launch_bounds__(kOptDqThreads, 1)
       uint32_t dw[32];
       const float2 nd2 = make_float2(-my_d, -my_d);
       const float d0 = static_cast<float>(c0 - r);  // key - query
-      if constexpr (BIAS && !CAP) bias_scores<64>(sv, sc.mul, sc.slope2, d0);
+      if constexpr (BIAS && !CAP) bias_scores<64>(sv, sc.slope, d0);
       float u_max = 0.f;  // the largest square of a visible raw score
       auto gradients = [&](auto edge_c, auto small_c) {
         constexpr bool EDGE = decltype(edge_c)::value;
@@ -1008,8 +1005,8 @@ __global__ void __launch_bounds__(kOptDqThreads, 1)
         for (int e = 0; e < 64; e += 2) {
           float2 add = make_float2(-my_l2, -my_l2);
           if constexpr (BIAS && CAP) {
-            add.x = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(e)), add.x);
-            add.y = fmaf(-sc.slope2, fabsf(d0 + static_cast<float>(e + 1)), add.y);
+            add.x = fmaf(-sc.slope, fabsf(d0 + static_cast<float>(e)), add.x);
+            add.y = fmaf(-sc.slope, fabsf(d0 + static_cast<float>(e + 1)), add.y);
           }
           const float2 x = make_float2(sv[e], sv[e + 1]);
           const bool v0 = !EDGE || ((vis[e >> 5] >> (e & 31)) & 1u);
@@ -1026,8 +1023,6 @@ __global__ void __launch_bounds__(kOptDqThreads, 1)
             }
             th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
             y = __ffma2_rn(th, make_float2(sc.cap2, sc.cap2), add);
-          } else if constexpr (BIAS) {
-            y = __fadd2_rn(x, add);
           } else {
             y = __ffma2_rn(x, make_float2(sc.mul, sc.mul), add);
           }

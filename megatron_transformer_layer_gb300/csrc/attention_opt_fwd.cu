@@ -501,9 +501,10 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           for (int c = 0; c < 4; ++c) vis[c] = bit_range(first - 32 * c, end - 32 * c);
         }
         auto sees = [&](int i) { return ((vis[i >> 5] >> (i & 31)) & 1u) != 0; };
-        // With a bias the scores are formed here, in log2 units.  Without one
-        // they stay raw until the exponent: the scale is positive and the cap
-        // monotone, so the raw maximum gives the row's.
+        // With a cap and a bias the scores are formed here, in log2 units; a bias
+        // alone is taken off the raw scores.  Those stay raw until the exponent:
+        // the scale is positive and the cap monotone, so the raw maximum gives
+        // the row's.
         // A cap needs the lowest visible score too: whether the warp's visible
         // scores are far enough below it (masked ones must not decide how the
         // cap is formed).
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
               }
             }
           }
-          bias_scores<128>(x, CAP ? 1.f : sc.mul, sc.slope2, static_cast<float>(key0 - q));
+          bias_scores<128>(x, sc.slope, static_cast<float>(key0 - q));
         }
         if (cut) {
 #pragma unroll
@@ -572,12 +573,10 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           ok = false;
           break;
         }
-        if constexpr (!BIAS) {
-          if constexpr (CAP) {
-            if (mx > -INFINITY) mx = fmaf(cap_r(make_float2(mx, mx), sc.mul).x, m2cap2.x, sc.cap2);
-          } else {
-            mx *= sc.mul;
-          }
+        if constexpr (!CAP) {
+          mx *= sc.mul;
+        } else if constexpr (!BIAS) {
+          if (mx > -INFINITY) mx = fmaf(cap_r(make_float2(mx, mx), sc.mul).x, m2cap2.x, sc.cap2);
         }
         const float m_new = fmaxf(m, mx);
         // a row that has seen nothing yet (m = -infinity) has l = 0 and O = 0
@@ -624,9 +623,11 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));
           }
         };
-        if constexpr (BIAS) {
+        if constexpr (!CAP) {
+          exponentials(IntC<0>{}, BoolC<false>{});
+        } else if constexpr (BIAS) {
           exponentials(IntC<1>{}, BoolC<false>{});
-        } else if constexpr (CAP) {
+        } else {
           if (small) {
             if (cut)
               exponentials(IntC<2>{}, BoolC<true>{});
@@ -636,8 +637,6 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             if (!cut) vis[0] = vis[1] = vis[2] = vis[3] = 0xFFFFFFFFu;
             exponentials(IntC<3>{}, BoolC<true>{});
           }
-        } else {
-          exponentials(IntC<0>{}, BoolC<false>{});
         }
         const float2 s01 = __fadd2_rn(__fadd2_rn(sm2[0], sm2[1]), __fadd2_rn(sm2[2], sm2[3]));
         l += s01.x + s01.y;

@@ -29,6 +29,11 @@ def test_negative_slopes_at_ragged_lengths(s, kind, cap, d):
     with_slopes(kind, 1, s, d, cap, [-1.0, -0.25, -0.5]).check()
 
 
+@pytest.mark.parametrize("kind", ["documents", "prefix", "any"])
+def test_negative_slopes_over_sequences_and_masks(kind):
+    with_slopes(kind, 2, 333, 64, 0.0, [-2.0, 0.5]).check()
+
+
 @pytest.mark.parametrize("cap", [0.0, 5.0])
 def test_steep_negative_slopes(cap):
     """Rows of nearly one key.  dz is then the small difference of dP and delta,
