@@ -502,8 +502,9 @@ __global__ void __launch_bounds__(kOptKvThreads, 1)
     auto stage_query = [&](int st) {
       have = false;
       if (grp != 0) return;
-      const int first = min(max(q_lo - q_r0, 0), 128);
-      const int end = min(max(min(q_hi, s) - q_r0, 0), 128);
+      // (the bounds, any 32-bit integers, cut to the sequence first)
+      const int first = min(max(max(q_lo, 0) - q_r0, 0), 128);
+      const int end = min(max(max(min(q_hi, s), 0) - q_r0, 0), 128);
       const int range = q_in ? first | (end << 8) : 128 << 8;
       sL[st * 128 + t] = q_in ? q_lse * kOptLog2e : INFINITY;
       sD[st * 128 + t] = q_in ? q_delta : 0.f;
@@ -959,8 +960,8 @@ __global__ void __launch_bounds__(kOptDqThreads, 1)
       const int64_t hrow = (static_cast<int64_t>(bi) * H + hh) * s;
       my_l2 = A.lse[hrow + r] * kOptLog2e;
       my_d = A.delta[hrow + r];
-      lo = A.key_lo[static_cast<int64_t>(bi) * s + r];
-      hi = min(A.key_hi[static_cast<int64_t>(bi) * s + r], s);
+      lo = max(A.key_lo[static_cast<int64_t>(bi) * s + r], 0);
+      hi = max(min(A.key_hi[static_cast<int64_t>(bi) * s + r], s), 0);
     }
     const CapPoly poly = cap_poly(1.f, sc.arg);
     const float cap_limit = cap_small_limit(sc.arg);

@@ -461,7 +461,9 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       const int halves = it.entry.w;
       if (halves < 0) break;
       const int q = it.entry.y * 128 + row, k_lo = it.entry.z;
-      const int row_lo = lo, row_hi = q < s ? min(hi, s) : hi;
+      // cut to the sequence (a caller's bounds are any 32-bit integers, from which
+      // nothing may be subtracted)
+      const int row_lo = max(lo, 0), row_hi = q < s ? max(min(hi, s), 0) : hi;
       const ScoreConst sc =
           score_const<CAP, BIAS>(rsqrtf(static_cast<float>(D)), A.softcap, slope);
       const CapPoly poly = cap_poly(sc.cap2, sc.arg);
