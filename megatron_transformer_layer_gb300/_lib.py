@@ -4,6 +4,11 @@ Argument marshalling only: every function here has the name of the C entry
 point it calls and forwards plain integers (device pointers, sizes, a
 cudaStream_t handle).  Anything with a ``data_ptr()`` method (a torch tensor)
 is accepted where a pointer is expected.  No computation happens in Python.
+
+The index and constant arrays of positions and masks (offsets, prefixes, key
+bounds, tables, positions, inverse frequencies, slopes) come as int64 or as
+expanded views easily, which a pointer does not show: given as tensors, their
+type, layout and length are checked here (TypeError, ValueError).
 """
 from __future__ import annotations
 
@@ -81,12 +86,14 @@ class mc_rotary_spec(ctypes.Structure):  # noqa: N801
 
 
 class mc_attention_options(ctypes.Structure):  # noqa: N801
+    lengths = (1 << 62,) * 3  # rows, table integers, slopes (make_attention_options)
     _fields_ = [("key_lo", ctypes.c_void_p), ("key_hi", ctypes.c_void_p),
                 ("tables", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
                 ("softcap", ctypes.c_float), ("causal", ctypes.c_int32)]
 
 
 class mc_layer_rotary(ctypes.Structure):  # noqa: N801
+    length = 1 << 62  # of positions (make_layer_rotary)
     _fields_ = [("spec", mc_rotary_spec), ("positions", ctypes.c_void_p),
                 ("inv_freq", ctypes.c_void_p)]
 
@@ -385,6 +392,44 @@ def _ref(struct):
     return None if struct is None else ctypes.byref(struct)
 
 
+_TYPES = {}  # torch's types by name, filled when a tensor first comes
+
+
+def _array(x, what, dtype, n):
+    """Pointer of an array of at least n elements: a contiguous tensor on the GPU
+    of the torch type named `dtype`, or a bare pointer, which is not checked."""
+    if x is None:
+        return None
+    try:
+        if x.dtype is _TYPES[dtype] and x.is_contiguous() and x.numel() >= n and x.is_cuda:
+            return x.data_ptr()
+    except (AttributeError, KeyError):  # no tensor, or the first one
+        pass
+    return _other_array(x, what, dtype, n)
+
+
+def _other_array(x, what, dtype, n):
+    if isinstance(x, int):
+        return x
+    import torch
+    _TYPES[dtype] = getattr(torch, dtype)
+    if isinstance(x, torch.Tensor):
+        if x.dtype is not _TYPES[dtype]:
+            raise TypeError(f"{what}: {dtype} expected, got {x.dtype}")
+        if not x.is_contiguous():
+            raise ValueError(f"{what}: a contiguous tensor expected, got strides {x.stride()}")
+        if x.numel() < n:
+            raise ValueError(f"{what}: {n} elements expected, got {x.numel()}")
+        if not x.is_cuda:
+            raise ValueError(f"{what}: a tensor on the GPU expected, got one on {x.device}")
+    return x.data_ptr()
+
+
+def _length(x):
+    """Elements of a tensor; of what is not one, as many as it takes."""
+    return x.numel() if hasattr(x, "numel") else 1 << 62
+
+
 def make_rotary_spec(rot_dim, sections=None, interleaved_pairs=False, interleaved_axes=False):
     """`sections`: pairs of each axis (default: one axis).  `interleaved_pairs`:
     pairs are neighbours (2p, 2p + 1); `interleaved_axes`: axes dealt in turn."""
@@ -398,18 +443,51 @@ def make_rotary_spec(rot_dim, sections=None, interleaved_pairs=False, interleave
 
 
 def make_layer_rotary(spec, positions, inv_freq):
-    """Keeps a reference to the tensors it points to."""
-    out = mc_layer_rotary(spec, _ptr(positions), _ptr(inv_freq))
+    """positions: int32 [axes, tokens], inv_freq: float32 [rot_dim / 2].  Keeps a
+    reference to the tensors it points to."""
+    out = mc_layer_rotary(spec, _array(positions, "positions", "int32", 0),
+                          _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2))
     out.tensors = (positions, inv_freq)
+    out.length = _length(positions)
     return out
 
 
 def make_attention_options(key_lo, key_hi, tables, slopes=None, softcap=0.0, causal=True):
-    """Keeps a reference to the tensors it points to."""
-    out = mc_attention_options(_ptr(key_lo), _ptr(key_hi), _ptr(tables), _ptr(slopes),
+    """key_lo, key_hi, tables: int32, slopes: float32 [heads].  Keeps a reference
+    to the tensors it points to."""
+    out = mc_attention_options(_array(key_lo, "key_lo", "int32", 0),
+                               _array(key_hi, "key_hi", "int32", 0),
+                               _array(tables, "tables", "int32", 0),
+                               _array(slopes, "slopes", "float32", 0),
                                float(softcap), 1 if causal else 0)
     out.tensors = (key_lo, key_hi, tables, slopes)
+    out.lengths = (min(_length(key_lo), _length(key_hi)), _length(tables), _length(slopes))
     return out
+
+
+def _options(options, micro_batch, seq_len, heads):
+    """options for a call of this shape, which its arrays must cover."""
+    if options is None:
+        return None
+    rows, tables, slopes = options.lengths
+    if rows < micro_batch * seq_len:
+        raise ValueError(f"key_lo, key_hi: {micro_batch * seq_len} elements expected, got {rows}")
+    if tables < 8 * micro_batch * ((seq_len + 127) // 128):
+        raise ValueError(f"tables: {8 * micro_batch * ((seq_len + 127) // 128)} elements expected, "
+                         f"got {tables}")
+    if slopes < heads:
+        raise ValueError(f"slopes: {heads} elements expected, got {slopes}")
+    return ctypes.byref(options)
+
+
+def _rotary(rotary, shape):
+    """rotary for a layer of this shape, which its positions must cover."""
+    if rotary is None:
+        return None
+    n = rotary.spec.axes * shape.micro_batch * shape.seq_len
+    if rotary.length < n:
+        raise ValueError(f"positions: {n} elements expected, got {rotary.length}")
+    return ctypes.byref(rotary)
 
 
 def _is_bf16(x):
@@ -426,8 +504,10 @@ def mc_rotary_forward(x, out, tokens, heads, head_dim, ld_in, ld_out, positions,
     if out.dtype != x.dtype:
         raise TypeError(f"rotary positions: {x.dtype} in, {out.dtype} out")
     return lib().mc_rotary_forward(_ptr(x), _ptr(out), _is_bf16(x), tokens, heads, head_dim, ld_in,
-                                   ld_out, _ptr(positions), _ptr(inv_freq), ctypes.byref(spec),
-                                   _ptr(status), _stream(stream))
+                                   ld_out, _array(positions, "positions", "int32",
+                                                  spec.axes * tokens),
+                                   _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2),
+                                   ctypes.byref(spec), _ptr(status), _stream(stream))
 
 
 def mc_rotary_backward(dout, din, tokens, heads, head_dim, ld_dout, ld_din, positions, inv_freq,
@@ -435,7 +515,9 @@ def mc_rotary_backward(dout, din, tokens, heads, head_dim, ld_dout, ld_din, posi
     if din.dtype != dout.dtype:
         raise TypeError(f"rotary positions: {dout.dtype} in, {din.dtype} out")
     return lib().mc_rotary_backward(_ptr(dout), _ptr(din), _is_bf16(dout), tokens, heads, head_dim,
-                                    ld_dout, ld_din, _ptr(positions), _ptr(inv_freq),
+                                    ld_dout, ld_din, _array(positions, "positions", "int32",
+                                                            spec.axes * tokens),
+                                    _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2),
                                     ctypes.byref(spec), _ptr(status), _stream(stream))
 
 
@@ -445,22 +527,32 @@ def mc_attention_mask_table_ints(micro_batch, seq_len) -> int:
 
 def mc_attention_mask_documents(offsets, n_docs, prefix, causal, window, micro_batch, seq_len,
                                 key_lo, key_hi, tables, status=None, stream=None) -> int:
-    return lib().mc_attention_mask_documents(_ptr(offsets), n_docs, _ptr(prefix), causal, window,
-                                             micro_batch, seq_len, _ptr(key_lo), _ptr(key_hi),
-                                             _ptr(tables), _ptr(status), _stream(stream))
+    rows, ints = micro_batch * seq_len, 8 * micro_batch * ((seq_len + 127) // 128)
+    return lib().mc_attention_mask_documents(_array(offsets, "offsets", "int32", n_docs + 1), n_docs,
+                                             _array(prefix, "prefix", "int32", n_docs), causal,
+                                             window, micro_batch, seq_len,
+                                             _array(key_lo, "key_lo", "int32", rows),
+                                             _array(key_hi, "key_hi", "int32", rows),
+                                             _array(tables, "tables", "int32", ints),
+                                             _ptr(status), _stream(stream))
 
 
 def mc_attention_mask_intervals(micro_batch, seq_len, key_lo, key_hi, tables, status=None,
                                 stream=None) -> int:
-    return lib().mc_attention_mask_intervals(micro_batch, seq_len, _ptr(key_lo), _ptr(key_hi),
-                                             _ptr(tables), _ptr(status), _stream(stream))
+    rows, ints = micro_batch * seq_len, 8 * micro_batch * ((seq_len + 127) // 128)
+    return lib().mc_attention_mask_intervals(micro_batch, seq_len,
+                                             _array(key_lo, "key_lo", "int32", rows),
+                                             _array(key_hi, "key_hi", "int32", rows),
+                                             _array(tables, "tables", "int32", ints),
+                                             _ptr(status), _stream(stream))
 
 
 def mc_attention_forward_opt(qkv, o, lse, micro_batch, seq_len, heads, head_dim, options,
                              status=None, stream=None) -> int:
     return lib().mc_attention_forward_opt(_ptr(qkv), _ptr(o), _ptr(lse), micro_batch, seq_len,
-                                          heads, head_dim, _ref(options), _ptr(status),
-                                          _stream(stream))
+                                          heads, head_dim,
+                                          _options(options, micro_batch, seq_len, heads),
+                                          _ptr(status), _stream(stream))
 
 
 def mc_attention_backward_opt_ws_bytes(micro_batch, seq_len, heads, head_dim, options) -> int:
@@ -473,8 +565,9 @@ def mc_attention_backward_opt(qkv, o, lse, dout, dqkv, delta, micro_batch, seq_l
                               status=None, stream=None) -> int:
     return lib().mc_attention_backward_opt(_ptr(qkv), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dqkv),
                                            _ptr(delta), micro_batch, seq_len, heads, head_dim,
-                                           _ref(options), _ptr(ds_workspace), ds_workspace_bytes,
-                                           _ptr(status), _stream(stream))
+                                           _options(options, micro_batch, seq_len, heads),
+                                           _ptr(ds_workspace), ds_workspace_bytes, _ptr(status),
+                                           _stream(stream))
 
 
 def mc_layer_workspace_bytes_opt(shape, attention) -> int:
@@ -483,15 +576,21 @@ def mc_layer_workspace_bytes_opt(shape, attention) -> int:
 
 def mc_layer_forward_opt(shape, weights, rotary, attention, x, y, saved, ws, ws_bytes,
                          stream=None) -> int:
-    return lib().mc_layer_forward_opt(ctypes.byref(shape), ctypes.byref(weights), _ref(rotary),
-                                      _ref(attention), _ptr(x), _ptr(y), _ptr(saved), _ptr(ws),
-                                      ws_bytes, _stream(stream))
+    return lib().mc_layer_forward_opt(ctypes.byref(shape), ctypes.byref(weights),
+                                      _rotary(rotary, shape),
+                                      _options(attention, shape.micro_batch, shape.seq_len,
+                                               shape.heads),
+                                      _ptr(x), _ptr(y), _ptr(saved), _ptr(ws), ws_bytes,
+                                      _stream(stream))
 
 
 def mc_layer_backward_opt(shape, weights, rotary, attention, x, dy, saved, dx, grads, ws, ws_bytes,
                           stream=None) -> int:
-    return lib().mc_layer_backward_opt(ctypes.byref(shape), ctypes.byref(weights), _ref(rotary),
-                                       _ref(attention), _ptr(x), _ptr(dy), _ptr(saved), _ptr(dx),
+    return lib().mc_layer_backward_opt(ctypes.byref(shape), ctypes.byref(weights),
+                                       _rotary(rotary, shape),
+                                       _options(attention, shape.micro_batch, shape.seq_len,
+                                                shape.heads),
+                                       _ptr(x), _ptr(dy), _ptr(saved), _ptr(dx),
                                        ctypes.byref(grads), _ptr(ws), ws_bytes, _stream(stream))
 
 
