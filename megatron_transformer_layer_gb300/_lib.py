@@ -8,7 +8,9 @@ is accepted where a pointer is expected.  No computation happens in Python.
 The index and constant arrays of positions and masks (offsets, prefixes, key
 bounds, tables, positions, inverse frequencies, slopes) come as int64 or as
 expanded views easily, which a pointer does not show: given as tensors, their
-type, layout and length are checked here (TypeError, ValueError).
+type, layout and length are checked here (TypeError, ValueError).  Without a
+`stream` those calls go to torch's current one; the other stage calls to the
+legacy default stream, which side streams are not ordered with.
 """
 from __future__ import annotations
 
@@ -425,6 +427,15 @@ def _other_array(x, what, dtype, n):
     return x.data_ptr()
 
 
+def _on(stream, x):
+    """A call's stream: without one, torch's current stream of x's device, as the
+    layer's calls (for a bare pointer the legacy default stream)."""
+    if stream is None and getattr(x, "is_cuda", False):
+        import torch
+        return torch.cuda.current_stream(x.device).cuda_stream
+    return _stream(stream)
+
+
 def _length(x):
     """Elements of a tensor; of what is not one, as many as it takes."""
     return x.numel() if hasattr(x, "numel") else 1 << 62
@@ -507,7 +518,7 @@ def mc_rotary_forward(x, out, tokens, heads, head_dim, ld_in, ld_out, positions,
                                    ld_out, _array(positions, "positions", "int32",
                                                   spec.axes * tokens),
                                    _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2),
-                                   ctypes.byref(spec), _ptr(status), _stream(stream))
+                                   ctypes.byref(spec), _ptr(status), _on(stream, x))
 
 
 def mc_rotary_backward(dout, din, tokens, heads, head_dim, ld_dout, ld_din, positions, inv_freq,
@@ -518,7 +529,7 @@ def mc_rotary_backward(dout, din, tokens, heads, head_dim, ld_dout, ld_din, posi
                                     ld_dout, ld_din, _array(positions, "positions", "int32",
                                                             spec.axes * tokens),
                                     _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2),
-                                    ctypes.byref(spec), _ptr(status), _stream(stream))
+                                    ctypes.byref(spec), _ptr(status), _on(stream, dout))
 
 
 def mc_attention_mask_table_ints(micro_batch, seq_len) -> int:
@@ -534,7 +545,7 @@ def mc_attention_mask_documents(offsets, n_docs, prefix, causal, window, micro_b
                                              _array(key_lo, "key_lo", "int32", rows),
                                              _array(key_hi, "key_hi", "int32", rows),
                                              _array(tables, "tables", "int32", ints),
-                                             _ptr(status), _stream(stream))
+                                             _ptr(status), _on(stream, key_lo))
 
 
 def mc_attention_mask_intervals(micro_batch, seq_len, key_lo, key_hi, tables, status=None,
@@ -544,7 +555,7 @@ def mc_attention_mask_intervals(micro_batch, seq_len, key_lo, key_hi, tables, st
                                              _array(key_lo, "key_lo", "int32", rows),
                                              _array(key_hi, "key_hi", "int32", rows),
                                              _array(tables, "tables", "int32", ints),
-                                             _ptr(status), _stream(stream))
+                                             _ptr(status), _on(stream, key_lo))
 
 
 def mc_attention_forward_opt(qkv, o, lse, micro_batch, seq_len, heads, head_dim, options,
@@ -552,7 +563,7 @@ def mc_attention_forward_opt(qkv, o, lse, micro_batch, seq_len, heads, head_dim,
     return lib().mc_attention_forward_opt(_ptr(qkv), _ptr(o), _ptr(lse), micro_batch, seq_len,
                                           heads, head_dim,
                                           _options(options, micro_batch, seq_len, heads),
-                                          _ptr(status), _stream(stream))
+                                          _ptr(status), _on(stream, qkv))
 
 
 def mc_attention_backward_opt_ws_bytes(micro_batch, seq_len, heads, head_dim, options) -> int:
@@ -567,7 +578,7 @@ def mc_attention_backward_opt(qkv, o, lse, dout, dqkv, delta, micro_batch, seq_l
                                            _ptr(delta), micro_batch, seq_len, heads, head_dim,
                                            _options(options, micro_batch, seq_len, heads),
                                            _ptr(ds_workspace), ds_workspace_bytes, _ptr(status),
-                                           _stream(stream))
+                                           _on(stream, qkv))
 
 
 def mc_layer_workspace_bytes_opt(shape, attention) -> int:
@@ -581,7 +592,7 @@ def mc_layer_forward_opt(shape, weights, rotary, attention, x, y, saved, ws, ws_
                                       _options(attention, shape.micro_batch, shape.seq_len,
                                                shape.heads),
                                       _ptr(x), _ptr(y), _ptr(saved), _ptr(ws), ws_bytes,
-                                      _stream(stream))
+                                      _on(stream, x))
 
 
 def mc_layer_backward_opt(shape, weights, rotary, attention, x, dy, saved, dx, grads, ws, ws_bytes,
@@ -591,7 +602,7 @@ def mc_layer_backward_opt(shape, weights, rotary, attention, x, dy, saved, dx, g
                                        _options(attention, shape.micro_batch, shape.seq_len,
                                                 shape.heads),
                                        _ptr(x), _ptr(dy), _ptr(saved), _ptr(dx),
-                                       ctypes.byref(grads), _ptr(ws), ws_bytes, _stream(stream))
+                                       ctypes.byref(grads), _ptr(ws), ws_bytes, _on(stream, x))
 
 
 def mc_selftest_bounds_check(index, extent, buf, status, stream=None) -> int:
