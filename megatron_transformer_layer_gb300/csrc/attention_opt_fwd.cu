@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
   uint64_t* v_full = bars + 6;     // [4] per half-tile slot (VS used)
   uint64_t* v_empty = bars + 10;   // [4]  after the half's PV steps
   uint64_t* s_full = bars + 14;    // S in TMEM
-  uint64_t* s_free = bars + 15;    // the softmax holds S in registers (256 threads, 8 warps)
+  uint64_t* s_free = bars + 15;    // the softmax holds S in registers (256 threads)
   uint64_t* p_full = bars + 16;    // P in TMEM (256 threads)
   uint64_t* pv_done = bars + 17;   // O += P V complete
   uint64_t* o_free = bars + 18;    // the item's O is in registers (256 threads)
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, CAP ? 8 : 256);
+    mbar_init(s_free, 256);
     mbar_init(p_full, 256);
     mbar_init(pv_done, 1);
     mbar_init(o_free, 256);
@@ -483,13 +483,8 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
           tmem_ld_32x32b_x32_nowait(tS + lane_off + half * 128 + 32 * c, x + 32 * c);
         tmem_ld_wait();
         tc_fence_before();
-        // One arrival per warp leaves a capped softmax more issue slots (1022
-        // against 1040 us over 16,384 tokens), but a warp's own barrier costs
-        // the others as much or more (712 against 703 us).
-        if constexpr (CAP)
-          mbar_arrive_warp(s_free, lane);
-        else
-          mbar_arrive(s_free);
+        // (one arrival per warp: the same with a cap, 712 against 703 us without)
+        mbar_arrive(s_free);
         const int key0 = k_lo + j * kOptKeys + half * 128;
         // ---- keys [first, end) of this half are visible (the last block may lack
         //      its second half, whose S is an older one)
