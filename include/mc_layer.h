@@ -496,7 +496,8 @@ typedef struct mc_rotary_spec {
  * behind the heads in a row is neither read nor written): fp32, or bf16 when
  * is_bf16 != 0, rounded once.  Over the Q and K of a packed Q|K|V row:
  * heads = 2 H, ld = 3a.  positions: int32 [axes, tokens], any value (angles
- * are formed in 64 bits); inv_freq: fp32 [rot_dim / 2], finite.  out == in
+ * are formed in 64 bits); inv_freq: fp32 [rot_dim / 2], finite and, for the
+ * angles to be exact, below 2^64 in size.  out == in
  * (with the same stride) turns in place; otherwise they must not overlap.
  * rot_dim <= 512, head_dim <= 1024, heads * head_dim <= 2^22 (else
  * MC_ERR_UNSUPPORTED).  Vectors of 16 bytes are used where rot_dim / 2,
@@ -559,12 +560,18 @@ int mc_attention_mask_intervals(int32_t micro_batch, int32_t seq_len, const int3
  *                    either sign; constants: they get no gradient)
  * then the softmax over the keys of the query's interval.  causal != 0 states
  * that no interval reaches past its own query (key_hi[i] <= i + 1), which
- * halves the backward's workspace; an interval that does is then reported as
- * MC_ERR_DEVICE_BOUNDS in `status` and the gradients are not valid. */
+ * halves the backward's workspace: it has no tile for a key block behind the
+ * query's 128-row block.  A mask that needs one is reported as
+ * MC_ERR_DEVICE_BOUNDS in `status` by a backward pass with a workspace, whose
+ * gradients are then not valid; nothing else reads `causal`, and what the mask
+ * shows within its own block, or without a workspace, is computed as it is. */
 typedef struct mc_attention_options {
   const int32_t* key_lo;
   const int32_t* key_hi;
-  const int32_t* tables; /* made from key_lo / key_hi for the same shape */
+  /* made from key_lo / key_hi for the same shape: of tables that were not, the
+   * sequence and block numbers are checked (MC_ERR_DEVICE_BOUNDS) and the ranges
+   * cut to the sequence, but rows that they leave out are not written */
+  const int32_t* tables;
   const float* slopes;   /* or NULL */
   float softcap;         /* 0: none; else 2^-16 .. 2^16 */
   int32_t causal;
@@ -573,9 +580,10 @@ typedef struct mc_attention_options {
 /* mc_attention_forward over an interval mask: same layouts, types and errors
  * (lse is -infinity for a row that sees nothing).  MC_ERR_ARGUMENT for a
  * softcap that is neither 0 nor in its range.  Values in rows that a query
- * does not see have no influence as long as they are finite: a NaN or infinity
- * in K or V can reach the other queries of blocks that hold it, and in the
- * backward pass one in Q or dO the other keys. */
+ * does not see have no influence as long as they are finite (in the backward
+ * pass: and the products dO V with them, in 32 bits): a NaN or infinity in K or
+ * V can reach the other queries of blocks that hold it, and in the backward
+ * pass one in Q or dO the other keys. */
 int mc_attention_forward_opt(const uint16_t* qkv, uint16_t* o, float* lse, int32_t micro_batch,
                              int32_t seq_len, int32_t heads, int32_t head_dim,
                              const mc_attention_options* options, int* status, void* stream);

@@ -1,6 +1,10 @@
 // Entry points of the attention over interval masks: argument checks and the
 // launch order.  The kernels are in attention_opt_fwd.cu and
 // attention_opt_bwd.cu; the delta = rowsum(dO O) pre-pass is attention.cu's.
+// It takes the stored bf16 O, each element of which is off by up to 2^-8 of
+// itself, and sums in 32 bits: the exact sum of P dP would need every score of a
+// row before its first dz, a pass of its own over S and dP.  The error it leaves
+// in dz shows most in rows that see few keys, where O averages little.
 #include <cuda_runtime.h>
 
 #include "mc_layer_internal.h"

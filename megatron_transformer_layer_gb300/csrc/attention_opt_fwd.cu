@@ -19,12 +19,23 @@
 //
 // Bound by the products (2870 clocks per block at D = 128) where nothing is
 // capped or biased: causal over 16,384 tokens and 16 heads 703 us, 0.82 of the
-// measured matrix rate.  A cap's or bias's multiply-adds exceed them: 1022 and
-// 890 us.  Over short documents (4096 tokens, 64 heads, 88 us, 3.0 TB/s) the
-// partly masked blocks, the wait for an item's first S and the stores, 32 bytes
-// per clock and SM, show.  128-key blocks in two CTAs per SM and softmax warps
-// that take two passes were slower, as were sixteen softmax warps of 64 scores
-// (packed 105 us, capped 1097 us) and storing O behind the next P (91, 1120 us).
+// measured matrix rate.  With a cap (1035 to 1058 us, 4870 clocks per block) or a
+// bias (867 us) neither the tensor pipe (45% active with a cap) nor the issue
+// slots are full: the cap's multiply-adds take 1536 clocks and the exponentials
+// 1024, on different units, and about 1600 are waits, the exchange of maxima and
+// transfers, which nothing overlaps, because both warps of a lane quarter hold
+// halves of the same rows and wait at the same barriers.  Over short documents
+// (4096 tokens, 64 heads, 88 us, 3.0 TB/s) the partly masked blocks, the wait for
+// an item's first S and the stores, 32 bytes per clock and SM, show.  128-key
+// blocks in two CTAs per SM and softmax warps that take two passes were slower,
+// as were sixteen softmax warps of 64 scores (packed 105 us, capped 1097 us) and
+// storing O behind the next P (91, 1120 us).
+//
+// P is rounded to bf16, by at most 2^-8 of itself: an operand of a tcgen05
+// product has the type of the other one, here V's.  The row sums take P before
+// that, sums and statistics are 32-bit, and O is rounded once more when stored.
+// Those two roundings are the kernel's whole error, 0.0017 to 0.0022 of the
+// result; with P in 32 bits, O's alone leaves 0.0016 to 0.0017.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(kOptFwdThreads, 1)
             if constexpr (CUT)  // (the cap of -infinity is not -infinity)
               pv = make_float2(sees(2 * i) ? pv.x : 0.f, sees(2 * i + 1) ? pv.y : 0.f);
             sm2[i & 3] = __fadd2_rn(sm2[i & 3], pv);
-            x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));
+            x[i] = __uint_as_float(pack_bf16x2(pv.x, pv.y));  // V's type (see the top)
           }
         };
         if constexpr (!CAP) {

@@ -9,9 +9,11 @@
 // formed in integer arithmetic as turns in 64-bit fixed point (the float's 24
 // bits times 1 / 2 pi to 128 bits), and whole turns drop out of the product
 // with the position by the wrap of 64-bit integers.  A position of 2^31 leaves
-// an error of 2^-33 turns; sincospif gets 32 bits of the turn.  (The same in
-// 64-bit floats is exact enough too, but they run at 1/64 of the 32-bit rate
-// here.)
+// an error of 2^-33 turns for frequencies up to 2^64 (above, the 128 bits of
+// 1 / 2 pi run out).  What is left of the turn goes to sincospif as a 32-bit
+// float of half turns, below 1 and so off by at most 2^-25: 9.4e-8 radians, as
+// much as the cosine's own rounding.  (The same in 64-bit floats is exact enough
+// too, but they run at 1/64 of the 32-bit rate here.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kRotWarps * 32)
       const int tk = fast_div(i, A.div_pairs), p = i - tk * A.pairs;
       const int64_t pos = positions[A.axis[p] * A.tokens + t0 + tk];
       const uint64_t w = static_cast<uint64_t>(A.inverse ? -pos : pos) * turns[p];
-      // the nearest 2^-32 of a turn, in half turns
+      // the nearest 2^-32 of a turn, in half turns (24 bits of it as a float)
       const int32_t x = static_cast<int32_t>(static_cast<uint32_t>((w + 0x80000000ull) >> 32));
       float s, c;
       sincospif(static_cast<float>(x) * 4.656612873077393e-10f, &s, &c);
