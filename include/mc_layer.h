@@ -631,6 +631,110 @@ int mc_layer_backward_opt(const mc_layer_shape* shape, const mc_layer_weights* w
                           const float* x, const float* dy, const void* saved, float* dx,
                           const mc_layer_grads* grads, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Norms of queries and keys, head by head, with rotary positions in the
+ * same pass.
+ *
+ * A head x of head_dim elements, with its gain g and shift c, becomes
+ *   y = (x - m) / sqrt(mean((x - m)^2) + eps) * g + c,
+ * m = mean(x) with MC_QK_NORM_CENTRED, else 0 (the root mean square alone), and
+ * y then turns as by mc_rotary_forward. */
+#define MC_QK_NORM_CENTRED 1u
+typedef struct mc_qk_norm {
+  const uint16_t *q_gain, *q_shift; /* bf16 [head_dim]; NULL: ones, zeros */
+  const uint16_t *k_gain, *k_shift;
+  float eps;                        /* 1e-12 .. 1 */
+  uint32_t flags;                   /* MC_QK_NORM_CENTRED or 0 */
+} mc_qk_norm;
+
+/* Norms and turns q_heads + k_heads heads of head_dim (at most 256) elements at
+ * the start of each of `tokens` rows: the first q_heads with the queries' gain
+ * and shift, the others with the keys' (either number may be 0: the queries of
+ * a cross attention lie in rows of their own).  Rows, types, positions and
+ * in-place use as mc_rotary_forward; spec NULL: nothing turns, positions and
+ * inv_freq are not read.  Sums are 32-bit: the squares of a head must not
+ * overflow there. */
+int mc_qk_norm_forward(const void* in, void* out, int32_t is_bf16, int64_t tokens,
+                       int32_t q_heads, int32_t k_heads, int32_t head_dim, int64_t ld_in,
+                       int64_t ld_out, const mc_qk_norm* norm, const int32_t* positions,
+                       const float* inv_freq, const mc_rotary_spec* spec, int* status,
+                       void* stream);
+
+/* Floats of device scratch of mc_qk_norm_backward.  0 for an invalid shape. */
+size_t mc_qk_norm_scratch_floats(int64_t tokens, int32_t q_heads, int32_t k_heads,
+                                 int32_t head_dim);
+
+/* The gradients of mc_qk_norm_forward from its input `in` and dout: din (which
+ * may be dout or in, with the same stride), and of the gains and shifts, fp32
+ * [head_dim], summed over tokens and heads in a fixed order (added to what is
+ * there when `accumulate` is non-zero).  A NULL gradient is not formed; `grads`
+ * may be NULL, and `scratch` when none is asked for.  A gradient of heads that
+ * the call does not have (q_heads or k_heads 0) is left as it is. */
+typedef struct mc_qk_norm_grads {
+  float *q_gain, *q_shift, *k_gain, *k_shift;
+} mc_qk_norm_grads;
+int mc_qk_norm_backward(const void* in, const void* dout, void* din, int32_t is_bf16,
+                        int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                        int64_t ld_in, int64_t ld_dout, int64_t ld_din, const mc_qk_norm* norm,
+                        const int32_t* positions, const float* inv_freq,
+                        const mc_rotary_spec* spec, const mc_qk_norm_grads* grads,
+                        int32_t accumulate, float* scratch, int* status, void* stream);
+
+/* ---- Attention to keys and values of another length (an encoder's states).
+ *
+ * `sequences` sequences; query row i of sequence n sees all of the sequence's
+ * keys:
+ *   O_i = sum_j softmax_j(scale q_i k_j) v_j.
+ * Sequence n owns the query rows [q_offsets[n], q_offsets[n + 1]) of Q and O
+ * and the key rows [kv_offsets[n], kv_offsets[n + 1]) of K and V (int32
+ * [sequences + 1], ascending; NULL: equal runs of the rows, which `sequences`
+ * must divide).  Of those the first q_lens[n] (kv_lens[n]; int32 [sequences],
+ * NULL: all) are real and the others padding: padded keys are seen by no
+ * query, and what K and V hold there (infinities and NaN too) has no
+ * influence; padded queries, and all queries of a sequence without keys, get O
+ * = 0 and a log-sum-exp of -infinity, and give no gradients.  Rows before the
+ * first and behind the last sequence are neither read nor written.  Offsets
+ * and lengths are cut to the rows that there are.
+ *
+ * Query head h (columns [h head_dim, (h + 1) head_dim) of a row) reads key head
+ * h / (heads / kv_heads); its rows are ld_q elements apart in Q, ld_o in O, and
+ * those of K and V ld_kv.  K and V of a packed projection K | V: v = k +
+ * kv_heads head_dim, ld_kv = 2 kv_heads head_dim.  max_q and max_kv bound the
+ * rows of a sequence (0: not known) where offsets are given; a sequence with
+ * more is reported as MC_ERR_DEVICE_BOUNDS and its rows beyond are not
+ * computed. */
+typedef struct mc_cross_attention {
+  int32_t sequences;
+  int32_t heads, kv_heads; /* kv_heads divides heads, by at most 128 */
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t q_rows, kv_rows; /* rows of Q and O, and of K and V */
+  int32_t max_q, max_kv;
+  int64_t ld_q, ld_kv, ld_o; /* multiples of 8; ld_q and ld_o of head_dim where kv_heads < heads */
+  const int32_t *q_offsets, *q_lens, *kv_offsets, *kv_lens;
+  float scale;             /* 0: 1 / sqrt(head_dim); else 2^-16 .. 2^16 */
+} mc_cross_attention;
+
+/* O bf16 [q_rows, ld_o] and lse fp32 [heads, q_rows] (natural log-sum-exp of
+ * the scaled scores). */
+int mc_attention_forward_cross(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                               uint16_t* o, float* lse, const mc_cross_attention* cross,
+                               int* status, void* stream);
+
+/* Bytes of the workspace of mc_attention_backward_cross: dz tiles of 32 KB per
+ * pair of 128-row blocks, of as many key heads as stay below 2 GB, of one at
+ * least.  0 for an invalid shape. */
+size_t mc_attention_backward_cross_ws_bytes(const mc_cross_attention* cross);
+
+/* dq, dk, dv (bf16, rows as Q, K and V: ld_q, ld_kv) from dout (rows as O) and
+ * the forward's o and lse.  dk and dv are summed over the query heads that
+ * share a key head; padded rows get zeros.  `delta` is fp32 scratch [heads,
+ * q_rows]; `ws` device memory of ws_bytes (16-byte aligned, less than
+ * mc_attention_backward_cross_ws_bytes -> MC_ERR_WORKSPACE). */
+int mc_attention_backward_cross(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                const uint16_t* o, const float* lse, const uint16_t* dout,
+                                uint16_t* dq, uint16_t* dk, uint16_t* dv, float* delta,
+                                const mc_cross_attention* cross, void* ws, size_t ws_bytes,
+                                int* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

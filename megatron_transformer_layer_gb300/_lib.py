@@ -100,6 +100,34 @@ class mc_layer_rotary(ctypes.Structure):  # noqa: N801
                 ("inv_freq", ctypes.c_void_p)]
 
 
+MC_QK_NORM_CENTRED = 1
+
+
+class mc_qk_norm(ctypes.Structure):  # noqa: N801
+    lengths = (1 << 62,) * 2  # shortest of the queries' and of the keys' arrays (make_qk_norm)
+    _fields_ = [("q_gain", ctypes.c_void_p), ("q_shift", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("k_shift", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class mc_qk_norm_grads(ctypes.Structure):  # noqa: N801
+    lengths = (1 << 62,) * 2
+    _fields_ = [("q_gain", ctypes.c_void_p), ("q_shift", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("k_shift", ctypes.c_void_p)]
+
+
+class mc_cross_attention(ctypes.Structure):  # noqa: N801
+    lengths = (1 << 62,) * 4  # of the four arrays (make_cross_attention)
+    _fields_ = [("sequences", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("q_rows", ctypes.c_int32), ("kv_rows", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("ld_q", ctypes.c_int64), ("ld_kv", ctypes.c_int64), ("ld_o", ctypes.c_int64),
+                ("q_offsets", ctypes.c_void_p), ("q_lens", ctypes.c_void_p),
+                ("kv_offsets", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -110,6 +138,8 @@ _SZ = ctypes.c_size_t
 
 _OPT = ctypes.POINTER(mc_attention_options)
 _ROT = ctypes.POINTER(mc_layer_rotary)
+_NORM = ctypes.POINTER(mc_qk_norm)
+_CROSS = ctypes.POINTER(mc_cross_attention)
 
 _SIGNATURES = {
     "mc_layer_check_shape": (_INT, [ctypes.POINTER(mc_layer_shape)]),
@@ -159,6 +189,16 @@ _SIGNATURES = {
     "mc_attention_backward_opt_ws_bytes": (_SZ, [_I32, _I32, _I32, _I32, _OPT]),
     "mc_attention_backward_opt": (_INT, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _OPT, _P,
                                          _SZ, _P, _P]),
+    "mc_qk_norm_forward": (_INT, [_P, _P, _I32, _I64, _I32, _I32, _I32, _I64, _I64, _NORM, _P, _P,
+                                  ctypes.POINTER(mc_rotary_spec), _P, _P]),
+    "mc_qk_norm_scratch_floats": (_SZ, [_I64, _I32, _I32, _I32]),
+    "mc_qk_norm_backward": (_INT, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I64, _I64, _I64,
+                                   _NORM, _P, _P, ctypes.POINTER(mc_rotary_spec),
+                                   ctypes.POINTER(mc_qk_norm_grads), _I32, _P, _P, _P]),
+    "mc_attention_forward_cross": (_INT, [_P, _P, _P, _P, _P, _CROSS, _P, _P]),
+    "mc_attention_backward_cross_ws_bytes": (_SZ, [_CROSS]),
+    "mc_attention_backward_cross": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _CROSS, _P, _SZ,
+                                           _P, _P]),
     "mc_layer_workspace_bytes_opt": (_SZ, [ctypes.POINTER(mc_layer_shape), _OPT]),
     "mc_layer_forward_opt": (_INT, [ctypes.POINTER(mc_layer_shape),
                                     ctypes.POINTER(mc_layer_weights), _ROT, _OPT, _P, _P, _P, _P,
@@ -530,6 +570,153 @@ def mc_rotary_backward(dout, din, tokens, heads, head_dim, ld_dout, ld_din, posi
                                                             spec.axes * tokens),
                                     _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2),
                                     ctypes.byref(spec), _ptr(status), _on(stream, dout))
+
+
+# ---- norms of queries and keys with their rotation
+
+def _norm_struct(cls, dtype, n, q_gain, q_shift, k_gain, k_shift, *rest):
+    arrays = (q_gain, q_shift, k_gain, k_shift)
+    names = ("q_gain", "q_shift", "k_gain", "k_shift")
+    out = cls(*[_array(x, w, dtype, n) for x, w in zip(arrays, names)], *rest)
+    out.tensors = arrays
+    out.lengths = tuple(min(_length(x) for x in arrays[2 * i: 2 * i + 2]) for i in range(2))
+    return out
+
+
+def make_qk_norm(q_gain=None, k_gain=None, q_shift=None, k_shift=None, eps=1e-5, centred=False):
+    """Gains and shifts: bfloat16 [head_dim], None for ones and zeros; `centred`
+    takes the mean off (LayerNorm).  Keeps a reference to the tensors."""
+    return _norm_struct(mc_qk_norm, "bfloat16", 0, q_gain, q_shift, k_gain, k_shift, float(eps),
+                        MC_QK_NORM_CENTRED if centred else 0)
+
+
+def make_qk_norm_grads(q_gain=None, k_gain=None, q_shift=None, k_shift=None):
+    """Where the gradients of the gains and shifts go: float32 [head_dim], None
+    for those that are not wanted.  Keeps a reference to the tensors."""
+    return _norm_struct(mc_qk_norm_grads, "float32", 0, q_gain, q_shift, k_gain, k_shift)
+
+
+def _norm_ref(struct, what, q_heads, k_heads, head_dim):
+    """struct for a call of these heads, which its arrays must cover."""
+    if struct is None:
+        return None
+    for n, used, of in zip(struct.lengths, (q_heads, k_heads), "qk"):
+        if used and n < head_dim:
+            raise ValueError(f"{what} of {of}: {head_dim} elements expected, got {n}")
+    return ctypes.byref(struct)
+
+
+def _turning(positions, inv_freq, spec, tokens):
+    if spec is None:
+        return None, None, None
+    return (_array(positions, "positions", "int32", spec.axes * tokens),
+            _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2), ctypes.byref(spec))
+
+
+def mc_qk_norm_forward(x, out, tokens, q_heads, k_heads, head_dim, ld_in, ld_out, norm,
+                       positions=None, inv_freq=None, spec=None, status=None, stream=None) -> int:
+    """Norms (and, with a spec, rotary positions) over q_heads + k_heads heads at
+    the start of each row of x (a bf16 or fp32 tensor; `out` of the same type, or
+    x itself)."""
+    if out.dtype != x.dtype:
+        raise TypeError(f"norms of queries and keys: {x.dtype} in, {out.dtype} out")
+    return lib().mc_qk_norm_forward(_ptr(x), _ptr(out), _is_bf16(x), tokens, q_heads, k_heads,
+                                    head_dim, ld_in, ld_out,
+                                    _norm_ref(norm, "norm", q_heads, k_heads, head_dim),
+                                    *_turning(positions, inv_freq, spec, tokens), _ptr(status),
+                                    _on(stream, x))
+
+
+def mc_qk_norm_scratch_floats(tokens, q_heads, k_heads, head_dim) -> int:
+    return lib().mc_qk_norm_scratch_floats(tokens, q_heads, k_heads, head_dim)
+
+
+def mc_qk_norm_backward(x, dout, din, tokens, q_heads, k_heads, head_dim, ld_in, ld_dout, ld_din,
+                        norm, positions=None, inv_freq=None, spec=None, grads=None, accumulate=0,
+                        scratch=None, status=None, stream=None) -> int:
+    """The gradients of mc_qk_norm_forward: din from x and dout (all of one
+    type), and those of the gains and shifts that `grads` asks for (scratch:
+    mc_qk_norm_scratch_floats float32)."""
+    if dout.dtype != x.dtype or din.dtype != x.dtype:
+        raise TypeError(f"norms of queries and keys: {x.dtype} in, {dout.dtype} and {din.dtype} "
+                        "for its gradients")
+    need = 0 if grads is None else mc_qk_norm_scratch_floats(tokens, q_heads, k_heads, head_dim)
+    return lib().mc_qk_norm_backward(_ptr(x), _ptr(dout), _ptr(din), _is_bf16(x), tokens, q_heads,
+                                     k_heads, head_dim, ld_in, ld_dout, ld_din,
+                                     _norm_ref(norm, "norm", q_heads, k_heads, head_dim),
+                                     *_turning(positions, inv_freq, spec, tokens),
+                                     _norm_ref(grads, "gradient", q_heads, k_heads, head_dim),
+                                     accumulate, _array(scratch, "scratch", "float32", need),
+                                     _ptr(status), _on(stream, x))
+
+
+# ---- attention to keys and values of another length
+
+def make_cross_attention(sequences, q_rows, kv_rows, heads, kv_heads, head_dim, ld_q=None,
+                         ld_kv=None, ld_o=None, q_offsets=None, q_lens=None, kv_offsets=None,
+                         kv_lens=None, max_q=0, max_kv=0, scale=0.0):
+    """Row strides default to the heads' own width.  Offsets int32 [sequences +
+    1], lengths int32 [sequences].  Keeps a reference to the tensors."""
+    arrays = (q_offsets, q_lens, kv_offsets, kv_lens)
+    names = ("q_offsets", "q_lens", "kv_offsets", "kv_lens")
+    out = mc_cross_attention(
+        sequences, heads, kv_heads, head_dim, q_rows, kv_rows, max_q, max_kv,
+        heads * head_dim if ld_q is None else ld_q, kv_heads * head_dim if ld_kv is None else ld_kv,
+        heads * head_dim if ld_o is None else ld_o,
+        *[_array(x, w, "int32", sequences + 1 - (i & 1)) for i, (x, w) in enumerate(zip(arrays, names))],
+        float(scale))
+    out.tensors = arrays
+    return out
+
+
+def _rows(x, what, rows, ld, width):
+    """Pointer of a bf16 tensor of rows that are ld elements apart, which it must
+    cover (a bare pointer is not checked)."""
+    if x is None or isinstance(x, int):
+        return x
+    if str(x.dtype) != "torch.bfloat16":
+        raise TypeError(f"{what}: bfloat16 expected, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{what}: a tensor on the GPU expected, got one on {x.device}")
+    if x.dim() != 2 or x.shape[0] < rows or x.shape[1] < width or x.stride(1) != 1 \
+            or (rows > 1 and x.stride(0) != ld):
+        raise ValueError(f"{what}: {rows} rows of {width} elements, {ld} apart, expected, got shape "
+                         f"{tuple(x.shape)}, strides {x.stride()}")
+    return x.data_ptr()
+
+
+def mc_attention_forward_cross(q, k, v, o, lse, cross, status=None, stream=None) -> int:
+    """Attention of the rows of q to those of k and v, see make_cross_attention
+    (bf16 tensors [rows, heads * head_dim] or views of wider rows; lse float32
+    [heads, q_rows])."""
+    return lib().mc_attention_forward_cross(
+        *_cross_rows(cross, q=q, k=k, v=v, o=o),
+        _array(lse, "lse", "float32", cross.heads * cross.q_rows), ctypes.byref(cross),
+        _ptr(status), _on(stream, q))
+
+
+def _cross_rows(c, **tensors):
+    got = []
+    for name, x in tensors.items():
+        of_kv = name in ("k", "v", "dk", "dv")
+        ld = c.ld_kv if of_kv else c.ld_q if name in ("q", "dq") else c.ld_o
+        got.append(_rows(x, name, c.kv_rows if of_kv else c.q_rows, ld,
+                         (c.kv_heads if of_kv else c.heads) * c.head_dim))
+    return got
+
+
+def mc_attention_backward_cross_ws_bytes(cross) -> int:
+    return lib().mc_attention_backward_cross_ws_bytes(ctypes.byref(cross))
+
+
+def mc_attention_backward_cross(q, k, v, o, lse, dout, dq, dk, dv, delta, cross, ws, ws_bytes,
+                                status=None, stream=None) -> int:
+    rows = _cross_rows(cross, q=q, k=k, v=v, o=o, dout=dout, dq=dq, dk=dk, dv=dv)
+    n = cross.heads * cross.q_rows
+    return lib().mc_attention_backward_cross(*rows[:4], _array(lse, "lse", "float32", n), *rows[4:],
+                                             _array(delta, "delta", "float32", n),
+                                             ctypes.byref(cross), _ptr(ws), ws_bytes, _ptr(status),
+                                             _on(stream, q))
 
 
 def mc_attention_mask_table_ints(micro_batch, seq_len) -> int:

@@ -62,6 +62,8 @@ enum ErrorSite : int {
   kSiteAttention = 20,
   kSiteRotary = 21,
   kSiteMask = 22,
+  kSiteQkNorm = 23,
+  kSiteCross = 24,
   kSiteSelfTest = 30,
 };
 
@@ -286,6 +288,26 @@ void rotary_axes(const mc_rotary_spec* spec, uint8_t* axis);
 int launch_rotary(const void* in, void* out, bool bf16, int64_t tokens, int heads, int head_dim,
                   int64_t ld_in, int64_t ld_out, const int32_t* positions, const float* inv_freq,
                   const mc_rotary_spec* spec, bool inverse, int* status, cudaStream_t stream);
+
+// Norms of queries and keys with their rotation (qk_norm.cu).
+struct QkNormCall {
+  const void *in, *dout;
+  void* out;  // backward: din
+  bool bf16, backward;
+  int64_t tokens, ld_in, ld_dout, ld_out;
+  int q_heads, k_heads, head_dim;
+  const mc_qk_norm* norm;
+  const int32_t* positions;
+  const float* inv_freq;
+  const mc_rotary_spec* spec;  // or NULL
+  const mc_qk_norm_grads* grads;
+  int accumulate;
+  float* scratch;
+  int* status;
+};
+int check_qk_norm(const mc_qk_norm* norm);
+size_t qk_norm_scratch_floats(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim);
+int launch_qk_norm(const QkNormCall& q, cudaStream_t stream);
 
 // Attention over an interval mask with optional score cap and distance bias
 // (attention_opt.cu: checks and dispatch; attention_opt_fwd.cu,

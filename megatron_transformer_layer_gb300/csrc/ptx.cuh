@@ -274,6 +274,24 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, int2 v) {
                : "memory");
 }
 
+// Loads from a shared::cluster address.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Arrive on an mbarrier given by its shared::cluster address (this CTA's or
 // another CTA's of the cluster).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
