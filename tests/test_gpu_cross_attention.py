@@ -84,61 +84,104 @@ class Problem:
         blank = ~np.isfinite(lse) & owned
         assert (glse[blank] == -np.inf).all()
         if seen.any():
-            off = np.abs(glse - lse)[seen] / ltol[seen]
+            off = np.abs(glse[seen] - lse[seen]) / ltol[seen]
             assert off.max() <= 1, f"lse: {off.max():.3g} of the tolerance"
         return self
 
+    def backward(self):
+        """dq, dk, dv [rows, ...] of NaN-free buffers whose other places stay as they were."""
+        c = self.cross
+        self.dq_all = torch.full_like(self.q_all, KEEP)
+        self.dkv_all = torch.full_like(self.kv_all, KEEP)
+        delta = torch.empty(self.heads, self.q_rows, device=DEV)
+        n = L.mc_attention_backward_cross_ws_bytes(c)
+        ws = torch.full((n + 256,), 0xff, dtype=torch.uint8, device=DEV)  # NaN
+        st = status()
+        dk, dv = self.dkv_all[:, : self.akv], self.dkv_all[:, self.akv: 2 * self.akv]
+        assert L.mc_attention_backward_cross(self.q, self.k, self.v, self.o, self.lse, self.dout,
+                                             self.dq_all[:, : self.a], dk, dv, delta, c, ws, n,
+                                             st) == 0
+        check_status(st)
+        assert (ws[n:] == 0xff).all()
+        return self.dq_all[:, : self.a], dk, dv
 
-# ------------------------------------------------------------------ forward
+    def check_backward(self):
+        ref, tol, t32 = O.backward(*map(self.clean, (self.q, self.k, self.v, self.dout)),
+                                   self.q_seq, self.k_seq, self.heads, self.kv_heads, self.d,
+                                   self.scale)
+        got = [to_f64(x) for x in self.backward()]
+        for name, g, r, t, e, seq in zip(("dQ", "dK", "dV"), got, ref, tol, t32,
+                                         (self.q_seq, self.k_seq, self.k_seq)):
+            owned = np.zeros(len(g), dtype=bool)
+            for first, slot, real in seq:
+                owned[first: first + slot] = True
+                assert (g[first + real: first + slot] == 0).all(), name
+            assert (g[~owned] == KEEP).all(), name
+            if owned.any():
+                off = (np.abs(g - r) / t)[owned]
+                assert off.max() <= 1, f"{name}: {off.max():.3g} of the tolerance"
+                # roundings of either sign: the 2-norm within two of them, and the
+                # 32-bit part (see the other attention's test)
+                assert np.linalg.norm((g - r)[owned]) <= \
+                    2 * O.HALF_BF16 * np.linalg.norm(r) + np.linalg.norm(e), name
+        assert (to_f64(self.dq_all)[:, self.a:] == KEEP).all()
+        assert (to_f64(self.dkv_all)[:, 2 * self.akv:] == KEEP).all()
+        return self
+
+    def check(self):
+        return self.check_forward().check_backward()
+
+
+# ------------------------------------------------------------------ forward and backward
 @pytest.mark.parametrize("sq,sk", [(1, 1), (1, 127), (2, 128), (127, 129), (128, 255), (129, 256),
                                    (200, 257), (64, 400), (300, 1), (1, 3000), (260, 700)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_lengths(sq, sk, d):
-    Problem(1, sq, sk, 2, 2, d).check_forward()
+    Problem(1, sq, sk, 2, 2, d).check()
 
 
 @pytest.mark.parametrize("heads,kv_heads", [(3, 3), (6, 2), (5, 1), (8, 1), (12, 4), (7, 1), (48, 1),
                                             (100, 1), (128, 1), (16, 8)])
 @pytest.mark.parametrize("sq,sk", [(1, 300), (5, 130), (70, 390)])
 def test_grouped_heads(heads, kv_heads, sq, sk):
-    Problem(2, 2 * sq, 2 * sk, heads, kv_heads, 64, kv_lens=[sk, sk // 3]).check_forward()
+    Problem(2, 2 * sq, 2 * sk, heads, kv_heads, 64, kv_lens=[sk, sk // 3]).check()
 
 
 def test_grouped_heads_of_128():
-    Problem(3, 3 * 33, 3 * 300, 8, 2, 128, kv_lens=[300, 1, 129], wide=128).check_forward()
+    Problem(3, 3 * 33, 3 * 300, 8, 2, 128, kv_lens=[300, 1, 129], wide=128).check()
 
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_padded(d):
     """Padded keys and queries hold NaN; a sequence has no keys, another no queries."""
     Problem(5, 5 * 150, 5 * 300, 4, 2, d, q_lens=[150, 1, 0, 77, 128],
-            kv_lens=[300, 0, 256, 1, 299], wide=128).check_forward()
+            kv_lens=[300, 0, 256, 1, 299], wide=128).check()
     Problem(5, 5 * 150, 5 * 300, 3, 3, d, q_lens=[150, 1, 0, 77, 128],
-            kv_lens=[300, 0, 256, 1, 299], wide=8).check_forward()
+            kv_lens=[300, 0, 256, 1, 299], wide=8).check()
 
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_packed(d):
     Problem(6, 700, 900, 4, 4, d, q_offsets=[3, 3, 130, 131, 400, 640, 690],
-            kv_offsets=[10, 300, 300, 301, 557, 700, 890]).check_forward()
+            kv_offsets=[10, 300, 300, 301, 557, 700, 890]).check()
     Problem(6, 700, 900, 4, 2, d, q_offsets=[3, 3, 130, 131, 400, 640, 690], max_q=300, max_kv=290,
-            kv_offsets=[10, 300, 300, 301, 557, 700, 890]).check_forward()
+            kv_offsets=[10, 300, 300, 301, 557, 700, 890]).check()
 
 
 def test_packed_with_padding_inside():
     Problem(3, 500, 600, 2, 1, 128, q_offsets=[0, 200, 260, 480], q_lens=[180, 60, 0],
-            kv_offsets=[0, 100, 400, 590], kv_lens=[99, 300, 20]).check_forward()
+            kv_offsets=[0, 100, 400, 590], kv_lens=[99, 300, 20]).check()
 
 
 def test_infinities_in_the_padding():
     Problem(4, 4 * 20, 4 * 200, 2, 2, 64, kv_lens=[200, 100, 0, 129], q_lens=[20, 3, 20, 1],
-            hole=float("inf")).check_forward()
+            hole=float("inf")).check()
 
 
 def test_offsets_outside_the_rows_are_cut():
     Problem(3, 100, 100, 2, 2, 64, q_offsets=[-5, 40, 90, 1000], q_lens=[7, -3, 50],
             kv_offsets=[-2 ** 31, 10, 90, 2 ** 31 - 1], kv_lens=[2 ** 31 - 1] * 3,
-            hole=0.0).check_forward()
+            hole=0.0).check()
 
 
 def test_a_sequence_longer_than_stated_is_reported():
@@ -148,26 +191,25 @@ def test_a_sequence_longer_than_stated_is_reported():
     assert L.mc_attention_forward_cross(p.q, p.k, p.v, p.o, p.lse, p.cross, st) == 0
     torch.cuda.synchronize()
     assert int(st[0]) == L.MC_ERR_DEVICE_BOUNDS
-    ok = Problem(1, 40, 40, 2, 2, 64)  # the next call is as ever
-    ok.check_forward()
+    Problem(1, 40, 40, 2, 2, 64).check()  # the next call is as ever
 
 
 @pytest.mark.parametrize("scale", [1.0, 0.01, 2.0 ** -16])
 def test_scale(scale):
-    Problem(1, 130, 300, 2, 2, 64, scale=scale, qstd=0.5).check_forward()
+    Problem(1, 130, 300, 2, 2, 64, scale=scale, qstd=0.5).check()
 
 
 def test_growing_scores():
     """Maxima that grow from block to block, so that O is rescaled."""
     p = Problem(1, 140, 2000, 2, 2, 128, qstd=1.0)
     p.kv_all[:, : p.akv] *= torch.linspace(0.1, 8.0, 2000, device=DEV).bfloat16()[:, None]
-    p.check_forward()
+    p.check()
 
 
 def test_many_items():
     """More items than SMs hold at once: blocks taken over by running CTAs."""
     Problem(40, 40 * 130, 40 * 70, 9, 9, 64, kv_lens=[1 + (i * 37) % 70 for i in range(40)],
-            q_lens=[130 - (i * 11) % 130 for i in range(40)]).check_forward()
+            q_lens=[130 - (i * 11) % 130 for i in range(40)]).check()
 
 
 @pytest.mark.parametrize("n,sk,heads,kv_heads,d", [(1, 8191, 8, 1, 128), (2, 4097, 4, 4, 64),
@@ -175,16 +217,29 @@ def test_many_items():
 def test_one_token_long_states(n, sk, heads, kv_heads, d):
     """Few rows: the keys of an item are shared out."""
     Problem(n, n, n * sk, heads, kv_heads, d,
-            kv_lens=[max(0, sk - 700 * i) for i in range(n)]).check_forward()
+            kv_lens=[max(0, sk - 700 * i) for i in range(n)]).check()
 
 
 def test_same_bits_again():
     p = Problem(2, 2 * 30, 2 * 3000, 4, 2, 128, kv_lens=[3000, 1234])
     p.forward()
     o, lse = p.o.clone(), p.lse.clone()
+    first = [x.clone() for x in p.backward()]
     for _ in range(3):
         p.forward()
         assert torch.equal(p.o, o) and torch.equal(p.lse, lse)
+        assert all(torch.equal(x, y) for x, y in zip(p.backward(), first))
+
+
+def test_heads_in_groups():
+    """Packed sequences whose longest is not known: the tiles of one key head fill
+    the workspace, the heads take turns."""
+    n, rows = 150, 2900
+    cuts = [rows * i // n for i in range(n + 1)]
+    p = Problem(n, rows, rows + 40, 6, 3, 64, q_offsets=cuts, kv_offsets=[c + 10 for c in cuts])
+    per_head = n * ((rows + 63) // 64) * ((rows + 40 + 127) // 128) * 32768
+    assert L.mc_attention_backward_cross_ws_bytes(p.cross) == per_head > 2 ** 30
+    p.check()
 
 
 def test_nan_in_a_real_key_stays_in_its_sequence():
