@@ -20,11 +20,27 @@
 namespace mc {
 namespace {
 
-constexpr int kNormWarps = 4;
-constexpr int kNormTurns = 8;    // turns of an item, at most
-constexpr int kNormTable = 512;  // (token, pair) entries of a warp's cos / sin table (4 KB)
+constexpr int kNormTable = 224;  // (token, pair) entries of a warp's cos / sin table
 constexpr int kNormMaxDim = 256;
-constexpr int kNormMaxBlocks = 1024;  // of the backward pass: rows of partial sums
+constexpr int kNormWords = kNormMaxDim / 2 + 8;  // of gains or shifts, two elements each
+constexpr int kNormMaxBlocks = 512;  // of the backward pass: rows of partial sums
+// A chunk of a warp's work is this many turns of its lanes, 1 KB of each input a
+// turn, and so many chunks are on their way.
+constexpr int kNormTurnBytes = 1024;
+template <bool BACK>
+struct NormCfg {
+  // (the backward pass takes 168 registers a thread: 12 warps per SM)
+  static constexpr int kWarps = BACK ? 12 : 8, kBlocks = BACK ? 1 : 2;
+  static constexpr int kTurns = BACK ? 2 : 4;
+  static constexpr int kInputs = BACK ? 2 : 1;
+  static constexpr int kStages = 3;
+  static constexpr int kStage = kTurns * kInputs * kNormTurnBytes;
+  static constexpr int kWarp = kStages * kStage + 2 * kNormTable * 4;
+  static constexpr int kSmem = kWarps * (kWarp + kStages * 8) + kNormMaxDim / 2 * 8 +
+                               2 * kNormWords * 4 + kNormMaxDim / 2;
+  static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "blocks per SM");
+  static_assert(kStages * kStage >= 2 * kNormMaxDim * 4, "a warp's sums go through its ring");
+};
 
 // Queries (0) and keys (1) are walked apart, each by blocks of its own, so that
 // a lane's gains, shifts and gradient sums stay in registers.
@@ -33,17 +49,17 @@ struct NormType {
   const uint16_t* shift;  // or NULL: zeros
   float* dgain;           // or NULL
   float* dshift;
-  int64_t items;       // (token group, head range) pairs, one warp each
+  int64_t chunks;      // (token group, head range) pairs, shared out to the warps in runs
   int head0, heads;    // of the row's heads
-  int tok_item, head_item, ranges;  // an item: tokens, heads of each; ranges per token
+  int tok_chunk, head_chunk, ranges;  // a chunk: tokens, heads of each; ranges per token group
   int block0, blocks;
-  uint32_t div_head_item;
+  uint32_t div_head_chunk;
 };
 
 struct NormArgs {
   NormType type[2];
   int64_t tokens, ld_in, ld_dout, ld_out;
-  int d, pairs;
+  int d, pairs, axes;
   int lanes, units;  // lanes of a head (a power of two) and its units
   int centred, inverse, accumulate;
   float eps;
@@ -52,38 +68,157 @@ struct NormArgs {
   uint8_t axis[kRotaryMaxPairs];
 };
 
+// Elements in 32 bits, two at a time where a vector has an even number of them.
+template <int VEC>
+struct Two {
+  using P = float2;
+};
+template <>
+struct Two<1> {
+  using P = float;
+};
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float sum(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float2 swap(float2 a) { return make_float2(a.y, a.x); }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum(float a) { return a; }
+__device__ __forceinline__ float swap(float a) { return a; }
+template <typename P>
+__device__ __forceinline__ P both(float x);
+template <>
+__device__ __forceinline__ float2 both<float2>(float x) { return make_float2(x, x); }
+template <>
+__device__ __forceinline__ float both<float>(float x) { return x; }
+__device__ __forceinline__ float& at(float2& p, int i) { return i ? p.y : p.x; }
+__device__ __forceinline__ float& at(float& p, int) { return p; }
+
+template <typename T, int VEC, typename P>
+__device__ __forceinline__ void unpack(const RotVec<T, VEC>& v, P* f) {
+  if constexpr (VEC == 1) {
+    f[0] = to_f32(v.e[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) f[i] = make_float2(v.e[2 * i], v.e[2 * i + 1]);
+  }
+}
+template <typename T, int VEC, typename P>
+__device__ __forceinline__ RotVec<T, VEC> pack(const P* f) {
+  RotVec<T, VEC> v;
+  if constexpr (VEC == 1) {
+    v.e[0] = from_f32<T>(f[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) w[i] = pack_bf16x2(f[i].x, f[i].y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v.e[2 * i] = f[i].x, v.e[2 * i + 1] = f[i].y;
+  }
+  return v;
+}
+
 // A unit is two vectors: the halves of VEC pairs, or of adjacent pairs and of
 // what does not turn two neighbouring ones (the second may be missing).  `lanes`
 // lanes hold a head, one unit (or N, for narrow vectors) each, and a lane has
 // the same unit of every head it meets: its gains are loaded once, its cosines
 // once per token.  Of a warp's turn the lanes hold 32 / lanes heads, of the same
 // token or of the next ones.
+//
+// A warp's chunks are one run of the rows.  With vectors of 16 bytes they come
+// by bulk copies into a ring of its own, so that the loads on their way do not
+// depend on registers; with narrower ones (odd sizes or addresses) the lanes
+// load them.
 template <typename T, int VEC, bool ADJACENT, bool BACK, bool SHIFT>
-__global__ void __launch_bounds__(kNormWarps * 32)
+__global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBlocks)
     qk_norm_kernel(const T* in, const T* dout, T* out, const int32_t* __restrict__ positions,
                    const float* __restrict__ inv_freq, const __grid_constant__ NormArgs A,
                    int* status) {
   using V = RotVec<T, VEC>;
+  using P = typename Two<VEC>::P;
+  using C = NormCfg<BACK>;
+  constexpr int W = VEC > 1 ? VEC / 2 : 1, E = VEC > 1 ? 2 : 1;  // VEC = W E
+  constexpr bool kBulk = VEC * sizeof(T) == 16;
   constexpr bool kSplit = !ADJACENT || VEC == 1;  // a pair's halves are in two vectors
-  constexpr int N = VEC * sizeof(T) == 16 ? 1 : (VEC == 2 ? 2 : 4);
-  __shared__ uint64_t turns[kNormMaxDim / 2];
-  __shared__ __align__(16) float table[kNormWarps][2][kNormTable];
+  constexpr int N = kBulk ? 1 : (VEC == 2 ? 2 : 4);
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  uint8_t* const ring = smem + warp * C::kWarp;
+  float* const t_cos = reinterpret_cast<float*>(ring + C::kStages * C::kStage);
+  float* const t_sin = t_cos + kNormTable;
+  uint64_t* const turns = reinterpret_cast<uint64_t*>(smem + C::kWarps * C::kWarp);
+  uint64_t* const full = turns + kNormMaxDim / 2 + warp * C::kStages;
+  if (kBulk && lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
   pdl_wait();  // the previous kernel on the stream has completed
   pdl_launch();
-  for (int p = threadIdx.x; p < A.pairs; p += kNormWarps * 32) turns[p] = turns_fixed(inv_freq[p]);
-  __syncthreads();
-  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  float* const t_cos = table[warp][0];
-  float* const t_sin = table[warp][1];
   const NormType& Y = A.type[static_cast<int>(blockIdx.x) >= A.type[1].block0 ? 1 : 0];
   const int d = A.d, L = A.lanes;
   const int seg = lane / L, per_turn = 32 / L;
   const float inv_d = 1.f / static_cast<float>(d);
 
+  // this warp's run of chunks
+  const int64_t warps = static_cast<int64_t>(Y.blocks) * C::kWarps;
+  const int64_t me = static_cast<int64_t>(static_cast<int>(blockIdx.x) - Y.block0) * C::kWarps + warp;
+  const int64_t per = Y.chunks / warps, more = Y.chunks - per * warps;
+  const int64_t c_begin = me * per + min(me, more), c_end = c_begin + per + (me < more ? 1 : 0);
+  struct Chunk {
+    int64_t t0;
+    int h0, ntok, nh;
+  };
+  auto bound = [&](Chunk& x) {
+    x.ntok = static_cast<int>(min(static_cast<int64_t>(Y.tok_chunk), A.tokens - x.t0));
+    x.nh = min(Y.head_chunk, Y.heads - x.h0);
+  };
+  auto advance = [&](Chunk& x) {
+    x.h0 += Y.head_chunk;
+    if (x.h0 >= Y.heads) x.h0 = 0, x.t0 += Y.tok_chunk;
+    bound(x);
+  };
+  Chunk x;
+  x.t0 = c_begin / Y.ranges * Y.tok_chunk;
+  x.h0 = static_cast<int>(c_begin % Y.ranges) * Y.head_chunk;
+  bound(x);
+  [[maybe_unused]] Chunk ahead = x;  // the next one to load
+  // A row's heads of the next chunk into stage st, a copy per token and input.
+  auto issue = [&](int st) {
+    const uint32_t bytes = static_cast<uint32_t>(ahead.nh * d * static_cast<int>(sizeof(T)));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes * ahead.ntok * C::kInputs);
+    __syncwarp();
+    for (int tk = lane; tk < ahead.ntok; tk += 32) {
+      uint8_t* dst = ring + st * C::kStage + tk * bytes;
+      const int64_t col = static_cast<int64_t>(Y.head0 + ahead.h0) * d;
+      bulk_load(dst, in + (ahead.t0 + tk) * A.ld_in + col, bytes, &full[st]);
+      if constexpr (BACK)
+        bulk_load(dst + C::kTurns * kNormTurnBytes, dout + (ahead.t0 + tk) * A.ld_dout + col, bytes,
+                  &full[st]);
+    }
+    advance(ahead);
+  };
+  if constexpr (kBulk) {
+    __syncwarp();
+    for (int i = 0; i < C::kStages; ++i)
+      if (c_begin + i < c_end) issue(i);
+  }
+  uint32_t* const words = reinterpret_cast<uint32_t*>(turns + kNormMaxDim / 2 + C::kWarps * C::kStages);
+  uint8_t* const axis = reinterpret_cast<uint8_t*>(words + 2 * kNormWords);
+  for (int p = threadIdx.x; p < A.pairs; p += C::kWarps * 32) {
+    turns[p] = turns_fixed(inv_freq[p]);
+    axis[p] = A.axis[p];
+  }
+
   // this lane's units: first dimensions of the two vectors (-1: none) and the
   // first pair of each (of both, where the vectors are halves; -1: does not turn)
   int oa[N], ob[N], pa[N], pb[N];
-  float ga[N][VEC], gb[N][VEC], ca[N][VEC], cb[N][VEC];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const int u = lane % L + j * L;
@@ -102,218 +237,320 @@ __global__ void __launch_bounds__(kNormWarps * 32)
         }
       }
     }
+  }
+  // Gains and shifts, bf16, unit by unit in shared memory: the first vector's
+  // element in the low half of a word, the second's above.  (Forward, they are
+  // read once per token, into its factors.)
+  if (warp == 0 && seg == 0) {
+    const uint32_t one = 0x3F80u;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      ga[j][i] = gb[j][i] = 1.f;
-      ca[j][i] = cb[j][i] = 0.f;
-      if (Y.gain && oa[j] >= 0) ga[j][i] = bf16_lo(Y.gain[oa[j] + i]);
-      if (Y.gain && ob[j] >= 0) gb[j][i] = bf16_lo(Y.gain[ob[j] + i]);
-      if constexpr (!BACK) {
-        if (Y.shift && oa[j] >= 0) ca[j][i] = bf16_lo(Y.shift[oa[j] + i]);
-        if (Y.shift && ob[j] >= 0) cb[j][i] = bf16_lo(Y.shift[ob[j] + i]);
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int w = (lane + j * L) * VEC + i;
+        if (oa[j] < 0) continue;
+        const uint32_t lo = Y.gain ? Y.gain[oa[j] + i] : one;
+        const uint32_t hi = Y.gain && ob[j] >= 0 ? Y.gain[ob[j] + i] : one;
+        words[w] = lo | (hi << 16);
+        const uint32_t slo = !BACK && Y.shift ? Y.shift[oa[j] + i] : 0u;
+        const uint32_t shi = !BACK && Y.shift && ob[j] >= 0 ? Y.shift[ob[j] + i] : 0u;
+        words[kNormWords + w] = slo | (shi << 16);
       }
+  }
+  __syncthreads();  // `turns`, `axis` and `words`
+  using Words = RotVec<uint32_t, VEC>;
+  auto load_words = [&](int part, int j) -> Words {
+    Words w = {};
+    if (oa[j] >= 0)
+      w = *reinterpret_cast<const Words*>(words + part * kNormWords + (lane % L + j * L) * VEC);
+    return w;
+  };
+  // (the backward pass needs the gains at every head)
+  uint32_t gain[BACK ? N : 1][VEC];
+  if constexpr (BACK) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const Words w = load_words(0, j);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) gain[j][i] = w.e[i];
     }
   }
   // backward: this lane's sums of t n and t
-  float sga[BACK ? N : 1][VEC] = {}, sgb[BACK ? N : 1][VEC] = {};
-  float sca[BACK && SHIFT ? N : 1][VEC] = {}, scb[BACK && SHIFT ? N : 1][VEC] = {};
-  float cs[N][VEC], sn[N][VEC];  // of the token `held` (adjacent: half for each vector)
+  P sga[BACK ? N : 1][W] = {}, sgb[BACK ? N : 1][W] = {};
+  P sca[BACK && SHIFT ? N : 1][W] = {}, scb[BACK && SHIFT ? N : 1][W] = {};
+  // What a token's angles make of a head, by element: own factor, partner's
+  // factor, and a constant:  y = r (x f + partner(x) h) + k, gains and shifts in
+  // them (forward), t = dout f + partner(dout) h (backward).
+  P fa[N][W], fb[N][W], ha[N][W], hb[N][W];
+  P ka[!BACK && SHIFT ? N : 1][W], kb[!BACK && SHIFT ? N : 1][W];
+  auto factors = [&](int j, const float (&cs)[VEC], const float (&sn)[VEC]) {
+    [[maybe_unused]] Words wg, wc;
+    if constexpr (!BACK) wg = load_words(0, j);
+    if constexpr (!BACK && SHIFT) wc = load_words(1, j);
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+    for (int i = 0; i < VEC; ++i) {
+      // the angle of element i of a and of b, and its place in the pair
+      const int ia = kSplit ? i : i / 2, ib = kSplit ? i : VEC / 2 + i / 2;
+      const float sa = kSplit || i % 2 == 0 ? -sn[ia] : sn[ia];
+      const float sb = kSplit || i % 2 == 1 ? sn[ib] : -sn[ib];
+      float &f0 = at(fa[j][i / E], i % E), &f1 = at(fb[j][i / E], i % E);
+      float &h0 = at(ha[j][i / E], i % E), &h1 = at(hb[j][i / E], i % E);
+      if constexpr (BACK) {
+        f0 = cs[ia], h0 = sa, f1 = cs[ib], h1 = sb;
+      } else {
+        // the partners' gains and shifts
+        const int o = kSplit || VEC == 1 ? i : i ^ 1;
+        const uint32_t g = wg.e[i], go = wg.e[o];
+        f0 = bf16_lo(g) * cs[ia];
+        h0 = (kSplit ? bf16_hi(g) : bf16_lo(go)) * sa;
+        f1 = bf16_hi(g) * cs[ib];
+        h1 = (kSplit ? bf16_lo(g) : bf16_hi(go)) * sb;
+        if constexpr (SHIFT) {
+          const uint32_t c = wc.e[i], co = wc.e[o];
+          at(ka[j][i / E], i % E) = bf16_lo(c) * cs[ia] + (kSplit ? bf16_hi(c) : bf16_lo(co)) * sa;
+          at(kb[j][i / E], i % E) = bf16_hi(c) * cs[ib] + (kSplit ? bf16_lo(c) : bf16_hi(co)) * sb;
+        }
+      }
+    }
+  };
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) cs[j][i] = 1.f, sn[j][i] = 0.f;
+  for (int j = 0; j < N; ++j) {
+    float cs[VEC], sn[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    factors(j, cs, sn);
+  }
 
   // sums over the lanes of a head
+  auto head_sum = [&](float& a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < L) a += __shfl_xor_sync(0xffffffffu, a, o);
+  };
   auto head_sum2 = [&](float& a, float& b) {
-    for (int o = L >> 1; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < L) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+  };
+  // x f + partner(x) h of both vectors
+  auto turn = [&](int j, P (&a)[W], P (&b)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const P u = a[i], v = b[i];
+      a[i] = fma(u, fa[j][i], mul(kSplit ? v : swap(u), ha[j][i]));
+      b[i] = fma(v, fb[j][i], mul(kSplit ? u : swap(v), hb[j][i]));
     }
   };
 
-  struct Raw {
-    V a[N], b[N];
-    [[maybe_unused]] V da[N], db[N];
-    int tok, head;  // tok < 0: nothing
+  // The positions of a group's tokens (axis by axis, 32 at most: a lane each) are
+  // loaded a group ahead.
+  const int my_axis = lane / Y.tok_chunk, my_tok = lane - my_axis * Y.tok_chunk;
+  auto positions_of = [&](int64_t t0) -> int32_t {
+    return A.pairs > 0 && my_axis < A.axes && t0 + my_tok < A.tokens
+               ? positions[my_axis * A.tokens + t0 + my_tok]
+               : 0;
   };
-  const int64_t warps = static_cast<int64_t>(Y.blocks) * kNormWarps;
-  for (int64_t item = static_cast<int64_t>(static_cast<int>(blockIdx.x) - Y.block0) * kNormWarps + warp;
-       item < Y.items; item += warps) {
-    const int64_t group = item / Y.ranges;
-    const int64_t t0 = group * Y.tok_item;
-    const int ntok = static_cast<int>(min(static_cast<int64_t>(Y.tok_item), A.tokens - t0));
-    const int h0 = static_cast<int>(item - group * Y.ranges) * Y.head_item;
-    const int nh = min(Y.head_item, Y.heads - h0);
-    const int total = ntok * nh;
-    auto load = [&](int e) {
-      Raw x;
-      x.tok = -1;
-      x.head = 0;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          x.a[j].e[i] = x.b[j].e[i] = from_f32<T>(0.f);
-          if constexpr (BACK) x.da[j].e[i] = x.db[j].e[i] = from_f32<T>(0.f);
-        }
-      if (e < total) {
-        x.tok = nh == Y.head_item ? fast_div(e, Y.div_head_item) : e / nh;
-        x.head = Y.head0 + h0 + (e - x.tok * nh);
-        const T* row = in + (t0 + x.tok) * A.ld_in + static_cast<int64_t>(x.head) * d;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if (oa[j] >= 0) x.a[j] = *reinterpret_cast<const V*>(row + oa[j]);
-          if (ob[j] >= 0) x.b[j] = *reinterpret_cast<const V*>(row + ob[j]);
-        }
-        if constexpr (BACK) {
-          const T* drow = dout + (t0 + x.tok) * A.ld_dout + static_cast<int64_t>(x.head) * d;
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            if (oa[j] >= 0) x.da[j] = *reinterpret_cast<const V*>(drow + oa[j]);
-            if (ob[j] >= 0) x.db[j] = *reinterpret_cast<const V*>(drow + ob[j]);
-          }
-        }
-      }
-      return x;
-    };
-    Raw cur = load(seg);
-    int held = -1;
-    if (A.pairs > 0) {
-      __syncwarp();  // the table of the item before has been read
-      for (int i = lane; i < ntok * A.pairs; i += 32) {
-        const int tk = fast_div(i, A.div_pairs), p = i - tk * A.pairs;
-        const int64_t pos = positions[A.axis[p] * A.tokens + t0 + tk];
-        float s, c;
-        turn_sincos(A.inverse ? -pos : pos, turns[p], &s, &c);
-        t_cos[i] = c;
-        t_sin[i] = s;
+  int32_t pos_next = c_begin < c_end ? positions_of(x.t0) : 0;
+  int64_t tabled = -1;  // the token group whose angles are in the table
+  int held = -1;        // and the token of it in cs, sn
+  int n = 0;            // chunks done
+  for (int64_t c = c_begin; c < c_end; ++c, ++n, advance(x)) {
+    const int st = n % C::kStages;
+    if (A.pairs > 0 && x.t0 != tabled) {
+      tabled = x.t0;
+      held = -1;
+      const int32_t pos_now = pos_next;
+      pos_next = positions_of(x.t0 + Y.tok_chunk);
+      __syncwarp();  // the table of the group before has been read
+      for (int i0 = 0; i0 < x.ntok * A.pairs; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < x.ntok * A.pairs;
+        const int tk = in ? fast_div(i, A.div_pairs) : 0, p = in ? i - tk * A.pairs : 0;
+        const int64_t pos = __shfl_sync(0xffffffffu, pos_now, axis[p] * Y.tok_chunk + tk);
+        if (in) turn_sincos(A.inverse ? -pos : pos, turns[p], t_sin + i, t_cos + i);
       }
       __syncwarp();
     }
+    if constexpr (kBulk) {
+      if (!mbar_wait_warp(&full[st], (n / C::kStages) & 1, status, kSiteQkNorm)) break;
+    }
+    const int total = x.ntok * x.nh;
+#pragma unroll 1
     for (int e0 = 0; e0 < total; e0 += per_turn) {
-      if (A.pairs > 0 && cur.tok >= 0 && cur.tok != held) {
-        held = cur.tok;
+      // (token, head) e of the chunk: this lane's, or none
+      const int e = e0 + seg;
+      const bool live = e < total;
+      int tok = 0, head = live ? e : 0;
+      if (x.ntok > 1 && live) {
+        tok = x.nh == Y.head_chunk ? fast_div(e, Y.div_head_chunk) : e / x.nh;
+        head = e - tok * x.nh;
+      }
+      head += Y.head0 + x.h0;
+      const T* row;
+      [[maybe_unused]] const T* drow = nullptr;
+      if constexpr (kBulk) {
+        row = reinterpret_cast<const T*>(ring + st * C::kStage) + (live ? e : 0) * d;
+        if constexpr (BACK) drow = row + C::kTurns * kNormTurnBytes / static_cast<int>(sizeof(T));
+      } else {
+        row = in + (x.t0 + tok) * A.ld_in + static_cast<int64_t>(head) * d;
+        if constexpr (BACK) drow = dout + (x.t0 + tok) * A.ld_dout + static_cast<int64_t>(head) * d;
+      }
+      P a[N][W] = {}, b[N][W] = {};
+      [[maybe_unused]] P ta[N][W] = {}, tb[N][W] = {};
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (live && oa[j] >= 0) {
+          unpack<T, VEC>(*reinterpret_cast<const V*>(row + oa[j]), a[j]);
+          if constexpr (BACK) unpack<T, VEC>(*reinterpret_cast<const V*>(drow + oa[j]), ta[j]);
+        }
+        if (live && ob[j] >= 0) {
+          unpack<T, VEC>(*reinterpret_cast<const V*>(row + ob[j]), b[j]);
+          if constexpr (BACK) unpack<T, VEC>(*reinterpret_cast<const V*>(drow + ob[j]), tb[j]);
+        }
+      }
+      if (A.pairs > 0 && live && tok != held) {
+        held = tok;
         const float* c0 = t_cos + held * A.pairs;
         const float* s0 = t_sin + held * A.pairs;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int j = 0; j < N; ++j) {
+          float cs[VEC], sn[VEC];
+          // (the first pair's cosines, or those of either vector, one after another)
+          constexpr int kRun = kSplit ? VEC : VEC / 2;
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const int p = kSplit ? pa[j] : (i < VEC / 2 ? pa[j] : pb[j]);
-            const int at = kSplit || i < VEC / 2 ? i : i - VEC / 2;
-            if (p >= 0) cs[j][i] = c0[p + at], sn[j][i] = s0[p + at];
+          for (int i = 0; i < VEC; i += kRun) {
+            const int p = i == 0 ? pa[j] : pb[j];
+            RotVec<float, kRun> co, si;
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) co.e[k] = 1.f, si.e[k] = 0.f;
+            if (p >= 0) {
+              if constexpr (kBulk) {  // (runs are aligned)
+                co = *reinterpret_cast<const RotVec<float, kRun>*>(c0 + p);
+                si = *reinterpret_cast<const RotVec<float, kRun>*>(s0 + p);
+              } else {
+#pragma unroll
+                for (int k = 0; k < kRun; ++k) co.e[k] = c0[p + k], si.e[k] = s0[p + k];
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) cs[i + k] = co.e[k], sn[i + k] = si.e[k];
           }
+          factors(j, cs, sn);
+        }
       }
-      // pairs turn by the angle whose cosine and sine are cs, sn
-      auto turn = [&](int j, float (&a)[VEC], float (&b)[VEC]) {
-        if constexpr (kSplit) {
+      // u = t g
+      [[maybe_unused]] P ua[BACK ? N : 1][W], ub[BACK ? N : 1][W];
+      if constexpr (BACK) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float u = a[i], v = b[i];
-            a[i] = u * cs[j][i] - v * sn[j][i];
-            b[i] = u * sn[j][i] + v * cs[j][i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC / 2; ++i) {
-            const float u = a[2 * i], v = a[2 * i + 1], x = b[2 * i], y = b[2 * i + 1];
-            a[2 * i] = u * cs[j][i] - v * sn[j][i];
-            a[2 * i + 1] = u * sn[j][i] + v * cs[j][i];
-            b[2 * i] = x * cs[j][VEC / 2 + i] - y * sn[j][VEC / 2 + i];
-            b[2 * i + 1] = x * sn[j][VEC / 2 + i] + y * cs[j][VEC / 2 + i];
-          }
-        }
-      };
-      float a[N][VEC], b[N][VEC];
-      [[maybe_unused]] float ta[N][VEC], tb[N][VEC];
-      float sum = 0.f, usum = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          a[j][i] = to_f32(cur.a[j].e[i]);
-          b[j][i] = to_f32(cur.b[j].e[i]);
-          sum += a[j][i] + b[j][i];
-          if constexpr (BACK) {
-            ta[j][i] = to_f32(cur.da[j].e[i]);
-            tb[j][i] = to_f32(cur.db[j].e[i]);
-          }
-        }
-        if constexpr (BACK) {
+        for (int j = 0; j < N; ++j) {
           turn(j, ta[j], tb[j]);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) usum += ta[j][i] * ga[j][i] + tb[j][i] * gb[j][i];
+          for (int i = 0; i < VEC; ++i) {
+            at(ua[j][i / E], i % E) = at(ta[j][i / E], i % E) * bf16_lo(gain[j][i]);
+            at(ub[j][i / E], i % E) = at(tb[j][i / E], i % E) * bf16_hi(gain[j][i]);
+          }
         }
       }
+      float um = 0.f;  // mean(u), if it counts
       if (A.centred) {
-        head_sum2(sum, usum);
-        const float m = sum * inv_d;
+        P s2 = both<P>(0.f), us2 = both<P>(0.f);
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            if (oa[j] >= 0) a[j][i] -= m;
-            if (ob[j] >= 0) b[j][i] -= m;
+          for (int i = 0; i < W; ++i) {
+            s2 = add(s2, add(a[j][i], b[j][i]));
+            if constexpr (BACK) us2 = add(us2, add(ua[j][i], ub[j][i]));
+          }
+        float s1 = sum(s2), us1 = sum(us2);
+        if constexpr (BACK)
+          head_sum2(s1, us1);
+        else
+          head_sum(s1);
+        um = us1 * inv_d;
+        const P ma = both<P>(-s1 * inv_d);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            if (oa[j] >= 0) a[j][i] = add(a[j][i], ma);
+            if (ob[j] >= 0) b[j][i] = add(b[j][i], ma);
           }
       }
-      float sq = 0.f, ux = 0.f;
+      P qa = both<P>(0.f), qb = both<P>(0.f), xa = both<P>(0.f), xb = both<P>(0.f);
 #pragma unroll
       for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          sq += a[j][i] * a[j][i] + b[j][i] * b[j][i];
-          if constexpr (BACK)
-            ux += ta[j][i] * ga[j][i] * a[j][i] + tb[j][i] * gb[j][i] * b[j][i];
+        for (int i = 0; i < W; ++i) {
+          qa = fma(a[j][i], a[j][i], qa);
+          qb = fma(b[j][i], b[j][i], qb);
+          if constexpr (BACK) {
+            xa = fma(a[j][i], ua[j][i], xa);
+            xb = fma(b[j][i], ub[j][i], xb);
+          }
         }
-      head_sum2(sq, ux);
+      float sq = sum(add(qa, qb)), ux = sum(add(xa, xb));
+      if constexpr (BACK)
+        head_sum2(sq, ux);
+      else
+        head_sum(sq);
       const float r = rsqrtf(fmaf(sq, inv_d, A.eps));
-      const float un = ux * r * inv_d, um = A.centred ? usum * inv_d : 0.f;  // mean(u n), mean(u)
-      T* row = out + (t0 + max(cur.tok, 0)) * A.ld_out + static_cast<int64_t>(cur.head) * d;
-      const bool put = cur.tok >= 0 &&
-                       MC_DCHECK(t0 + cur.tok < A.tokens && cur.head < Y.head0 + Y.heads, status,
-                                 kSiteQkNorm);
+      T* to = out + (x.t0 + tok) * A.ld_out + static_cast<int64_t>(head) * d;
+      const bool put = live && MC_DCHECK(x.t0 + tok < A.tokens && head < Y.head0 + Y.heads, status,
+                                         kSiteQkNorm);
+      // backward: r (u - n mean(u n) - mean(u)) = r u + x k1 + k0
+      [[maybe_unused]] const P k1 = both<P>(-r * r * (ux * r * inv_d)), k0 = both<P>(-r * um);
+      const P rr = both<P>(r);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        V ya, yb;
         if constexpr (BACK) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float na = a[j][i] * r, nb = b[j][i] * r;
-            ya.e[i] = from_f32<T>(r * (ta[j][i] * ga[j][i] - na * un - um));
-            yb.e[i] = from_f32<T>(r * (tb[j][i] * gb[j][i] - nb * un - um));
-            sga[j][i] += ta[j][i] * na;
-            sgb[j][i] += tb[j][i] * nb;
+          for (int i = 0; i < W; ++i) {
+            sga[j][i] = fma(mul(ta[j][i], rr), a[j][i], sga[j][i]);
+            sgb[j][i] = fma(mul(tb[j][i], rr), b[j][i], sgb[j][i]);
             if constexpr (SHIFT) {
-              sca[j][i] += ta[j][i];
-              scb[j][i] += tb[j][i];
+              sca[j][i] = add(sca[j][i], ta[j][i]);
+              scb[j][i] = add(scb[j][i], tb[j][i]);
             }
+            a[j][i] = fma(ua[j][i], rr, fma(a[j][i], k1, k0));
+            b[j][i] = fma(ub[j][i], rr, fma(b[j][i], k1, k0));
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            a[j][i] = fmaf(a[j][i] * r, ga[j][i], ca[j][i]);
-            b[j][i] = fmaf(b[j][i] * r, gb[j][i], cb[j][i]);
-          }
           turn(j, a[j], b[j]);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            ya.e[i] = from_f32<T>(a[j][i]);
-            yb.e[i] = from_f32<T>(b[j][i]);
+          for (int i = 0; i < W; ++i) {
+            if constexpr (SHIFT) {
+              a[j][i] = fma(a[j][i], rr, ka[j][i]);
+              b[j][i] = fma(b[j][i], rr, kb[j][i]);
+            } else {
+              a[j][i] = mul(a[j][i], rr);
+              b[j][i] = mul(b[j][i], rr);
+            }
           }
         }
-        if (put && oa[j] >= 0) *reinterpret_cast<V*>(row + oa[j]) = ya;
-        if (put && ob[j] >= 0) *reinterpret_cast<V*>(row + ob[j]) = yb;
+        if (put && oa[j] >= 0) *reinterpret_cast<V*>(to + oa[j]) = pack<T, VEC>(a[j]);
+        if (put && ob[j] >= 0) *reinterpret_cast<V*>(to + ob[j]) = pack<T, VEC>(b[j]);
       }
-      cur = load(e0 + per_turn + seg);
     }
+    if constexpr (kBulk) {
+      __syncwarp();  // the stage has been read
+      if (c + C::kStages < c_end) issue(st);
+    }
+  }
+  if constexpr (kBulk) {
+    // (only after a wait that ran out: what is on its way must land)
+    for (int i = n; i < n + C::kStages && c_begin + i < c_end; ++i)
+      mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, status, kSiteQkNorm, 200000000ull, false);
   }
 
   if constexpr (BACK) {
     if (!Y.dgain && !Y.dshift) return;
     // Sums over the heads of a warp's turn, then over the warps, in this order
-    // whatever ran when: repeated calls give the same bits.  (`table` is free:
-    // 2 x 256 floats of each warp.)
-    __syncthreads();
+    // whatever ran when: repeated calls give the same bits.
+    float* const mine = reinterpret_cast<float*>(ring);
+    __syncwarp();
     auto over_turn = [&](float v) {
       for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       return v;
@@ -322,20 +559,19 @@ __global__ void __launch_bounds__(kNormWarps * 32)
     for (int j = 0; j < N; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float g0 = over_turn(sga[j][i]), g1 = over_turn(sgb[j][i]);
+        const float g0 = over_turn(at(sga[j][i / E], i % E)), g1 = over_turn(at(sgb[j][i / E], i % E));
         float c0 = 0.f, c1 = 0.f;
-        if constexpr (SHIFT) c0 = over_turn(sca[j][i]), c1 = over_turn(scb[j][i]);
+        if constexpr (SHIFT) c0 = over_turn(at(sca[j][i / E], i % E)), c1 = over_turn(at(scb[j][i / E], i % E));
         if (seg == 0) {
-          if (oa[j] >= 0) t_cos[oa[j] + i] = g0, t_sin[oa[j] + i] = c0;
-          if (ob[j] >= 0) t_cos[ob[j] + i] = g1, t_sin[ob[j] + i] = c1;
+          if (oa[j] >= 0) mine[oa[j] + i] = g0, mine[d + oa[j] + i] = c0;
+          if (ob[j] >= 0) mine[ob[j] + i] = g1, mine[d + ob[j] + i] = c1;
         }
       }
     __syncthreads();
-    for (int k = threadIdx.x; k < 2 * d; k += kNormWarps * 32) {
-      const int part = k >= d, at = k - part * d;
+    for (int k = threadIdx.x; k < 2 * d; k += C::kWarps * 32) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kNormWarps; ++w) v += table[w][part][at];
+      for (int w = 0; w < C::kWarps; ++w) v += reinterpret_cast<float*>(smem + w * C::kWarp)[k];
       A.partials[static_cast<int64_t>(blockIdx.x) * 2 * d + k] = v;
     }
   }
@@ -383,13 +619,15 @@ struct NormCall {
 template <typename T, int VEC, bool ADJACENT, bool BACK, bool SHIFT>
 int norm_launch(const NormCall& c, NormArgs A) {
   auto kern = qk_norm_kernel<T, VEC, ADJACENT, BACK, SHIFT>;
+  using C = NormCfg<BACK>;
   // at most as many blocks as are resident at once
   static PerDeviceInit init;
   long long resident = 0;
   const cudaError_t e = once_per_device(init, [&](long long* value) {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (r != cudaSuccess) return r;
     int per_sm = 0;
-    const cudaError_t r =
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNormWarps * 32, 0);
+    r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::kWarps * 32, C::kSmem);
     *value = static_cast<long long>(per_sm < 1 ? 1 : per_sm) * num_sms();
     return r;
   }, &resident);
@@ -402,35 +640,38 @@ int norm_launch(const NormCall& c, NormArgs A) {
   while (A.lanes < A.units && A.lanes < 32) A.lanes *= 2;
   const int per_turn = 32 / A.lanes;
   A.div_pairs = fast_div_magic(A.pairs > 0 ? A.pairs : 1);
-  // Turns of an item: enough that forming its table does not show, fewer where
-  // the call is too short to fill the SMs otherwise.
+  // Turns of a chunk: one where the call is too short to fill the SMs otherwise.
   int64_t blocks[2] = {0, 0}, all = 0;
+  double cost[2] = {0.0, 0.0};
   const int64_t all_turns =
       A.tokens * (A.type[0].heads + A.type[1].heads) / per_turn;
-  const int64_t fill = all_turns / (32ll * num_sms());
-  const int turns = fill < 1 ? 1 : fill > kNormTurns ? kNormTurns : static_cast<int>(fill);
+  const int turns = all_turns < C::kTurns * resident * C::kWarps ? 1 : C::kTurns;
   for (int t = 0; t < 2; ++t) {
     NormType& Y = A.type[t];
-    Y.items = 0;
-    Y.head_item = Y.tok_item = Y.ranges = 1;
+    Y.chunks = 0;
+    Y.head_chunk = Y.tok_chunk = Y.ranges = 1;
     if (Y.heads > 0) {
       const int slots = per_turn * turns;
-      Y.head_item = Y.heads < slots ? Y.heads : slots;
-      int tk = slots / Y.head_item;
+      Y.head_chunk = Y.heads < slots ? Y.heads : slots;
+      int tk = slots / Y.head_chunk;
       if (A.pairs > 0 && tk > kNormTable / A.pairs) tk = kNormTable / A.pairs;
+      if (A.pairs > 0 && tk > 32 / A.axes) tk = 32 / A.axes;
       if (tk > A.tokens) tk = static_cast<int>(A.tokens);
-      Y.tok_item = tk;
-      Y.ranges = (Y.heads + Y.head_item - 1) / Y.head_item;
-      Y.items = (A.tokens + tk - 1) / tk * Y.ranges;
+      Y.tok_chunk = tk;
+      Y.ranges = (Y.heads + Y.head_chunk - 1) / Y.head_chunk;
+      Y.chunks = (A.tokens + tk - 1) / tk * Y.ranges;
     }
-    Y.div_head_item = fast_div_magic(Y.head_item);
-    blocks[t] = (Y.items + kNormWarps - 1) / kNormWarps;
+    Y.div_head_chunk = fast_div_magic(Y.head_chunk);
+    blocks[t] = (Y.chunks + C::kWarps - 1) / C::kWarps;
     all += blocks[t];
+    // a token's angles and factors take a warp as long as a turn and a half
+    cost[t] = static_cast<double>(Y.chunks) *
+              (turns + (A.pairs > 0 ? 1.5 * Y.tok_chunk / Y.ranges : 0.0));
   }
   const int64_t most = BACK && resident > kNormMaxBlocks ? kNormMaxBlocks : resident;
   if (all > most) {
-    // shared out by the items, one block at least where there are any
-    const int64_t q = (blocks[0] * most + all / 2) / all;
+    // shared out by the work, one block at least where there is any
+    const int64_t q = static_cast<int64_t>(cost[0] / (cost[0] + cost[1]) * most + 0.5);
     if (blocks[0] > 0 && blocks[1] > 0) {
       blocks[0] = q < 1 ? 1 : q > most - 1 ? most - 1 : q;
       blocks[1] = most - blocks[0];
@@ -442,8 +683,8 @@ int norm_launch(const NormCall& c, NormArgs A) {
   A.type[0].blocks = static_cast<int>(blocks[0]);
   A.type[1].block0 = A.type[0].blocks;
   A.type[1].blocks = static_cast<int>(blocks[1]);
-  launch_kernel(kern, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), dim3(kNormWarps * 32), 0,
-                c.st, 1, static_cast<const T*>(c.in), static_cast<const T*>(c.dout),
+  launch_kernel(kern, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), dim3(C::kWarps * 32),
+                C::kSmem, c.st, 1, static_cast<const T*>(c.in), static_cast<const T*>(c.dout),
                 static_cast<T*>(c.out), c.positions, c.inv_freq, A, c.status);
   if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
   if constexpr (BACK) {
@@ -463,7 +704,11 @@ int norm_launch(const NormCall& c, NormArgs A) {
 
 template <typename T, int VEC>
 int norm_vec(const NormCall& c, const NormArgs& A, bool adjacent, bool back) {
-  const bool shift = A.type[0].dshift || A.type[1].dshift;
+  const bool shift = back ? A.type[0].dshift || A.type[1].dshift
+                          : A.type[0].shift || A.type[1].shift;
+  if (!back && shift)
+    return adjacent ? norm_launch<T, VEC, true, false, true>(c, A)
+                    : norm_launch<T, VEC, false, false, true>(c, A);
   if (!back)
     return adjacent ? norm_launch<T, VEC, true, false, false>(c, A)
                     : norm_launch<T, VEC, false, false, false>(c, A);
@@ -564,6 +809,7 @@ int launch_qk_norm(const QkNormCall& q, cudaStream_t st) {
   A.ld_out = q.ld_out;
   A.d = q.head_dim;
   A.pairs = q.spec ? q.spec->rot_dim / 2 : 0;
+  A.axes = q.spec ? q.spec->axes : 1;
   A.centred = (q.norm->flags & MC_QK_NORM_CENTRED) ? 1 : 0;
   A.inverse = back ? 1 : 0;
   A.accumulate = q.accumulate;

@@ -121,7 +121,7 @@ def test_workspace(kw, tiles):
 
 def test_norm_scratch():
     assert L.mc_qk_norm_scratch_floats(1, 2, 1, 64) == 3 * 2 * 64
-    assert L.mc_qk_norm_scratch_floats(4096, 64, 64, 128) == 1024 * 2 * 128
+    assert L.mc_qk_norm_scratch_floats(4096, 64, 64, 128) == 512 * 2 * 128
     for bad in ((0, 1, 1, 64), (4, 0, 0, 64), (4, 1, -1, 64), (4, 1, 1, 0), (4, 1, 1, 257)):
         assert L.mc_qk_norm_scratch_floats(*bad) == 0
 
