@@ -37,7 +37,9 @@ struct XBwdArgs {
   uint8_t* tiles;
   int hk0, heads;      // the key heads of this launch
   int kv_items, q_items;
+  int shares;          // SPLIT: CTAs of a cluster
   int kv_steal, q_steal;
+  int sort;
 };
 
 // Tile (query block, key block) of a (sequence, key head) in the workspace.
@@ -98,7 +100,8 @@ struct alignas(16) XKvItem {
   int count;           // blocks of queries (-1: no more items)
   int q0, queries;     // the sequence's first query row, and its real queries
   int n, hk, kb;
-  int pad[3];
+  int first;           // its first block of queries
+  int pad[2];
 };
 constexpr int kXKvRing = 4;
 constexpr int kXKvThreads = 640;
@@ -116,11 +119,14 @@ struct XKvCfg {
   // aligned (checked at run time).
   static constexpr int kQ = D == 64 ? 3 : 2, kdO = 2;
   static constexpr int kUsed = (2 + kQ + kdO) * kTile + static_cast<int>(kXTileBytes) +
-                               4 * 128 * 4 + kXKvRing * static_cast<int>(sizeof(XKvItem)) + 36 * 8;
+                               4 * 128 * 4 + kXKvRing * static_cast<int>(sizeof(XKvItem)) + 36 * 8 + kCrossSorted;
   // one CTA per SM: it takes all 512 TMEM columns
   static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kUsed <= 227 * 1024, "dkdv kernel shared memory");
+  // SPLIT: the share's sums in 32 bits, rows padded to spread banks
+  static constexpr int kPitch = D + 4;
+  static_assert(2 * 128 * kPitch * 4 <= (2 + kQ + kdO) * kTile, "a share's sums fit");
 };
 
 // Persistent: one CTA per SM walks the (key block, key head) items, each against
@@ -137,7 +143,12 @@ struct XKvCfg {
 // dz at [16g + 8, 16g + 16), over columns that the thread itself has read.
 // An item's dV and dK are stored during the next item's first block: its
 // S^T and weights run meanwhile, as do the loads of its K and V.
-template <int D>
+//
+// Where key blocks do not fill the SMs (few key heads) a cluster of up to 8 CTAs
+// takes an item, each a share of its queries, and adds up its part of the rows of
+// dV and dK from all shares, read in their order from the others' shared memory
+// (SPLIT; 2048 queries to 4096 keys, 16 heads on 2 key heads: see the launch).
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kXKvThreads, 1)
     cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -183,6 +194,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
   void* response = bars + 32;     // 16 bytes, aligned as the items are
   uint64_t* ds_full = bars + 34;  // the dz^T tile of block i is in sDs (16 warps)
   uint64_t* ds_free = bars + 35;  // its bulk store has read sDs
+  int8_t* order = reinterpret_cast<int8_t*>(bars + 36);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -233,14 +245,17 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
   pdl_wait();  // the previous kernel on the stream has completed
   const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 384;
 
-  // Item k, the key blocks of a head one after another: they share its queries in L2.
+  if (!SPLIT && B.sort) {
+    if (warp == 3) cross_order(A, false, order, lane);
+    __syncthreads();
+  }
+  const int share = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   auto item_of = [&](int k) -> XKvItem {
     XKvItem it = {};
-    const int per_seq = B.heads * A.nkb;
-    it.n = k / per_seq;
-    const int in = k - it.n * per_seq;
-    it.hk = B.hk0 + in / A.nkb;
-    it.kb = in % A.nkb;
+    const CrossItem which = cross_item(k, B.heads, A.nkb);
+    it.n = !SPLIT && B.sort ? order[which.n] : which.n;
+    it.hk = B.hk0 + which.hk;
+    it.kb = which.block;
     const CrossRows q = cross_queries(A, it.n), kv = cross_keys(A, it.n);
     it.k0 = kv.first + it.kb * 128;
     it.real = min(max(kv.real - it.kb * 128, 0), 128);
@@ -248,6 +263,10 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
     it.q0 = q.first;
     it.queries = q.real;
     it.count = it.real > 0 ? (q.real + A.pq - 1) / A.pq : 0;
+    if constexpr (SPLIT) {
+      it.first = it.count * share / B.shares;
+      it.count = it.count * (share + 1) / B.shares - it.first;
+    }
     return it;
   };
 
@@ -261,6 +280,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         bool ok = true, v_loaded = true;
         const uint32_t q_bytes = static_cast<uint32_t>(A.G * A.pq * 128 * C::kChunks);
         OptItems steal(response, steal_bar, B.kv_items, B.kv_steal);
+        if constexpr (SPLIT) steal.k = static_cast<int>(blockIdx.x) / B.shares;
         struct Cur {
           int k0, count, q0, hk;
         };
@@ -269,7 +289,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           XKvItem it = {};
           it.count = -1;
           if (steal.more) it = item_of(steal.k);
-          c = {it.k0, it.count, it.q0, it.hk};
+          c = {it.k0, it.count, it.q0 + it.first * A.pq, it.hk};
           const int slot = r % kXKvRing;
           if (!mbar_wait(&it_empty[slot], ((r / kXKvRing) & 1) ^ 1u, status, kSiteCross))
             return false;
@@ -280,7 +300,10 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         ok = announce(0, cur);
         // (an item's first loads are issued before the next item is asked about)
         auto go_on = [&](int r) -> bool {
-          if (steal.more && !steal.next(status)) return false;
+          if constexpr (SPLIT)
+            steal.more = false;
+          else if (steal.more && !steal.next(status))
+            return false;
           return announce(r + 1, next);
         };
         for (int r = 0; ok && cur.count >= 0; ++r, cur = next) {
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
             }
           }
         }
-        steal.finish(status);
+        if constexpr (!SPLIT) steal.finish(status);
         pdl_launch();  // every load of this CTA is issued
         // Copies still in flight must land before the CTA exits.
         const int kn = v_loaded ? n : n + 1;  // K tiles issued
@@ -381,7 +404,8 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         const int slot = r % kXKvRing;
         if (!(ok = mbar_wait_warp(&it_full[slot], (r / kXKvRing) & 1, status, kSiteCross))) break;
         const int count = __shfl_sync(0xffffffffu, items[slot].count, 0);
-        const int queries = __shfl_sync(0xffffffffu, items[slot].queries, 0);
+        // (those from its first block on)
+        const int queries = __shfl_sync(0xffffffffu, items[slot].queries - items[slot].first * A.pq, 0);
         __syncwarp();
         if (leader) mbar_arrive(&it_empty[slot]);
         if (count < 0) break;
@@ -466,12 +490,12 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           const int slot = r % kXKvRing;
           if (!mbar_wait(&it_full[slot], (r / kXKvRing) & 1, status, kSiteCross)) break;
           const int count = items[slot].count, n = items[slot].n, hk = items[slot].hk,
-                    kb = items[slot].kb;
+                    kb = items[slot].kb, first = items[slot].first;
           mbar_arrive(&it_empty[slot]);
           if (count < 0) break;
           for (int i = 0; i < count; ++i, ++g) {
             if (!(ok = mbar_wait(ds_full, g & 1, status, kSiteCross))) break;
-            bulk_store(B.tiles + cross_tile(B, n, hk, i, kb) * kXTileBytes, sDs,
+            bulk_store(B.tiles + cross_tile(B, n, hk, first + i, kb) * kXTileBytes, sDs,
                        static_cast<uint32_t>(kXTileBytes));
             bulk_commit();
             bulk_wait_read();
@@ -480,6 +504,10 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         }
         bulk_wait_all();  // complete before the CTA exits
       }
+    }
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync();  // the shares are in shared memory
     }
   } else {
     // ---------------------------------------------------------- compute
@@ -526,7 +554,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       }
       const XKvItem& it = items[slot];
       have = it.count > 0;
-      if (have && grp == 0) load_query(it.q0, it.queries, it.hk, 0);
+      if (have && grp == 0) load_query(it.q0, it.queries, it.hk, it.first);
     };
     // dV and dK of the item before, in TMEM until its last products are done,
     // or (keys that no query sees) zeros.
@@ -560,7 +588,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       const XKvItem& it = items[r % kXKvRing];
       const int count = it.count;
       if (count < 0) break;
-      const int q0 = it.q0, queries = it.queries, hk = it.hk;
+      const int q0 = it.q0, queries = it.queries, hk = it.hk, first = it.first;
       const bool edge = it.real < 128, mine = t < it.real;
       for (int i = 0; i < count; ++i, ++g) {
         const float* l2 = sL + (g & 1) * 128 + grp * 32;
@@ -578,7 +606,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         // the next block's queries: loaded here, staged behind this block's work
         if (i + 1 < count) {
           have = true;
-          if (grp == 0) load_query(q0, queries, hk, i + 1);
+          if (grp == 0) load_query(q0, queries, hk, first + i + 1);
         } else {
           look_ahead(r + 1);
         }
@@ -667,12 +695,13 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         if (have) stage_query((g + 1) & 1);
       }
       if (!ok) break;
-      if (count > 0) {
+      if (count > 0 || SPLIT) {
         p_k0 = it.k0;
         p_real = it.real;
         p_slot = it.slot;
         p_hk = it.hk;
         pending = true;
+        if (SPLIT && count == 0) look_ahead(r + 1);
       } else {
         store_item(false, it.k0, it.real, it.slot, it.hk);
         look_ahead(r + 1);
@@ -680,14 +709,60 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       }
       mbar_arrive_warp(&it_empty[r % kXKvRing], lane);
     }
-    if (ok && pending && mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteCross)) {
+    if constexpr (!SPLIT) {
+      if (ok && pending && mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteCross)) {
+        tc_fence_after();
+        store_item(true, p_k0, p_real, p_slot, p_hk);
+      }
+    } else {
+      // This share's dV and dK into shared memory, over K, V, Q and dO: every
+      // product that read them is complete.
+      if (g > 0 && !mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteCross)) ok = false;
       tc_fence_after();
-      store_item(true, p_k0, p_real, p_slot, p_hk);
+      float* sums = reinterpret_cast<float*>(smem);  // [2][128][kPitch]
+      const bool has = ok && g > 0;
+#pragma unroll 1
+      for (int task = grp; task < D / 16; task += 4) {
+        const int w = task / (D / 32), c = task % (D / 32);
+        float v[32] = {};
+        if (has) tmem_ld_32x32b_x32((w == 0 ? tdV : tdK) + lane_off + c * 32, v);
+        float* to = sums + (w * 128 + t) * C::kPitch + c * 32;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(to + 4 * i) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+      __syncwarp();
+      cluster_sync();  // (every thread of every CTA, whatever it met)
+      constexpr int kPer = D / 4;  // threads of a row, four columns each
+      const int at = static_cast<int>(threadIdx.x) - 128, col = (at % kPer) * 4;
+      for (int rr = share + (at / kPer) * B.shares; rr < p_slot;
+           rr += (kXKvWarps * 32 / kPer) * B.shares) {
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int s = 0; s < B.shares; ++s) {
+            const float4 v = ld_cluster_v4(mapa_shared(sums + (w * 128 + rr) * C::kPitch + col, s));
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+          }
+          const float sc = w == 0 ? 1.f : A.scale;
+          uint2 out = make_uint2(pack_bf16x2(sum.x * sc, sum.y * sc), pack_bf16x2(sum.z * sc, sum.w * sc));
+          if (rr >= p_real) out = make_uint2(0u, 0u);  // padding
+          if (MC_DCHECK(p_k0 + rr < A.kv_rows && p_hk < A.KV, status, kSiteCross))
+            *reinterpret_cast<uint2*>((w == 0 ? B.dv : B.dk) +
+                                      (static_cast<int64_t>(p_k0) + rr) * A.ld_kv + p_hk * D + col) =
+                out;
+        }
+      }
     }
   }
 
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT) {
+    cluster_sync();  // the others have read this CTA's share
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -701,7 +776,7 @@ struct XDqCfg {
   static constexpr int kKTile = 128 * D * 2;
   static constexpr int kStage = static_cast<int>(kXTileBytes) + kKTile;
   static constexpr int kStages = 3;
-  static constexpr int kUsed = kStages * kStage + 24 * 8 + 4 * 48;  // barriers, items
+  static constexpr int kUsed = kStages * kStage + 24 * 8 + 4 * 48 + kCrossSorted;  // barriers, items, order
   // one CTA per SM, so that the CTAs that do not start are there to be stolen
   static constexpr int kSmem = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;
   static_assert(kSmem <= 227 * 1024, "dq kernel shared memory");
@@ -742,6 +817,7 @@ __global__ void __launch_bounds__(192, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   void* response = bars + 22;  // 16 bytes, aligned as the stages are
   XDqItem* items = reinterpret_cast<XDqItem*>(bars + 24);
+  int8_t* order = reinterpret_cast<int8_t*>(items + 4);
   int* status = A.status;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -773,14 +849,17 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the dK/dV kernel (the tiles) has completed
 
-  // Item k; the heads whose tiles were written last come first: they are still in L2.
+  // (the heads whose tiles were written last come first: they are still in L2)
+  if (B.sort) {
+    if (warp == 3) cross_order(A, true, order, lane);
+    __syncthreads();
+  }
   auto item_of = [&](int k) -> XDqItem {
     XDqItem it = {};
-    const int per_seq = B.heads * A.nqb;
-    it.n = A.n - 1 - k / per_seq;
-    const int in = k % per_seq;
-    it.hk = B.hk0 + B.heads - 1 - in / A.nqb;
-    it.qb = in % A.nqb;
+    const CrossItem which = cross_item(k, B.heads, A.nqb);
+    it.n = B.sort ? order[which.n] : A.n - 1 - which.n;
+    it.hk = B.hk0 + B.heads - 1 - which.hk;
+    it.qb = which.block;
     const CrossRows q = cross_queries(A, it.n), kv = cross_keys(A, it.n);
     const int at = it.qb * A.pq;
     it.q0 = q.first + at;
@@ -967,10 +1046,12 @@ int launch_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const ui
   if (!cross_q_map(&tq, q, D, A, A.ld_q) || !cross_kv_map(&tk, k, D, A) ||
       !cross_kv_map(&tv, v, D, A) || !cross_q_map(&td, dout, D, A, A.ld_o))
     return MC_ERR_CUDA;
-  static PerDeviceInit init_kv, init_q;
-  auto kv = cross_dkdv_kernel<D>;
+  static PerDeviceInit init_kv, init_split, init_q;
+  auto kv = cross_dkdv_kernel<D, false>;
+  auto kv_split = cross_dkdv_kernel<D, true>;
   auto dq = cross_dq_kernel<D>;
   if (cross_smem(init_kv, kv, XKvCfg<D>::kSmem) != cudaSuccess ||
+      cross_smem(init_split, kv_split, XKvCfg<D>::kSmem) != cudaSuccess ||
       cross_smem(init_q, dq, XDqCfg<D>::kSmem) != cudaSuccess)
     return MC_ERR_CUDA;
   const int64_t per_block = kXDeltaThreads / (D / 8) * kXDeltaPasses;
@@ -979,8 +1060,11 @@ int launch_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const ui
                 st, 1, o, dout, delta, A.q_rows, A.H, A.ld_o);
   if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
   const int at_once = heads_at_once(A), sms = num_sms();
+  B.sort = cross_sorts(A) ? 1 : 0;
+  // (items of unequal sequences are taken over by the CTAs that are done, whatever
+  // their number: the request's time is behind an item's)
   auto ctas = [&](int items, int* steal) {
-    *steal = items > 4 * sms ? 1 : 0;
+    *steal = items > (B.sort ? sms : 4 * sms) ? 1 : 0;
     return dim3(static_cast<unsigned>(*steal || items < sms ? items : sms));
   };
   for (B.hk0 = 0; B.hk0 < A.KV; B.hk0 += at_once) {
@@ -988,7 +1072,14 @@ int launch_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const ui
     B.kv_items = A.n * B.heads * A.nkb;
     B.q_items = A.n * B.heads * A.nqb;
     const dim3 kv_grid = ctas(B.kv_items, &B.kv_steal), q_grid = ctas(B.q_items, &B.q_steal);
-    launch_kernel(kv, kv_grid, dim3(kXKvThreads), XKvCfg<D>::kSmem, st, 1, tq, tk, tv, td, B);
+    // shares of an item: as many as SMs are left for, each four blocks at least
+    B.shares = 1;
+    while (B.shares < 8 && B.kv_items * B.shares * 2 <= sms && B.shares * 8 <= A.nqb) B.shares *= 2;
+    if (B.shares > 1)
+      launch_kernel(kv_split, dim3(static_cast<unsigned>(B.kv_items * B.shares)), dim3(kXKvThreads),
+                    XKvCfg<D>::kSmem, st, static_cast<unsigned>(B.shares), tq, tk, tv, td, B);
+    else
+      launch_kernel(kv, kv_grid, dim3(kXKvThreads), XKvCfg<D>::kSmem, st, 1, tq, tk, tv, td, B);
     if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
     launch_kernel(dq, q_grid, dim3(192), XDqCfg<D>::kSmem, st, 1, tk, B);
     if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;

@@ -68,7 +68,7 @@ struct XFwdCfg {
   // The dynamic shared memory starts 1024-byte aligned (checked at run time),
   // so no alignment slack is reserved: at D = 128 it would not fit.
   static constexpr int kUsed = kQTile + 2 * kKTile + kVSlots * kHalf + kXch +
-                               kXRing * static_cast<int>(sizeof(XItem)) + kBars;
+                               kXRing * static_cast<int>(sizeof(XItem)) + kBars + kCrossSorted;
   static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
   static_assert(kUsed <= 227 * 1024, "forward shared memory");
   static constexpr uint32_t kTmemCols = 512;
@@ -82,7 +82,7 @@ struct XFwdArgs {
   CrossArgs c;
   uint16_t* out;
   float* lse;
-  int items, steal;
+  int items, steal, sort;
   int shares;  // SPLIT: CTAs of a cluster
 };
 
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kXFwdThreads, 1)
   uint64_t* steal_bar = bars + 32;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
   void* response = bars + 34;  // 16 bytes, aligned as the items are
+  int8_t* order = reinterpret_cast<int8_t*>(bars + 38);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -170,14 +171,16 @@ __global__ void __launch_bounds__(kXFwdThreads, 1)
   pdl_wait();  // the previous kernel on the stream has completed
   const uint32_t tS = tmem + C::kColS, tO = tmem + C::kColO, tP = tmem + C::kColP;
 
-  // Item k, the blocks of a key head one after another: they share its keys in L2.
+  if (!SPLIT && F.sort) {
+    if (warp == 3) cross_order(A, true, order, lane);
+    __syncthreads();
+  }
   const int share = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   auto item_of = [&](int k) -> XItem {
     XItem it;
-    const int per_seq = A.KV * A.nqb;
-    const int n = k / per_seq, in = k - n * per_seq;
-    it.hk = in / A.nqb;
-    const int at = (in - it.hk * A.nqb) * A.pq;
+    const CrossItem which = cross_item(k, A.KV, A.nqb);
+    const int n = !SPLIT && F.sort ? order[which.n] : which.n, at = which.block * A.pq;
+    it.hk = which.hk;
     const CrossRows q = cross_queries(A, n), kv = cross_keys(A, n);
     it.q0 = q.first + at;
     it.real = min(max(q.real - at, 0), A.pq);
@@ -712,13 +715,16 @@ int launch_fwd_d(const uint16_t* q, const uint16_t* k, const uint16_t* v, XFwdAr
   if (!cross_q_map(&tq, q, D, A, A.ld_q) || !cross_kv_map(&tk, k, D, A) ||
       !cross_kv_map(&tv, v, D, A))
     return MC_ERR_CUDA;
-  // Shares of an item: as many as leave the SMs with work, each a key block at
-  // least.
+  // Shares of an item: as many as SMs are left for, each a key block at least
+  // (96 items of 1000 keys, D = 64: 13.5 us one CTA each, 18.8 in pairs that start in
+  // two rounds; 32 items of 8192 keys, D = 128: 43.5 us in shares of two, 27.3 of
+  // four).
   const int sms = num_sms(), blocks = (A.max_kv + kXKeys - 1) / kXKeys;
   F.shares = 1;
-  while (F.shares < 8 && F.items * F.shares * 2 <= 2 * sms && F.shares * 2 <= blocks) F.shares *= 2;
+  while (F.shares < 8 && F.items * F.shares * 2 <= sms && F.shares * 2 <= blocks) F.shares *= 2;
   if (F.shares > 1) return launch_fwd<D, true>(tq, tk, tv, F, F.items * F.shares, st);
-  F.steal = F.items > 4 * sms ? 1 : 0;
+  F.sort = cross_sorts(A) && F.items > sms ? 1 : 0;
+  F.steal = F.items > 4 * sms || F.sort ? 1 : 0;
   return launch_fwd<D, false>(tq, tk, tv, F, F.steal || F.items < sms ? F.items : sms, st);
 }
 

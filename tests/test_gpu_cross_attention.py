@@ -220,15 +220,25 @@ def test_one_token_long_states(n, sk, heads, kv_heads, d):
             kv_lens=[max(0, sk - 700 * i) for i in range(n)]).check()
 
 
+@pytest.mark.parametrize("n,sq,sk,heads,kv_heads,d", [(1, 1500, 130, 2, 1, 128), (2, 700, 100, 4, 1, 64),
+                                                      (1, 4000, 60, 2, 2, 64), (3, 900, 257, 3, 1, 128)])
+def test_many_queries_few_keys(n, sq, sk, heads, kv_heads, d):
+    """Few key blocks: the queries of an item are shared out in the backward pass."""
+    Problem(n, n * sq, n * sk, heads, kv_heads, d, q_lens=[max(1, sq - 650 * i) for i in range(n)],
+            kv_lens=[sk - 29 * i for i in range(n)], wide=64 * (d // 64)).check()
+
+
 def test_same_bits_again():
-    p = Problem(2, 2 * 30, 2 * 3000, 4, 2, 128, kv_lens=[3000, 1234])
-    p.forward()
-    o, lse = p.o.clone(), p.lse.clone()
-    first = [x.clone() for x in p.backward()]
-    for _ in range(3):
+    for p in (Problem(2, 2 * 30, 2 * 3000, 4, 2, 128, kv_lens=[3000, 1234]),
+              Problem(1, 2000, 200, 4, 2, 64),
+              Problem(20, 20 * 300, 20 * 260, 6, 6, 64, kv_lens=[13 * i for i in range(20)])):
         p.forward()
-        assert torch.equal(p.o, o) and torch.equal(p.lse, lse)
-        assert all(torch.equal(x, y) for x, y in zip(p.backward(), first))
+        o, lse = p.o.clone(), p.lse.clone()
+        first = [x.clone() for x in p.backward()]
+        for _ in range(3):
+            p.forward()
+            assert torch.equal(p.o, o) and torch.equal(p.lse, lse)
+            assert all(torch.equal(x, y) for x, y in zip(p.backward(), first))
 
 
 def test_heads_in_groups():
