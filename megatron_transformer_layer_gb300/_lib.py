@@ -672,9 +672,22 @@ def make_cross_attention(sequences, q_rows, kv_rows, heads, kv_heads, head_dim, 
 def _rows(x, what, rows, ld, width):
     """Pointer of a bf16 tensor of rows that are ld elements apart, which it must
     cover (a bare pointer is not checked)."""
+    try:
+        if x.dtype is _TYPES["bfloat16"] and x.is_cuda:
+            (n, w), (s0, s1) = x.shape, x.stride()
+            if n >= rows and w >= width and s1 == 1 and (s0 == ld or rows == 1):
+                return x.data_ptr()
+    except (AttributeError, KeyError, ValueError):  # no tensor, the first one, or not of rows
+        pass
+    return _other_rows(x, what, rows, ld, width)
+
+
+def _other_rows(x, what, rows, ld, width):
     if x is None or isinstance(x, int):
         return x
-    if str(x.dtype) != "torch.bfloat16":
+    import torch
+    _TYPES["bfloat16"] = torch.bfloat16
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"{what}: bfloat16 expected, got {x.dtype}")
     if not x.is_cuda:
         raise ValueError(f"{what}: a tensor on the GPU expected, got one on {x.device}")
@@ -689,20 +702,13 @@ def mc_attention_forward_cross(q, k, v, o, lse, cross, status=None, stream=None)
     """Attention of the rows of q to those of k and v, see make_cross_attention
     (bf16 tensors [rows, heads * head_dim] or views of wider rows; lse float32
     [heads, q_rows])."""
+    c = cross
+    a, akv = c.heads * c.head_dim, c.kv_heads * c.head_dim
+    n, nkv, ld_kv = c.q_rows, c.kv_rows, c.ld_kv
     return lib().mc_attention_forward_cross(
-        *_cross_rows(cross, q=q, k=k, v=v, o=o),
-        _array(lse, "lse", "float32", cross.heads * cross.q_rows), ctypes.byref(cross),
+        _rows(q, "q", n, c.ld_q, a), _rows(k, "k", nkv, ld_kv, akv), _rows(v, "v", nkv, ld_kv, akv),
+        _rows(o, "o", n, c.ld_o, a), _array(lse, "lse", "float32", c.heads * n), ctypes.byref(c),
         _ptr(status), _on(stream, q))
-
-
-def _cross_rows(c, **tensors):
-    got = []
-    for name, x in tensors.items():
-        of_kv = name in ("k", "v", "dk", "dv")
-        ld = c.ld_kv if of_kv else c.ld_q if name in ("q", "dq") else c.ld_o
-        got.append(_rows(x, name, c.kv_rows if of_kv else c.q_rows, ld,
-                         (c.kv_heads if of_kv else c.heads) * c.head_dim))
-    return got
 
 
 def mc_attention_backward_cross_ws_bytes(cross) -> int:
@@ -711,12 +717,16 @@ def mc_attention_backward_cross_ws_bytes(cross) -> int:
 
 def mc_attention_backward_cross(q, k, v, o, lse, dout, dq, dk, dv, delta, cross, ws, ws_bytes,
                                 status=None, stream=None) -> int:
-    rows = _cross_rows(cross, q=q, k=k, v=v, o=o, dout=dout, dq=dq, dk=dk, dv=dv)
-    n = cross.heads * cross.q_rows
-    return lib().mc_attention_backward_cross(*rows[:4], _array(lse, "lse", "float32", n), *rows[4:],
-                                             _array(delta, "delta", "float32", n),
-                                             ctypes.byref(cross), _ptr(ws), ws_bytes, _ptr(status),
-                                             _on(stream, q))
+    c = cross
+    a, akv = c.heads * c.head_dim, c.kv_heads * c.head_dim
+    n, nkv, ld_q, ld_kv, ld_o = c.q_rows, c.kv_rows, c.ld_q, c.ld_kv, c.ld_o
+    return lib().mc_attention_backward_cross(
+        _rows(q, "q", n, ld_q, a), _rows(k, "k", nkv, ld_kv, akv), _rows(v, "v", nkv, ld_kv, akv),
+        _rows(o, "o", n, ld_o, a), _array(lse, "lse", "float32", c.heads * n),
+        _rows(dout, "dout", n, ld_o, a), _rows(dq, "dq", n, ld_q, a),
+        _rows(dk, "dk", nkv, ld_kv, akv), _rows(dv, "dv", nkv, ld_kv, akv),
+        _array(delta, "delta", "float32", c.heads * n), ctypes.byref(c), _ptr(ws), ws_bytes,
+        _ptr(status), _on(stream, q))
 
 
 def mc_attention_mask_table_ints(micro_batch, seq_len) -> int:

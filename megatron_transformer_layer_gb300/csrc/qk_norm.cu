@@ -49,7 +49,8 @@ struct NormType {
   const uint16_t* shift;  // or NULL: zeros
   float* dgain;           // or NULL
   float* dshift;
-  int64_t chunks;      // (token group, head range) pairs, shared out to the warps in runs
+  int64_t chunks;      // (token group, head range) pairs, shared out to the warps in runs:
+  int64_t per_warp, more;  // so many each, the first `more` of them one more
   int head0, heads;    // of the row's heads
   int tok_chunk, head_chunk, ranges;  // a chunk: tokens, heads of each; ranges per token group
   int block0, blocks;
@@ -60,7 +61,7 @@ struct NormArgs {
   NormType type[2];
   int64_t tokens, ld_in, ld_dout, ld_out;
   int d, pairs, axes;
-  int lanes, units;  // lanes of a head (a power of two) and its units
+  int lanes, log_lanes, units;  // lanes of a head (a power of two) and its units
   int centred, inverse, accumulate;
   float eps;
   uint32_t div_pairs;
@@ -163,14 +164,13 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
   pdl_launch();
   const NormType& Y = A.type[static_cast<int>(blockIdx.x) >= A.type[1].block0 ? 1 : 0];
   const int d = A.d, L = A.lanes;
-  const int seg = lane / L, per_turn = 32 / L;
+  const int seg = lane >> A.log_lanes, per_turn = 32 >> A.log_lanes;
   const float inv_d = 1.f / static_cast<float>(d);
 
   // this warp's run of chunks
-  const int64_t warps = static_cast<int64_t>(Y.blocks) * C::kWarps;
-  const int64_t me = static_cast<int64_t>(static_cast<int>(blockIdx.x) - Y.block0) * C::kWarps + warp;
-  const int64_t per = Y.chunks / warps, more = Y.chunks - per * warps;
-  const int64_t c_begin = me * per + min(me, more), c_end = c_begin + per + (me < more ? 1 : 0);
+  const int me = (static_cast<int>(blockIdx.x) - Y.block0) * C::kWarps + warp;
+  const int64_t c_begin = me * Y.per_warp + min(static_cast<int64_t>(me), Y.more);
+  const int64_t c_end = c_begin + Y.per_warp + (me < Y.more ? 1 : 0);
   struct Chunk {
     int64_t t0;
     int h0, ntok, nh;
@@ -185,8 +185,13 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
     bound(x);
   };
   Chunk x;
-  x.t0 = c_begin / Y.ranges * Y.tok_chunk;
-  x.h0 = static_cast<int>(c_begin % Y.ranges) * Y.head_chunk;
+  int64_t group;
+  if (c_begin >> 31 == 0)  // (a 64-bit division takes half a microsecond)
+    group = static_cast<uint32_t>(c_begin) / static_cast<uint32_t>(Y.ranges);
+  else
+    group = c_begin / Y.ranges;
+  x.t0 = group * Y.tok_chunk;
+  x.h0 = static_cast<int>(c_begin - group * Y.ranges) * Y.head_chunk;
   bound(x);
   [[maybe_unused]] Chunk ahead = x;  // the next one to load
   // A row's heads of the next chunk into stage st, a copy per token and input.
@@ -209,6 +214,15 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
     for (int i = 0; i < C::kStages; ++i)
       if (c_begin + i < c_end) issue(i);
   }
+  // The positions of a group's tokens (axis by axis, 32 at most: a lane each) are
+  // loaded a group ahead.
+  const int my_axis = lane / Y.tok_chunk, my_tok = lane - my_axis * Y.tok_chunk;
+  auto positions_of = [&](int64_t t0) -> int32_t {
+    return A.pairs > 0 && my_axis < A.axes && t0 + my_tok < A.tokens
+               ? positions[my_axis * A.tokens + t0 + my_tok]
+               : 0;
+  };
+  int32_t pos_next = c_begin < c_end ? positions_of(x.t0) : 0;
   uint32_t* const words = reinterpret_cast<uint32_t*>(turns + kNormMaxDim / 2 + C::kWarps * C::kStages);
   uint8_t* const axis = reinterpret_cast<uint8_t*>(words + 2 * kNormWords);
   for (int p = threadIdx.x; p < A.pairs; p += C::kWarps * 32) {
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
   int oa[N], ob[N], pa[N], pb[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int u = lane % L + j * L;
+    const int u = (lane & (L - 1)) + j * L;
     oa[j] = ob[j] = pa[j] = pb[j] = -1;
     if (u < A.units) {
       if (kSplit && u * VEC < A.pairs) {
@@ -241,7 +255,7 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
   // Gains and shifts, bf16, unit by unit in shared memory: the first vector's
   // element in the low half of a word, the second's above.  (Forward, they are
   // read once per token, into its factors.)
-  if (warp == 0 && seg == 0) {
+  if (warp == C::kWarps - 1 && seg == 0) {
     const uint32_t one = 0x3F80u;
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -262,7 +276,7 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
   auto load_words = [&](int part, int j) -> Words {
     Words w = {};
     if (oa[j] >= 0)
-      w = *reinterpret_cast<const Words*>(words + part * kNormWords + (lane % L + j * L) * VEC);
+      w = *reinterpret_cast<const Words*>(words + part * kNormWords + ((lane & (L - 1)) + j * L) * VEC);
     return w;
   };
   // (the backward pass needs the gains at every head)
@@ -322,18 +336,23 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
   }
 
   // sums over the lanes of a head
+  auto over_lanes = [&](auto&& step) {
+    switch (A.log_lanes) {  // (the usual sizes without a loop)
+      case 2: step(2), step(1); break;
+      case 3: step(4), step(2), step(1); break;
+      case 4: step(8), step(4), step(2), step(1); break;
+      default:
+        for (int o = L >> 1; o > 0; o >>= 1) step(o);
+    }
+  };
   auto head_sum = [&](float& a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      if (o < L) a += __shfl_xor_sync(0xffffffffu, a, o);
+    over_lanes([&](int o) { a += __shfl_xor_sync(0xffffffffu, a, o); });
   };
   auto head_sum2 = [&](float& a, float& b) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      if (o < L) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-      }
+    over_lanes([&](int o) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    });
   };
   // x f + partner(x) h of both vectors
   auto turn = [&](int j, P (&a)[W], P (&b)[W]) {
@@ -345,15 +364,6 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
     }
   };
 
-  // The positions of a group's tokens (axis by axis, 32 at most: a lane each) are
-  // loaded a group ahead.
-  const int my_axis = lane / Y.tok_chunk, my_tok = lane - my_axis * Y.tok_chunk;
-  auto positions_of = [&](int64_t t0) -> int32_t {
-    return A.pairs > 0 && my_axis < A.axes && t0 + my_tok < A.tokens
-               ? positions[my_axis * A.tokens + t0 + my_tok]
-               : 0;
-  };
-  int32_t pos_next = c_begin < c_end ? positions_of(x.t0) : 0;
   int64_t tabled = -1;  // the token group whose angles are in the table
   int held = -1;        // and the token of it in cs, sn
   int n = 0;            // chunks done
@@ -381,34 +391,35 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
 #pragma unroll 1
     for (int e0 = 0; e0 < total; e0 += per_turn) {
       // (token, head) e of the chunk: this lane's, or none
-      const int e = e0 + seg;
-      const bool live = e < total;
-      int tok = 0, head = live ? e : 0;
-      if (x.ntok > 1 && live) {
+      const bool live = e0 + seg < total;
+      const int e = live ? e0 + seg : 0;
+      int tok = 0, head = e;
+      if (x.ntok > 1) {
         tok = x.nh == Y.head_chunk ? fast_div(e, Y.div_head_chunk) : e / x.nh;
         head = e - tok * x.nh;
       }
-      head += Y.head0 + x.h0;
+      // (Lanes without a vector or a head load some other one: what they make of it
+      // enters no sum and is not stored.)
+      const int64_t col = static_cast<int64_t>(Y.head0 + x.h0 + head) * d;
       const T* row;
       [[maybe_unused]] const T* drow = nullptr;
       if constexpr (kBulk) {
-        row = reinterpret_cast<const T*>(ring + st * C::kStage) + (live ? e : 0) * d;
+        row = reinterpret_cast<const T*>(ring + st * C::kStage) + e * d;
         if constexpr (BACK) drow = row + C::kTurns * kNormTurnBytes / static_cast<int>(sizeof(T));
       } else {
-        row = in + (x.t0 + tok) * A.ld_in + static_cast<int64_t>(head) * d;
-        if constexpr (BACK) drow = dout + (x.t0 + tok) * A.ld_dout + static_cast<int64_t>(head) * d;
+        row = in + (x.t0 + tok) * A.ld_in + col;
+        if constexpr (BACK) drow = dout + (x.t0 + tok) * A.ld_dout + col;
       }
-      P a[N][W] = {}, b[N][W] = {};
-      [[maybe_unused]] P ta[N][W] = {}, tb[N][W] = {};
+      P a[N][W], b[N][W];
+      [[maybe_unused]] P ta[N][W], tb[N][W];
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (live && oa[j] >= 0) {
-          unpack<T, VEC>(*reinterpret_cast<const V*>(row + oa[j]), a[j]);
-          if constexpr (BACK) unpack<T, VEC>(*reinterpret_cast<const V*>(drow + oa[j]), ta[j]);
-        }
-        if (live && ob[j] >= 0) {
-          unpack<T, VEC>(*reinterpret_cast<const V*>(row + ob[j]), b[j]);
-          if constexpr (BACK) unpack<T, VEC>(*reinterpret_cast<const V*>(drow + ob[j]), tb[j]);
+        const int la = max(oa[j], 0), lb = max(ob[j], 0);
+        unpack<T, VEC>(*reinterpret_cast<const V*>(row + la), a[j]);
+        unpack<T, VEC>(*reinterpret_cast<const V*>(row + lb), b[j]);
+        if constexpr (BACK) {
+          unpack<T, VEC>(*reinterpret_cast<const V*>(drow + la), ta[j]);
+          unpack<T, VEC>(*reinterpret_cast<const V*>(drow + lb), tb[j]);
         }
       }
       if (A.pairs > 0 && live && tok != held) {
@@ -456,15 +467,20 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
       }
       float um = 0.f;  // mean(u), if it counts
       if (A.centred) {
-        P s2 = both<P>(0.f), us2 = both<P>(0.f);
+        float s1 = 0.f, us1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int j = 0; j < N; ++j) {
+          P sa = a[j][0], sb = b[j][0], va, vb;
+          if constexpr (BACK) va = ua[j][0], vb = ub[j][0];
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            s2 = add(s2, add(a[j][i], b[j][i]));
-            if constexpr (BACK) us2 = add(us2, add(ua[j][i], ub[j][i]));
+          for (int i = 1; i < W; ++i) {
+            sa = add(sa, a[j][i]);
+            sb = add(sb, b[j][i]);
+            if constexpr (BACK) va = add(va, ua[j][i]), vb = add(vb, ub[j][i]);
           }
-        float s1 = sum(s2), us1 = sum(us2);
+          s1 += (oa[j] >= 0 ? sum(sa) : 0.f) + (ob[j] >= 0 ? sum(sb) : 0.f);
+          if constexpr (BACK) us1 += (oa[j] >= 0 ? sum(va) : 0.f) + (ob[j] >= 0 ? sum(vb) : 0.f);
+        }
         if constexpr (BACK)
           head_sum2(s1, us1);
         else
@@ -475,15 +491,17 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
         for (int j = 0; j < N; ++j)
 #pragma unroll
           for (int i = 0; i < W; ++i) {
-            if (oa[j] >= 0) a[j][i] = add(a[j][i], ma);
-            if (ob[j] >= 0) b[j][i] = add(b[j][i], ma);
+            a[j][i] = add(a[j][i], ma);
+            b[j][i] = add(b[j][i], ma);
           }
       }
-      P qa = both<P>(0.f), qb = both<P>(0.f), xa = both<P>(0.f), xb = both<P>(0.f);
+      float sq = 0.f, ux = 0.f;
 #pragma unroll
-      for (int j = 0; j < N; ++j)
+      for (int j = 0; j < N; ++j) {
+        P qa = mul(a[j][0], a[j][0]), qb = mul(b[j][0], b[j][0]), xa, xb;
+        if constexpr (BACK) xa = mul(a[j][0], ua[j][0]), xb = mul(b[j][0], ub[j][0]);
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+        for (int i = 1; i < W; ++i) {
           qa = fma(a[j][i], a[j][i], qa);
           qb = fma(b[j][i], b[j][i], qb);
           if constexpr (BACK) {
@@ -491,28 +509,31 @@ __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBl
             xb = fma(b[j][i], ub[j][i], xb);
           }
         }
-      float sq = sum(add(qa, qb)), ux = sum(add(xa, xb));
+        sq += (oa[j] >= 0 ? sum(qa) : 0.f) + (ob[j] >= 0 ? sum(qb) : 0.f);
+        if constexpr (BACK) ux += (oa[j] >= 0 ? sum(xa) : 0.f) + (ob[j] >= 0 ? sum(xb) : 0.f);
+      }
       if constexpr (BACK)
         head_sum2(sq, ux);
       else
         head_sum(sq);
       const float r = rsqrtf(fmaf(sq, inv_d, A.eps));
-      T* to = out + (x.t0 + tok) * A.ld_out + static_cast<int64_t>(head) * d;
-      const bool put = live && MC_DCHECK(x.t0 + tok < A.tokens && head < Y.head0 + Y.heads, status,
+      T* to = out + (x.t0 + tok) * A.ld_out + col;
+      const bool put = live && MC_DCHECK(x.t0 + tok < A.tokens && x.h0 + head < Y.heads, status,
                                          kSiteQkNorm);
       // backward: r (u - n mean(u n) - mean(u)) = r u + x k1 + k0
       [[maybe_unused]] const P k1 = both<P>(-r * r * (ux * r * inv_d)), k0 = both<P>(-r * um);
       const P rr = both<P>(r);
+      [[maybe_unused]] const P r_live = both<P>(live ? r : 0.f), one = both<P>(live ? 1.f : 0.f);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         if constexpr (BACK) {
 #pragma unroll
           for (int i = 0; i < W; ++i) {
-            sga[j][i] = fma(mul(ta[j][i], rr), a[j][i], sga[j][i]);
-            sgb[j][i] = fma(mul(tb[j][i], rr), b[j][i], sgb[j][i]);
+            sga[j][i] = fma(mul(ta[j][i], r_live), a[j][i], sga[j][i]);
+            sgb[j][i] = fma(mul(tb[j][i], r_live), b[j][i], sgb[j][i]);
             if constexpr (SHIFT) {
-              sca[j][i] = add(sca[j][i], ta[j][i]);
-              scb[j][i] = add(scb[j][i], tb[j][i]);
+              sca[j][i] = fma(ta[j][i], one, sca[j][i]);
+              scb[j][i] = fma(tb[j][i], one, scb[j][i]);
             }
             a[j][i] = fma(ua[j][i], rr, fma(a[j][i], k1, k0));
             b[j][i] = fma(ub[j][i], rr, fma(b[j][i], k1, k0));
@@ -636,8 +657,9 @@ int norm_launch(const NormCall& c, NormArgs A) {
   const int vecs = A.d / VEC;
   A.units = ADJACENT && VEC > 1 ? (vecs + 1) / 2
                                 : A.pairs / VEC + ((A.d - 2 * A.pairs) / VEC + 1) / 2;
-  A.lanes = 1;
-  while (A.lanes < A.units && A.lanes < 32) A.lanes *= 2;
+  A.log_lanes = 0;
+  while ((1 << A.log_lanes) < A.units && A.log_lanes < 5) ++A.log_lanes;
+  A.lanes = 1 << A.log_lanes;
   const int per_turn = 32 / A.lanes;
   A.div_pairs = fast_div_magic(A.pairs > 0 ? A.pairs : 1);
   // Turns of a chunk: one where the call is too short to fill the SMs otherwise.
@@ -645,7 +667,7 @@ int norm_launch(const NormCall& c, NormArgs A) {
   double cost[2] = {0.0, 0.0};
   const int64_t all_turns =
       A.tokens * (A.type[0].heads + A.type[1].heads) / per_turn;
-  const int turns = all_turns < C::kTurns * resident * C::kWarps ? 1 : C::kTurns;
+  const int turns = all_turns < 4 * C::kTurns * resident * C::kWarps ? 1 : C::kTurns;
   for (int t = 0; t < 2; ++t) {
     NormType& Y = A.type[t];
     Y.chunks = 0;
@@ -683,6 +705,12 @@ int norm_launch(const NormCall& c, NormArgs A) {
   A.type[0].blocks = static_cast<int>(blocks[0]);
   A.type[1].block0 = A.type[0].blocks;
   A.type[1].blocks = static_cast<int>(blocks[1]);
+  for (int t = 0; t < 2; ++t) {
+    NormType& Y = A.type[t];
+    const int64_t warps = static_cast<int64_t>(Y.blocks) * C::kWarps;
+    Y.per_warp = warps > 0 ? Y.chunks / warps : 0;
+    Y.more = Y.chunks - Y.per_warp * warps;
+  }
   launch_kernel(kern, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), dim3(C::kWarps * 32),
                 C::kSmem, c.st, 1, static_cast<const T*>(c.in), static_cast<const T*>(c.dout),
                 static_cast<T*>(c.out), c.positions, c.inv_freq, A, c.status);
