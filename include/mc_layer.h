@@ -679,6 +679,32 @@ int mc_qk_norm_backward(const void* in, const void* dout, void* din, int32_t is_
                         const mc_rotary_spec* spec, const mc_qk_norm_grads* grads,
                         int32_t accumulate, float* scratch, int* status, void* stream);
 
+/* The layer with norms of its queries and keys (any of qk_norm, rotary and
+ * attention may be NULL; qk_norm NULL is mc_layer_forward_opt / _backward_opt,
+ * to the bit): after the QKV projection Q and K are normed, and turned by
+ * `rotary`, in one pass.  The backward call writes the gradients that qk_norm->
+ * grads asks for (adds them with MC_ACCUMULATE_GRADS); the forward call does not
+ * read them.  Q and K as they come from the projection are kept in `saved`,
+ * which grows by them: mc_layer_saved_bytes_norm, mc_layer_workspace_bytes_norm
+ * (of qk_norm only whether it is NULL is read).  All shape flags combine with
+ * it. */
+typedef struct mc_layer_qk_norm {
+  mc_qk_norm norm;
+  mc_qk_norm_grads grads;
+} mc_layer_qk_norm;
+size_t mc_layer_saved_bytes_norm(const mc_layer_shape* shape, const mc_layer_qk_norm* qk_norm);
+size_t mc_layer_workspace_bytes_norm(const mc_layer_shape* shape, const mc_layer_qk_norm* qk_norm,
+                                     const mc_attention_options* attention);
+int mc_layer_forward_norm(const mc_layer_shape* shape, const mc_layer_weights* w,
+                          const mc_layer_qk_norm* qk_norm, const mc_layer_rotary* rotary,
+                          const mc_attention_options* attention, const float* x, float* y,
+                          void* saved, void* ws, size_t ws_bytes, void* stream);
+int mc_layer_backward_norm(const mc_layer_shape* shape, const mc_layer_weights* w,
+                           const mc_layer_qk_norm* qk_norm, const mc_layer_rotary* rotary,
+                           const mc_attention_options* attention, const float* x, const float* dy,
+                           const void* saved, float* dx, const mc_layer_grads* grads, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* ---- Attention to keys and values of another length (an encoder's states).
  *
  * `sequences` sequences; query row i of sequence n sees all of the sequence's

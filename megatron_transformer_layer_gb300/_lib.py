@@ -116,6 +116,10 @@ class mc_qk_norm_grads(ctypes.Structure):  # noqa: N801
                 ("k_gain", ctypes.c_void_p), ("k_shift", ctypes.c_void_p)]
 
 
+class mc_layer_qk_norm(ctypes.Structure):  # noqa: N801
+    _fields_ = [("norm", mc_qk_norm), ("grads", mc_qk_norm_grads)]
+
+
 class mc_cross_attention(ctypes.Structure):  # noqa: N801
     lengths = (1 << 62,) * 4  # of the four arrays (make_cross_attention)
     _fields_ = [("sequences", ctypes.c_int32), ("heads", ctypes.c_int32),
@@ -139,6 +143,7 @@ _SZ = ctypes.c_size_t
 _OPT = ctypes.POINTER(mc_attention_options)
 _ROT = ctypes.POINTER(mc_layer_rotary)
 _NORM = ctypes.POINTER(mc_qk_norm)
+_LNORM = ctypes.POINTER(mc_layer_qk_norm)
 _CROSS = ctypes.POINTER(mc_cross_attention)
 
 _SIGNATURES = {
@@ -195,6 +200,14 @@ _SIGNATURES = {
     "mc_qk_norm_backward": (_INT, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I64, _I64, _I64,
                                    _NORM, _P, _P, ctypes.POINTER(mc_rotary_spec),
                                    ctypes.POINTER(mc_qk_norm_grads), _I32, _P, _P, _P]),
+    "mc_layer_saved_bytes_norm": (_SZ, [ctypes.POINTER(mc_layer_shape), _LNORM]),
+    "mc_layer_workspace_bytes_norm": (_SZ, [ctypes.POINTER(mc_layer_shape), _LNORM, _OPT]),
+    "mc_layer_forward_norm": (_INT, [ctypes.POINTER(mc_layer_shape),
+                                     ctypes.POINTER(mc_layer_weights), _LNORM, _ROT, _OPT, _P, _P,
+                                     _P, _P, _SZ, _P]),
+    "mc_layer_backward_norm": (_INT, [ctypes.POINTER(mc_layer_shape),
+                                      ctypes.POINTER(mc_layer_weights), _LNORM, _ROT, _OPT, _P, _P,
+                                      _P, _P, ctypes.POINTER(mc_layer_grads), _P, _SZ, _P]),
     "mc_attention_forward_cross": (_INT, [_P, _P, _P, _P, _P, _CROSS, _P, _P]),
     "mc_attention_backward_cross_ws_bytes": (_SZ, [_CROSS]),
     "mc_attention_backward_cross": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _CROSS, _P, _SZ,
@@ -648,6 +661,52 @@ def mc_qk_norm_backward(x, dout, din, tokens, q_heads, k_heads, head_dim, ld_in,
                                      _norm_ref(grads, "gradient", q_heads, k_heads, head_dim),
                                      accumulate, _array(scratch, "scratch", "float32", need),
                                      _ptr(status), _on(stream, x))
+
+
+def make_layer_qk_norm(norm, grads=None):
+    """norm: make_qk_norm, grads: make_qk_norm_grads or None.  Keeps a reference to
+    their tensors."""
+    out = mc_layer_qk_norm(norm, mc_qk_norm_grads() if grads is None else grads)
+    out.parts = (norm, grads)
+    return out
+
+
+def _layer_norm(qk_norm, shape):
+    """qk_norm for a layer of this shape, whose heads its arrays must cover."""
+    if qk_norm is None:
+        return None
+    d = shape.head_dim or shape.hidden // max(shape.heads, 1)
+    for part, what in zip(qk_norm.parts, ("norm", "gradient")):
+        _norm_ref(part, what, 1, 1, d)
+    return ctypes.byref(qk_norm)
+
+
+def mc_layer_saved_bytes_norm(shape, qk_norm) -> int:
+    return lib().mc_layer_saved_bytes_norm(ctypes.byref(shape), _ref(qk_norm))
+
+
+def mc_layer_workspace_bytes_norm(shape, qk_norm, attention) -> int:
+    return lib().mc_layer_workspace_bytes_norm(ctypes.byref(shape), _ref(qk_norm), _ref(attention))
+
+
+def mc_layer_forward_norm(shape, weights, qk_norm, rotary, attention, x, y, saved, ws, ws_bytes,
+                          stream=None) -> int:
+    return lib().mc_layer_forward_norm(ctypes.byref(shape), ctypes.byref(weights),
+                                       _layer_norm(qk_norm, shape), _rotary(rotary, shape),
+                                       _options(attention, shape.micro_batch, shape.seq_len,
+                                                shape.heads),
+                                       _ptr(x), _ptr(y), _ptr(saved), _ptr(ws), ws_bytes,
+                                       _on(stream, x))
+
+
+def mc_layer_backward_norm(shape, weights, qk_norm, rotary, attention, x, dy, saved, dx, grads, ws,
+                           ws_bytes, stream=None) -> int:
+    return lib().mc_layer_backward_norm(ctypes.byref(shape), ctypes.byref(weights),
+                                        _layer_norm(qk_norm, shape), _rotary(rotary, shape),
+                                        _options(attention, shape.micro_batch, shape.seq_len,
+                                                 shape.heads),
+                                        _ptr(x), _ptr(dy), _ptr(saved), _ptr(dx),
+                                        ctypes.byref(grads), _ptr(ws), ws_bytes, _on(stream, x))
 
 
 # ---- attention to keys and values of another length

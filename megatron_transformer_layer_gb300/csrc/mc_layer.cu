@@ -68,15 +68,18 @@ struct Dims {
   bool fp8;       // MC_FP8_HYBRID
   bool ds_tiles;  // the attention backward's dS tiles (not MC_ATTN_DQ_RECOMPUTE)
   bool ds_square; // of every block pair: an interval mask that looks ahead
+  bool qk_norm;   // norms of Q and K: what they are formed from is kept
 };
 
 // What the attention stage adds to the plain causal one (either may be NULL).
 struct AttnStage {
   const mc_layer_rotary* rotary;
   const mc_attention_options* options;
+  const mc_layer_qk_norm* norm;
 };
 
-Dims dims_of(const mc_layer_shape& sh, const mc_attention_options* attention = nullptr) {
+Dims dims_of(const mc_layer_shape& sh, const mc_attention_options* attention = nullptr,
+             bool qk_norm = false) {
   Dims D;
   D.b = sh.micro_batch;
   D.s = sh.seq_len;
@@ -90,6 +93,7 @@ Dims dims_of(const mc_layer_shape& sh, const mc_attention_options* attention = n
   D.fp8 = (sh.flags & MC_FP8_HYBRID) != 0;
   D.ds_tiles = (sh.flags & MC_ATTN_DQ_RECOMPUTE) == 0;
   D.ds_square = attention && !attention->causal;
+  D.qk_norm = qk_norm;
   return D;
 }
 
@@ -139,6 +143,7 @@ struct Carver {
 
 struct Saved {
   uint16_t *ln1, *qkv, *o, *ln2, *hp, *g;
+  uint16_t* qk_raw;  // Q | K before their norms [T, 2a]
   float *mu1, *rs1, *lse, *x1, *mu2, *rs2;
   // MC_FP8_HYBRID: what the backward reads of the forward's 8-bit operands --
   // the transposed (K-major over tokens) activations for the weight
@@ -163,6 +168,7 @@ Saved plan_saved(const Dims& D, void* p, size_t* bytes) {  // NOLINT
   S.rs2 = c.take<float>(D.T);
   S.hp = c.take<uint16_t>(D.T * D.f);
   S.g = c.take<uint16_t>(D.T * D.f);
+  S.qk_raw = D.qk_norm ? c.take<uint16_t>(D.T * 2 * D.a) : nullptr;
   S.ln1_t = S.o_t = S.ln2_t = S.g_t = S.wqkv_t = S.wo_t = S.w1_t = S.w2_t = nullptr;
   S.scale_inv = nullptr;
   if (D.fp8) {
@@ -219,6 +225,8 @@ Work plan_ws(const Dims& D, bool with_saved, void* p, size_t* bytes) {
   const size_t col_part = static_cast<size_t>(kColsumMaxSplits) * widest;
   size_t part = ln_part > col_part ? ln_part : col_part;
   if (part < fp8_scratch_floats()) part = fp8_scratch_floats();
+  if (D.qk_norm && part < qk_norm_scratch_floats(D.T, D.H, D.H, D.d))
+    part = qk_norm_scratch_floats(D.T, D.H, D.H, D.d);
   W.partials = c.take<float>(part);
   W.ln1_q = W.o_q = W.ln2_q = W.g_q = W.wqkv_q = W.wo_q = W.w1_q = W.w2_q = nullptr;
   W.dy_q = W.dy_t = W.dhp_q = W.dhp_t = W.dx1_q = W.dx1_t = W.dqkv_q = W.dqkv_t = nullptr;
@@ -288,16 +296,47 @@ int check_stage(const Dims& D, const AttnStage& A) {
     if (!A.rotary->positions || !A.rotary->inv_freq) return MC_ERR_NULLPTR;
     if (!al(A.rotary->positions, 4) || !al(A.rotary->inv_freq, 4)) return MC_ERR_ALIGN;
   }
+  if (A.norm) {
+    MC_TRY(check_qk_norm(&A.norm->norm));
+    const mc_qk_norm_grads& g = A.norm->grads;
+    if (!al(g.q_gain, 4) || !al(g.q_shift, 4) || !al(g.k_gain, 4) || !al(g.k_shift, 4))
+      return MC_ERR_ALIGN;
+  }
   return A.options ? check_attention_options(A.options) : MC_OK;
 }
 
-// The attention stage: Q and K turn in place in the packed Q|K|V rows, then
-// causal attention or attention over the interval mask.
+// The norms of Q and K, which turn as they pass, if they do: from S.qk_raw into
+// the packed rows, and their gradients in place in W.dqkv.
+QkNormCall stage_norm(const Dims& D, const AttnStage& A, const Saved& S, const Work& W) {
+  QkNormCall q = {};
+  q.in = S.qk_raw;
+  q.out = S.qkv;
+  q.bf16 = true;
+  q.tokens = D.T;
+  q.ld_in = 2 * D.a;
+  q.ld_dout = q.ld_out = 3 * D.a;
+  q.q_heads = q.k_heads = static_cast<int>(D.H);
+  q.head_dim = static_cast<int>(D.d);
+  q.norm = &A.norm->norm;
+  if (A.rotary) {
+    q.positions = A.rotary->positions;
+    q.inv_freq = A.rotary->inv_freq;
+    q.spec = &A.rotary->spec;
+  }
+  q.status = W.status;
+  return q;
+}
+
+// The attention stage: Q and K are normed on their way into the packed Q|K|V
+// rows, or turn in place there, then causal attention or attention over the
+// interval mask.
 int attention_stage_forward(const Dims& D, const AttnStage& A, const Saved& S, const Work& W,
                             cudaStream_t st) {
   const int b = static_cast<int>(D.b), s = static_cast<int>(D.s), H = static_cast<int>(D.H),
             d = static_cast<int>(D.d);
-  if (A.rotary)
+  if (A.norm)
+    MC_TRY(launch_qk_norm(stage_norm(D, A, S, W), st));
+  else if (A.rotary)
     MC_TRY(launch_rotary(S.qkv, S.qkv, true, D.T, 2 * H, d, 3 * D.a, 3 * D.a, A.rotary->positions,
                          A.rotary->inv_freq, &A.rotary->spec, false, W.status, st));
   if (A.options)
@@ -307,7 +346,7 @@ int attention_stage_forward(const Dims& D, const AttnStage& A, const Saved& S, c
 
 // Its backward pass: dQ | dK | dV into W.dqkv, dQ and dK turned back there.
 int attention_stage_backward(const Dims& D, const AttnStage& A, const Saved& S, const Work& W,
-                             cudaStream_t st) {
+                             int acc, cudaStream_t st) {
   const int b = static_cast<int>(D.b), s = static_cast<int>(D.s), H = static_cast<int>(D.H),
             d = static_cast<int>(D.d);
   if (A.options)
@@ -316,6 +355,15 @@ int attention_stage_backward(const Dims& D, const AttnStage& A, const Saved& S, 
   else
     MC_TRY(launch_attention_backward(S.qkv, S.o, S.lse, W.dO, W.dqkv, W.delta, b, s, H, d,
                                      W.status, st, W.ds));
+  if (A.norm) {
+    QkNormCall q = stage_norm(D, A, S, W);
+    q.backward = true;
+    q.dout = q.out = W.dqkv;
+    q.grads = &A.norm->grads;
+    q.accumulate = acc;
+    q.scratch = W.partials;
+    return launch_qk_norm(q, st);
+  }
   if (!A.rotary) return MC_OK;
   return launch_rotary(W.dqkv, W.dqkv, true, D.T, 2 * H, d, 3 * D.a, 3 * D.a, A.rotary->positions,
                        A.rotary->inv_freq, &A.rotary->spec, true, W.status, st);
@@ -331,10 +379,14 @@ extern "C" {
 int mc_layer_check_shape(const mc_layer_shape* shape) { return check_shape(shape); }
 
 size_t mc_layer_saved_bytes(const mc_layer_shape* shape) {
+  return mc_layer_saved_bytes_norm(shape, nullptr);
+}
+
+size_t mc_layer_saved_bytes_norm(const mc_layer_shape* shape, const mc_layer_qk_norm* qk_norm) {
   if (check_shape(shape) != MC_OK) return 0;
   if (recompute(*shape)) return 0;  // nothing is kept between the passes
   size_t n = 0;
-  plan_saved(dims_of(*shape), nullptr, &n);
+  plan_saved(dims_of(*shape, nullptr, qk_norm != nullptr), nullptr, &n);
   return n;
 }
 
@@ -344,9 +396,14 @@ size_t mc_layer_workspace_bytes(const mc_layer_shape* shape) {
 
 size_t mc_layer_workspace_bytes_opt(const mc_layer_shape* shape,
                                     const mc_attention_options* attention) {
+  return mc_layer_workspace_bytes_norm(shape, nullptr, attention);
+}
+
+size_t mc_layer_workspace_bytes_norm(const mc_layer_shape* shape, const mc_layer_qk_norm* qk_norm,
+                                     const mc_attention_options* attention) {
   if (check_shape(shape) != MC_OK) return 0;
   size_t n = 0;
-  plan_ws(dims_of(*shape, attention), recompute(*shape), nullptr, &n);
+  plan_ws(dims_of(*shape, attention, qk_norm != nullptr), recompute(*shape), nullptr, &n);
   return n;
 }
 
@@ -371,6 +428,23 @@ Shards shards_of(const Dims& D, bool sp) { return sp ? Shards{D.t, D.T / D.t} : 
 // partial sums.  QKV and fc1 read all shards' LayerNorm output, which lie
 // side by side in one buffer: the all-gather.
 constexpr int kE4M3 = 0, kE5M2 = 1;
+
+// The QKV projection: one product into the packed rows, or, where Q and K are
+// normed on their way there, Q | K beside them and V into its columns.
+struct QkvPart {
+  int64_t col0, cols;
+  uint16_t* out;
+  int64_t ld;
+};
+struct QkvParts {
+  QkvPart part[2];
+  const QkvPart* begin() const { return part; }
+  const QkvPart* end() const { return part + 2; }
+};
+QkvParts qkv_parts(const Dims& D, const Saved& S) {
+  if (!D.qk_norm) return {{{0, 3 * D.a, S.qkv, 3 * D.a}, {0, 0, nullptr, 0}}};
+  return {{{0, 2 * D.a, S.qk_raw, 2 * D.a}, {2 * D.a, D.a, S.qkv + 2 * D.a, 3 * D.a}}};
+}
 
 // F1..F7 with FP8 GEMMs (MC_FP8_HYBRID): every GEMM operand is quantised to
 // E4M3 first (per-tensor current scaling) -- into a row-major copy for this
@@ -398,9 +472,11 @@ int enqueue_forward_fp8(const Dims& D, const AttnStage& A, const mc_layer_weight
   MC_TRY(quant(S.ln1, true, D.T, D.h, W.ln1_q, S.ln1_t, si + 0));
   // F2  QKV
   R.next("F2 QKV");
-  MC_TRY(launch_gemm_fp8(D.T, 3 * D.a, D.h, W.ln1_q, D.h, kE4M3, W.wqkv_q, D.h, kE4M3, si + 0,
-                         si + 4, S.qkv, 3 * D.a, MC_EPI_BIAS_BF16, w->b_qkv, nullptr, 0, 0, 1,
-                         W.status, st));
+  for (const QkvPart& p : qkv_parts(D, S))
+    if (p.cols)
+      MC_TRY(launch_gemm_fp8(D.T, p.cols, D.h, W.ln1_q, D.h, kE4M3, W.wqkv_q + p.col0 * D.h, D.h,
+                             kE4M3, si + 0, si + 4, p.out, p.ld, MC_EPI_BIAS_BF16,
+                             w->b_qkv + p.col0, nullptr, 0, 0, 1, W.status, st));
   // F3  attention (bf16), O quantised
   R.next("F3 causal attention");
   MC_TRY(attention_stage_forward(D, A, S, W, st));
@@ -442,8 +518,11 @@ int enqueue_forward(const Dims& D, const AttnStage& A, const mc_layer_weights* w
   }
   // F2  QKV (column-parallel: every partition's heads are output columns)
   R.next("F2 QKV");
-  MC_TRY(launch_gemm(D.T, 3 * D.a, D.h, S.ln1, D.h, 0, w->w_qkv, D.h, 0, S.qkv, 3 * D.a,
-                     MC_EPI_BIAS_BF16, w->b_qkv, nullptr, 0, 0, 1, W.status, st));
+  for (const QkvPart& p : qkv_parts(D, S))
+    if (p.cols)
+      MC_TRY(launch_gemm(D.T, p.cols, D.h, S.ln1, D.h, 0, w->w_qkv + p.col0 * D.h, D.h, 0, p.out,
+                         p.ld, MC_EPI_BIAS_BF16, w->b_qkv + p.col0, nullptr, 0, 0, 1, W.status,
+                         st));
   // F3  attention, local per head
   R.next("F3 causal attention");
   MC_TRY(attention_stage_forward(D, A, S, W, st));
@@ -523,7 +602,7 @@ int enqueue_backward_fp8(const Dims& D, const AttnStage& A, const mc_layer_weigh
                          W.dO, D.a, MC_EPI_STORE_BF16, nullptr, nullptr, 0, 0, 1, W.status, st));
   // B5  attention backward (bf16) -> dQ | dK | dV
   R.next("B5 attention backward");
-  MC_TRY(attention_stage_backward(D, A, S, W, st));
+  MC_TRY(attention_stage_backward(D, A, S, W, acc, st));
   // B6  QKV: db_qkv; dWqkv = dqkv^T ln1; dln1 = sum_p dqkv_p Wqkv_p
   R.next("B6 QKV");
   MC_TRY(launch_colsum(W.dqkv, true, D.T, 3 * D.a, G.b_qkv, acc, nullptr, W.partials, W.status, st));
@@ -553,13 +632,21 @@ int mc_layer_forward_opt(const mc_layer_shape* shape, const mc_layer_weights* w,
                          const mc_layer_rotary* rotary, const mc_attention_options* attention,
                          const float* x, float* y, void* saved, void* ws, size_t ws_bytes,
                          void* stream) {
+  return mc_layer_forward_norm(shape, w, nullptr, rotary, attention, x, y, saved, ws, ws_bytes,
+                               stream);
+}
+
+int mc_layer_forward_norm(const mc_layer_shape* shape, const mc_layer_weights* w,
+                          const mc_layer_qk_norm* qk_norm, const mc_layer_rotary* rotary,
+                          const mc_attention_options* attention, const float* x, float* y,
+                          void* saved, void* ws, size_t ws_bytes, void* stream) {
   MC_TRY(check_shape(shape));
   MC_TRY(check_weights(w));
   const bool rc_mode = recompute(*shape);
   if (!x || !y || (!saved && !rc_mode) || !ws) return MC_ERR_NULLPTR;
   if (!al(x, 16) || !al(y, 16) || (saved && !al(saved, 256)) || !al(ws, 256)) return MC_ERR_ALIGN;
-  const Dims D = dims_of(*shape, attention);
-  const AttnStage A = {rotary, attention};
+  const Dims D = dims_of(*shape, attention, qk_norm != nullptr);
+  const AttnStage A = {rotary, attention, qk_norm};
   MC_TRY(check_stage(D, A));
   size_t need = 0;
   plan_ws(D, rc_mode, nullptr, &need);
@@ -582,6 +669,15 @@ int mc_layer_backward_opt(const mc_layer_shape* shape, const mc_layer_weights* w
                           const mc_layer_rotary* rotary, const mc_attention_options* attention,
                           const float* x, const float* dy, const void* saved, float* dx,
                           const mc_layer_grads* grads, void* ws, size_t ws_bytes, void* stream) {
+  return mc_layer_backward_norm(shape, w, nullptr, rotary, attention, x, dy, saved, dx, grads, ws,
+                                ws_bytes, stream);
+}
+
+int mc_layer_backward_norm(const mc_layer_shape* shape, const mc_layer_weights* w,
+                           const mc_layer_qk_norm* qk_norm, const mc_layer_rotary* rotary,
+                           const mc_attention_options* attention, const float* x, const float* dy,
+                           const void* saved, float* dx, const mc_layer_grads* grads, void* ws,
+                           size_t ws_bytes, void* stream) {
   MC_TRY(check_shape(shape));
   MC_TRY(check_weights(w));
   MC_TRY(check_grads(grads));
@@ -589,8 +685,8 @@ int mc_layer_backward_opt(const mc_layer_shape* shape, const mc_layer_weights* w
   if (!x || !dy || (!saved && !rc_mode) || !dx || !ws) return MC_ERR_NULLPTR;
   if (!al(x, 16) || !al(dy, 16) || !al(dx, 16) || (saved && !al(saved, 256)) || !al(ws, 256))
     return MC_ERR_ALIGN;
-  const Dims D = dims_of(*shape, attention);
-  const AttnStage A = {rotary, attention};
+  const Dims D = dims_of(*shape, attention, qk_norm != nullptr);
+  const AttnStage A = {rotary, attention, qk_norm};
   MC_TRY(check_stage(D, A));
   size_t need = 0;
   plan_ws(D, rc_mode, nullptr, &need);
@@ -661,7 +757,7 @@ int mc_layer_backward_opt(const mc_layer_shape* shape, const mc_layer_weights* w
                      nullptr, nullptr, 0, 0, 1, W.status, st));
   // B5  attention backward -> dQ | dK | dV
   R.next("B5 attention backward");
-  MC_TRY(attention_stage_backward(D, A, S, W, st));
+  MC_TRY(attention_stage_backward(D, A, S, W, acc, st));
   // B6  QKV: db_qkv, dWqkv = dqkv^T ln1, dln1 = sum_p dqkv_p Wqkv_p (per
   R.next("B6 QKV");
   //     shard in sequence-parallel mode)

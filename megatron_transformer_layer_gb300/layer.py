@@ -28,11 +28,14 @@ class TransformerLayer:
     def __init__(self, micro_batch, seq_len, hidden, heads, ffn_hidden, tp_parts=1, head_dim=0,
                  params=None, device="cuda", accumulate_grads=False, recompute=False,
                  workspace=None, sequence_parallel=False, fp8=False, attn_dq_recompute=False,
-                 rotary=None, attention=None):
+                 rotary=None, attention=None, qk_norm=None):
         # attn_dq_recompute: the attention backward forms S and dP again for
         # dQ instead of keeping dS tiles (whose workspace grows as seq_len^2)
         # rotary (make_layer_rotary), attention (make_attention_options):
         # positions and an interval mask of the attention stage, see set_stage
+        # qk_norm (make_qk_norm): norms of Q and K, head by head.  The gradients
+        # of its gains and shifts are grads["q_norm_g"], ["q_norm_b"],
+        # ["k_norm_g"] and ["k_norm_b"], of those it has
         flags = (L.MC_ACCUMULATE_GRADS if accumulate_grads else 0) | \
             (L.MC_RECOMPUTE_ACTIVATIONS if recompute else 0) | \
             (L.MC_SEQUENCE_PARALLEL if sequence_parallel else 0) | \
@@ -44,9 +47,10 @@ class TransformerLayer:
         self.device = torch.device(device)
         self.tokens = micro_batch * seq_len
         self.hidden = hidden
-        self.saved_bytes = L.mc_layer_saved_bytes(self.shape)
         self.rotary, self.attention = rotary, attention
-        self.ws_bytes = L.mc_layer_workspace_bytes_opt(self.shape, attention)
+        self.qk_norm = None if qk_norm is None else L.make_layer_qk_norm(qk_norm)
+        self.saved_bytes = L.mc_layer_saved_bytes_norm(self.shape, self.qk_norm)
+        self.ws_bytes = L.mc_layer_workspace_bytes_norm(self.shape, self.qk_norm, attention)
         # uint8 buffers: the caching allocator returns >= 512-byte aligned blocks.
         # With recomputation nothing is saved and a workspace may be shared by
         # the layers of a stack (pass the same `workspace` tensor to each).
@@ -68,6 +72,8 @@ class TransformerLayer:
         self.grads = {k: torch.zeros(v, dtype=torch.float32, device=self.device)
                       for k, v in shapes.items()}
         self._grads_c = L.make_grads(self.grads)
+        if qk_norm is not None:
+            self._set_norm(qk_norm)
         self._x = None
 
     @staticmethod
@@ -91,11 +97,27 @@ class TransformerLayer:
         self.params = params
         self.weights = L.make_weights(params)
 
+    def _set_norm(self, norm):
+        names = ("q_norm_g", "q_norm_b", "k_norm_g", "k_norm_b")
+        d = self.shape.head_dim or self.hidden // self.shape.heads
+        for name, x in zip(names, norm.tensors):
+            if x is not None and name not in self.grads:
+                self.grads[name] = torch.zeros(d, dtype=torch.float32, device=self.device)
+        gq, bq, gk, bk = (self.grads.get(n) if x is not None else None
+                          for n, x in zip(names, norm.tensors))
+        self.qk_norm = L.make_layer_qk_norm(norm, L.make_qk_norm_grads(gq, gk, bq, bk))
+
+    def set_qk_norm(self, norm):
+        """Other gains, shifts or eps (make_qk_norm) for a layer built with norms."""
+        if self.qk_norm is None:
+            raise ValueError("the layer was built without norms of Q and K: it keeps no room for them")
+        self._set_norm(norm)
+
     def set_stage(self, rotary=None, attention=None):
         """Positions and interval mask of the following forward / backward pairs
         (the tensors they point to stay the caller's).  The workspace must cover
         them: a mask that looks ahead needs a layer built with one."""
-        if L.mc_layer_workspace_bytes_opt(self.shape, attention) > self.ws_bytes:
+        if L.mc_layer_workspace_bytes_norm(self.shape, self.qk_norm, attention) > self.ws_bytes:
             raise L.McError(L.MC_ERR_WORKSPACE, "set_stage")
         self.rotary, self.attention = rotary, attention
 
@@ -105,9 +127,9 @@ class TransformerLayer:
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if y is None:
             y = torch.empty_like(x)
-        _check(L.mc_layer_forward_opt(self.shape, self.weights, self.rotary, self.attention, x, y,
-                                      self.saved, self.ws, self.ws_bytes, self._stream(stream)),
-               "mc_layer_forward")
+        _check(L.mc_layer_forward_norm(self.shape, self.weights, self.qk_norm, self.rotary,
+                                       self.attention, x, y, self.saved, self.ws, self.ws_bytes,
+                                       self._stream(stream)), "mc_layer_forward")
         self._x = x
         return y
 
@@ -116,9 +138,10 @@ class TransformerLayer:
         x = self._x if x is None else x
         if dx is None:
             dx = torch.empty_like(dy)
-        _check(L.mc_layer_backward_opt(self.shape, self.weights, self.rotary, self.attention, x, dy,
-                                       self.saved, dx, self._grads_c, self.ws, self.ws_bytes,
-                                       self._stream(stream)), "mc_layer_backward")
+        _check(L.mc_layer_backward_norm(self.shape, self.weights, self.qk_norm, self.rotary,
+                                        self.attention, x, dy, self.saved, dx, self._grads_c,
+                                        self.ws, self.ws_bytes, self._stream(stream)),
+               "mc_layer_backward")
         return dx
 
     def device_status(self, stream=None) -> int:
