@@ -167,6 +167,20 @@ def test_other_norms_and_a_graph():
         TransformerLayer(B, S, HID, H, F, params=params).set_qk_norm(a)
 
 
+def test_norms_that_do_not_cover_a_head():
+    params = TransformerLayer.random_params(HID, H, F, seed=3)
+    layer = TransformerLayer(B, S, HID, H, F, params=params, qk_norm=make_norm(True))
+    x = torch.randn(T, HID, generator=gen(1)).to(DEV)
+    short = L.make_qk_norm(vec(1, 1.0), vec(2, 1.0, D - 1))
+    layer.set_qk_norm(short)
+    with pytest.raises(ValueError, match="norm of k: 64 elements"):
+        layer.forward(x)
+    w = (layer.shape, layer.weights, L.make_layer_qk_norm(
+        make_norm(True), L.make_qk_norm_grads(torch.zeros(32, device=DEV))), None, None)
+    with pytest.raises(ValueError, match="gradient of q: 64 elements"):
+        L.mc_layer_backward_norm(*w, x, x, layer.saved, x, layer._grads_c, layer.ws, layer.ws_bytes)
+
+
 @pytest.mark.parametrize("heads,kv_heads,d", [(4, 4, 64), (6, 2, 128)])
 def test_a_decoders_cross_attention(heads, kv_heads, d):
     """Queries from one tensor, keys from another, each normed (the keys turned
