@@ -114,13 +114,14 @@ __device__ __forceinline__ void cross_load_q(void* dst, const CUtensorMap* map, 
     tma_load_3d(dst, map, bar, c * 64, hk * A.G, q0);
 }
 
-// Rows [valid, 128) of a [128][D] tile (64-wide chunks 16 KB apart) become
+// Rows [valid, end) of a [128][D] tile (64-wide chunks 16 KB apart) become
 // zeros, by a converged warp, before it issues products that contract over
 // them: a weight of 0 there does not help against a NaN.
 template <int D>
-__device__ __forceinline__ void cross_clear_tail(uint8_t* tile, int valid, int lane) {
+__device__ __forceinline__ void cross_clear_tail(uint8_t* tile, int valid, int lane,
+                                                 int end = 128) {
 #pragma unroll 1
-  for (int at = valid * 128 + lane * 16; at < 128 * 128; at += 512) {
+  for (int at = valid * 128 + lane * 16; at < end * 128; at += 512) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       *reinterpret_cast<uint4*>(tile + c * 16384 + at) = make_uint4(0, 0, 0, 0);
@@ -206,5 +207,10 @@ inline CrossArgs cross_args(const mc_cross_attention& c, int* status) {
   A.status = status;
   return A;
 }
+
+// The forward of two CTAs per SM, attention_cross_pair.cu.
+int launch_attention_cross_pair(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                uint16_t* o, float* lse, const CrossArgs& c, int d,
+                                cudaStream_t st);
 
 }  // namespace mc

@@ -16,11 +16,11 @@
 // its own), across items too.
 // TMEM: S [0, 256), O [256, 256 + D), P [384, 512) (bf16 pairs, 256 keys).
 //
-// Where items fill the SMs the kernel is persistent, one CTA per SM.  Where
-// they do not (a few queries, long states) a cluster of up to 8 CTAs takes an
-// item, each a share of its keys; they leave maxima, sums and O in shared memory
-// and each adds up its part of the rows, read from the others' shared memory in
-// the order of their shares (SPLIT).
+// Where items fill the SMs the kernel is persistent, one CTA per SM (D = 128 and many
+// keys; for the others see kXPairKeys).  Where they do not (a few queries, many
+// keys) a cluster of up to 8 CTAs takes an item, each a share of its keys; they leave
+// maxima, sums and O in shared memory and each adds up its part of the rows, read
+// from the others' shared memory in the order of their shares (SPLIT).
 //
 // P is rounded to bf16, by at most 2^-8 of itself: an operand of a tcgen05
 // product has the type of the other one, here V's.  The row sums take P before
@@ -41,6 +41,13 @@ constexpr int kXFwdThreads = 384;
 constexpr int kXRegsIo = 72, kXRegsSoftmax = 216;
 constexpr int kXKeys = 256;  // keys per block
 constexpr int kXRing = 4;    // items in shared memory
+// Up to so many keys two CTAs per SM take the items (attention_cross_pair.cu): at
+// D = 128, 4 x 1037 queries of 64 heads, 333 keys 67 us against 94 of this kernel, 900
+// keys 136 against 144, 960 139 against 141, 1024 140 against 136; one query of 8 heads
+// to ragged lengths up to 8192 (32 of them) 120 against 96.  At D = 64 always, where P
+// has columns of its own there: 333 keys 56 against 86, 8192 keys 586 against 655, one
+// query to 300 (300 sequences, 12 heads) 67 against 144.
+constexpr int kXPairKeys = 960;
 // O is rescaled only when a row's maximum grows by more than this (log2
 // units): P stays below 2^8 and the final division by the sum, taken against
 // the same maximum, cancels the difference.
@@ -711,10 +718,6 @@ template <int D>
 int launch_fwd_d(const uint16_t* q, const uint16_t* k, const uint16_t* v, XFwdArgs& F,
                  cudaStream_t st) {
   const CrossArgs& A = F.c;
-  CUtensorMap tq, tk, tv;
-  if (!cross_q_map(&tq, q, D, A, A.ld_q) || !cross_kv_map(&tk, k, D, A) ||
-      !cross_kv_map(&tv, v, D, A))
-    return MC_ERR_CUDA;
   // Shares of an item: as many as SMs are left for, each a key block at least
   // (96 items of 1000 keys, D = 64: 13.5 us one CTA each, 18.8 in pairs that start in
   // two rounds; 32 items of 8192 keys, D = 128: 43.5 us in shares of two, 27.3 of
@@ -722,10 +725,20 @@ int launch_fwd_d(const uint16_t* q, const uint16_t* k, const uint16_t* v, XFwdAr
   const int sms = num_sms(), blocks = (A.max_kv + kXKeys - 1) / kXKeys;
   F.shares = 1;
   while (F.shares < 8 && F.items * F.shares * 2 <= sms && F.shares * 2 <= blocks) F.shares *= 2;
-  if (F.shares > 1) return launch_fwd<D, true>(tq, tk, tv, F, F.items * F.shares, st);
-  F.sort = cross_sorts(A) && F.items > sms ? 1 : 0;
-  F.steal = F.items > 4 * sms || F.sort ? 1 : 0;
-  return launch_fwd<D, false>(tq, tk, tv, F, F.steal || F.items < sms ? F.items : sms, st);
+  if (F.shares == 1 && (D == 64 || A.max_kv <= kXPairKeys))
+    return launch_attention_cross_pair(q, k, v, F.out, F.lse, A, D, st);
+  CUtensorMap tq, tk, tv;
+  if (!cross_q_map(&tq, q, D, A, A.ld_q) || !cross_kv_map(&tk, k, D, A) ||
+      !cross_kv_map(&tv, v, D, A))
+    return MC_ERR_CUDA;
+  if constexpr (D == 128) {
+    if (F.shares == 1) {
+      F.sort = cross_sorts(A) && F.items > sms ? 1 : 0;
+      F.steal = F.items > 4 * sms || F.sort ? 1 : 0;
+      return launch_fwd<D, false>(tq, tk, tv, F, F.steal || F.items < sms ? F.items : sms, st);
+    }
+  }
+  return launch_fwd<D, true>(tq, tk, tv, F, F.items * F.shares, st);
 }
 
 }  // namespace

@@ -212,6 +212,17 @@ def test_many_items():
             q_lens=[130 - (i * 11) % 130 for i in range(40)]).check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("more", [0, 128, 300, 1000])
+@pytest.mark.parametrize("sq,heads,kv_heads", [(1, 8, 8), (3, 16, 8)])
+def test_ends_of_sequences(d, more, sq, heads, kv_heads):
+    """Last blocks of every kind, where items fill the SMs."""
+    ends = [1, 15, 16, 17, 32, 33, 64, 96, 97, 127, 128, 0]
+    lens = [n + more * (k % 3 != 1) for k, n in enumerate(ends)]
+    rows = 128 + more
+    Problem(len(ends), len(ends) * sq, len(ends) * rows, heads, kv_heads, d, kv_lens=lens).check()
+
+
 @pytest.mark.parametrize("n,sk,heads,kv_heads,d", [(1, 8191, 8, 1, 128), (2, 4097, 4, 4, 64),
                                                    (3, 2049, 6, 2, 128), (9, 600, 8, 8, 64)])
 def test_one_token_long_states(n, sk, heads, kv_heads, d):
