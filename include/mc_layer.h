@@ -718,16 +718,17 @@ int mc_layer_backward_norm(const mc_layer_shape* shape, const mc_layer_weights* 
  * query, and what K and V hold there (infinities and NaN too) has no
  * influence; padded queries, and all queries of a sequence without keys, get O
  * = 0 and a log-sum-exp of -infinity, and give no gradients.  Rows before the
- * first and behind the last sequence are neither read nor written.  Offsets
- * and lengths are cut to the rows that there are.
+ * first and behind the last sequence have no influence, whatever they hold, and
+ * are not written.  Offsets and lengths are cut to the rows that there are; all
+ * four arrays are read by the kernels, so that a captured call follows them.
  *
  * Query head h (columns [h head_dim, (h + 1) head_dim) of a row) reads key head
  * h / (heads / kv_heads); its rows are ld_q elements apart in Q, ld_o in O, and
  * those of K and V ld_kv.  K and V of a packed projection K | V: v = k +
  * kv_heads head_dim, ld_kv = 2 kv_heads head_dim.  max_q and max_kv bound the
  * rows of a sequence (0: not known) where offsets are given; a sequence with
- * more is reported as MC_ERR_DEVICE_BOUNDS and its rows beyond are not
- * computed. */
+ * more is reported as MC_ERR_DEVICE_BOUNDS, and then no result of the call is
+ * valid.  Outputs overlap neither one another nor an input. */
 typedef struct mc_cross_attention {
   int32_t sequences;
   int32_t heads, kv_heads; /* kv_heads divides heads, by at most 128 */

@@ -56,9 +56,9 @@ __device__ __forceinline__ CrossRows cross_keys(const CrossArgs& A, int n) {
 
 // Item k of the sequences by `heads` key heads by `blocks` blocks: the blocks of a
 // head one after another, so that CTAs that run together read the same K and V (or Q
-// and dO), which counts even where those stay in L2 either way: heads first, in
-// groups of at most 32 MB of them, 4 x 1037 queries of 64 heads to 256 keys took 81 us
-// against 74, 4096 to 8192 780 against 755.
+// and dO), which counts even where those stay in L2 either way: heads first, in groups
+// of at most 32 MB of them, with one CTA per SM, 4 x 1037 queries of 64 heads to 256
+// keys took 81 us against 74, 4096 to 8192 780 against 755.
 struct CrossItem {
   int n, hk, block;
 };

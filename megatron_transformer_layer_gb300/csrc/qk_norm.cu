@@ -137,6 +137,14 @@ __device__ __forceinline__ RotVec<T, VEC> pack(const P* f) {
 // by bulk copies into a ring of its own, so that the loads on their way do not
 // depend on registers; with narrower ones (odd sizes or addresses) the lanes
 // load them.
+//
+// Measured (bf16): 4096 tokens of 128 heads of 128, 49 us = 5.5 TB/s, 0.81 of a copy's
+// rate, at 210 instructions a turn of a warp; 8191 tokens of 40 such heads, centred, half
+// of a head turned in adjacent pairs, 53 us = 3.2 TB/s: a warp has some 35 turns there,
+// each a chain of two sums over the lanes, and little behind which to hide the last.
+// Two turns side by side in a warp were slower (57 us, more registers), smaller chunks
+// the same.  Backward 86 us = 4.7 TB/s for the first shape; 18 us for 2036 tokens of
+// 24 heads of 64, of which the sums of the gradients over blocks take 7.
 template <typename T, int VEC, bool ADJACENT, bool BACK, bool SHIFT>
 __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBlocks)
     qk_norm_kernel(const T* in, const T* dout, T* out, const int32_t* __restrict__ positions,

@@ -111,6 +111,8 @@ class TransformerLayer:
         """Other gains, shifts or eps (make_qk_norm) for a layer built with norms."""
         if self.qk_norm is None:
             raise ValueError("the layer was built without norms of Q and K: it keeps no room for them")
+        if norm is None:
+            raise ValueError("the layer was built with norms of Q and K: make_qk_norm() for plain ones")
         self._set_norm(norm)
 
     def set_stage(self, rotary=None, attention=None):

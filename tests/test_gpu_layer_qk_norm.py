@@ -171,6 +171,8 @@ def test_norms_that_do_not_cover_a_head():
     params = TransformerLayer.random_params(HID, H, F, seed=3)
     layer = TransformerLayer(B, S, HID, H, F, params=params, qk_norm=make_norm(True))
     x = torch.randn(T, HID, generator=gen(1)).to(DEV)
+    with pytest.raises(ValueError, match="with norms"):
+        layer.set_qk_norm(None)
     short = L.make_qk_norm(vec(1, 1.0), vec(2, 1.0, D - 1))
     layer.set_qk_norm(short)
     with pytest.raises(ValueError, match="norm of k: 64 elements"):
