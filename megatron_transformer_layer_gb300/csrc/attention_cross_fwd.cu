@@ -27,12 +27,14 @@
 // that, sums and statistics are 32-bit, and O is rounded once more when stored.
 //
 // Bound by the tensor cores and by what their products wait for: 4096 queries to 8192
-// keys, 64 heads of 128, 750-800 us = 1.37-1.47 PFLOP/s, 3,400-3,600 clocks a block of which the
-// products take 2,048 and the exponentials as many; loading S, the exchange of maxima
-// and the write of P stand between them.  Not kept there: a maximum that lags a block
-// behind (768 us), warps of their own for the store of O (784), K in three halves and
-// two tiles of Q (790), two CTAs per SM (840).  32 x 1 query to lengths up to 8192 (8 key
-// heads, 4.2 MB an item): 5.9 TB/s; equal lengths 6.8, a copy's rate.
+// keys, 64 heads of 128, 750-800 us = 1.37-1.47 PFLOP/s, 3,400-3,600 clocks a block of
+// which the products take 2,048; loading S, the exchange of maxima and the write of P
+// stand between the softmax of one block and the next.  Not kept there: a maximum that
+// lags a block behind (768 us), warps of their own for the store of O (784), K in three
+// halves and two tiles of Q (790), two CTAs per SM (840), a part of the exponentials as
+// polynomials on the multiply-add units (an eighth 768, three 849: those are busier than
+// the exponential unit).  32 x 1 query to lengths up to 8192 (8 key heads, 4.2 MB an item):
+// 5.9-6.1 TB/s; equal lengths 6.8, a copy's rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -13,11 +13,11 @@
 // its own where there are any (D = 64: [192, 256)), else over S, which it then holds
 // until its product is complete.
 //
-// What bounds it: the exponentials (16 a clock and SM) and, at D = 128, the products,
-// each about half of the time (4 x 1037 queries of 64 heads, D = 128: 128 keys 38 us,
-// 256 52 us, 512 81 us; S, softmax and product of one block are a chain of some 3000
-// clocks, of which two CTAs overlap two; D = 64: 4096 to 8192 keys 586 us, 3.7 of the
-// 4.6 exponentials a ns that the units give at 1.9 GHz).
+// What bounds it: S, softmax and product of a block are a chain of some 3,000 clocks at
+// D = 128, of which the two CTAs overlap two (4 x 1037 queries of 64 heads: 128 keys 38
+// us, 256 52 us, 512 81 us); the instructions of the softmax where S runs ahead (D =
+// 64: 4096 to 8192 keys 578 us; a part of the exponentials as polynomials, an eighth
+// 632).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -31,7 +31,8 @@ template <bool BACK>
 struct NormCfg {
   // (the backward pass takes 168 registers a thread: 12 warps per SM)
   static constexpr int kWarps = BACK ? 12 : 8, kBlocks = BACK ? 1 : 2;
-  static constexpr int kTurns = BACK ? 2 : 4;
+  // (4 turns, forward: 8191 tokens of 40 heads of 128 take 54 us against 50, one 58)
+  static constexpr int kTurns = 2;
   static constexpr int kInputs = BACK ? 2 : 1;
   static constexpr int kStages = 3;
   static constexpr int kStage = kTurns * kInputs * kNormTurnBytes;
@@ -40,6 +41,7 @@ struct NormCfg {
                                2 * kNormWords * 4 + kNormMaxDim / 2;
   static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "blocks per SM");
   static_assert(kStages * kStage >= 2 * kNormMaxDim * 4, "a warp's sums go through its ring");
+  static_assert(kWarps * kStages % 2 == 0, "the gains behind the barriers are read 16 bytes at a time");
 };
 
 // Queries (0) and keys (1) are walked apart, each by blocks of its own, so that
@@ -138,12 +140,12 @@ __device__ __forceinline__ RotVec<T, VEC> pack(const P* f) {
 // depend on registers; with narrower ones (odd sizes or addresses) the lanes
 // load them.
 //
-// Measured (bf16): 4096 tokens of 128 heads of 128, 49 us = 5.5 TB/s, 0.81 of a copy's
-// rate, at 210 instructions a turn of a warp; 8191 tokens of 40 such heads, centred, half
-// of a head turned in adjacent pairs, 53 us = 3.2 TB/s: a warp has some 35 turns there,
-// each a chain of two sums over the lanes, and little behind which to hide the last.
-// Two turns side by side in a warp were slower (57 us, more registers), smaller chunks
-// the same.  Backward 86 us = 4.7 TB/s for the first shape; 18 us for 2036 tokens of
+// Measured (bf16): 4096 tokens of 128 heads of 128, 46.7 us = 5.7 TB/s, 0.85 of a copy's
+// rate, at 240 instructions a turn of a warp; 8191 tokens of 40 such heads, centred, half
+// of a head turned in adjacent pairs, 50.4 us = 3.3 TB/s at 330: a warp has some 35 turns
+// there, each a chain of two sums over the lanes, four warps to a scheduler, which
+// issues 42% of the time.  Two turns side by side in a warp were slower (57 against 53 us:
+// more registers), more warps of fewer registers too (60).  Backward 86 us = 4.7 TB/s for the first shape; 18 us for 2036 tokens of
 // 24 heads of 64, of which the sums of the gradients over blocks take 7.
 template <typename T, int VEC, bool ADJACENT, bool BACK, bool SHIFT>
 __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBlocks)
