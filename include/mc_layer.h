@@ -748,7 +748,8 @@ int mc_attention_forward_cross(const uint16_t* q, const uint16_t* k, const uint1
 
 /* Bytes of the workspace of mc_attention_backward_cross: dz tiles of 32 KB per
  * pair of 128-row blocks, of as many key heads as stay below 2 GB, of one at
- * least.  0 for an invalid shape. */
+ * least.  0 for an invalid shape, and for more than 2^40 tiles a head, which a
+ * backward call refuses as MC_ERR_UNSUPPORTED (state max_q and max_kv). */
 size_t mc_attention_backward_cross_ws_bytes(const mc_cross_attention* cross);
 
 /* dq, dk, dv (bf16, rows as Q, K and V: ld_q, ld_kv) from dout (rows as O) and

@@ -97,7 +97,9 @@ int mc_attention_backward_cross(const uint16_t* q, const uint16_t* k, const uint
       !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
       !aligned(lse, 4) || !aligned(delta, 4) || !aligned(ws, 16))
     return MC_ERR_ALIGN;
-  if (ws_bytes < attention_cross_ws_bytes(*cross)) return MC_ERR_WORKSPACE;
+  const size_t need = attention_cross_ws_bytes(*cross);
+  if (need == 0) return MC_ERR_UNSUPPORTED;
+  if (ws_bytes < need) return MC_ERR_WORKSPACE;
   return launch_attention_cross_bwd(q, k, v, o, lse, dout, dq, dk, dv, delta, *cross,
                                     static_cast<uint8_t*>(ws), ws_bytes, status,
                                     static_cast<cudaStream_t>(stream));

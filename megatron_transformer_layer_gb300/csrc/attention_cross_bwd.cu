@@ -1027,6 +1027,7 @@ __global__ void __launch_bounds__(192, 1)
 // ---------------------------------------------------------------- launches
 // Key heads whose tiles are in the workspace at a time.
 constexpr int64_t kXTilesAtOnce = 2ll << 30;
+constexpr int64_t kXMostTiles = 1ll << 40;  // of a key head: what a workspace is for ends far below
 int64_t head_tiles(const CrossArgs& A) {
   return static_cast<int64_t>(A.n) * A.nqb * A.nkb * kXTileBytes;
 }
@@ -1098,6 +1099,8 @@ int launch_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const ui
 
 size_t attention_cross_ws_bytes(const mc_cross_attention& c) {
   const CrossArgs A = cross_args(c, nullptr);
+  // (sequences by blocks are below 2^30, key blocks below 2^22)
+  if (static_cast<int64_t>(A.n) * A.nqb * A.nkb > kXMostTiles) return 0;
   return static_cast<size_t>(heads_at_once(A) * head_tiles(A));
 }
 

@@ -119,6 +119,17 @@ def test_workspace(kw, tiles):
     assert L.mc_attention_backward_cross_ws_bytes(cross(**kw)) == tiles * 32768
 
 
+def test_workspace_beyond_all_memory():
+    """Sequences whose bounds are not known count as long as all rows are."""
+    rows = dict(sequences=256, q_rows=1 << 20, kv_rows=1 << 28, heads=128, kv_heads=1)
+    c = cross(q_offsets=P, kv_offsets=P, **rows)
+    assert L.mc_attention_backward_cross_ws_bytes(c) == 0
+    assert cross_calls(c)[1] == L.MC_ERR_UNSUPPORTED
+    c = cross(q_offsets=P, kv_offsets=P, max_q=1 << 12, max_kv=1 << 20, **rows)
+    assert L.mc_attention_backward_cross_ws_bytes(c) == 256 * 4096 * 8192 * 32768
+    assert cross_calls(c, ws_bytes=0)[1] == L.MC_ERR_WORKSPACE
+
+
 def test_norm_scratch():
     assert L.mc_qk_norm_scratch_floats(1, 2, 1, 64) == 3 * 2 * 64
     assert L.mc_qk_norm_scratch_floats(4096, 64, 64, 128) == 512 * 2 * 128

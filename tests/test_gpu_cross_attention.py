@@ -194,6 +194,13 @@ def test_a_sequence_longer_than_stated_is_reported():
     Problem(1, 40, 40, 2, 2, 64).check()  # the next call is as ever
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("wide", [8, 24])
+def test_rows_of_other_widths(d, wide):
+    """Strides that are multiples of 8 elements only."""
+    Problem(2, 300, 400, 3, 3, d, q_lens=[150, 3], kv_lens=[130, 200], wide=wide).check()
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.01, 2.0 ** -16])
 def test_scale(scale):
     Problem(1, 130, 300, 2, 2, 64, scale=scale, qstd=0.5).check()

@@ -118,6 +118,37 @@ def test_layer_with_norms(flags, centred, rotary, mask):
             assert m["finite"] and m["max_rel"] <= tol[0] and m["norm_rel"] <= mean, (n, m)
 
 
+@pytest.mark.parametrize("gains", [True, False])
+def test_heads_of_128(gains):
+    """Heads of 128: the layer against its parts, the norms and the attention by their
+    stage calls and the rest in float64."""
+    heads, d = 2, 128
+    a = heads * d
+    params = TransformerLayer.random_params(HID, heads, F, seed=3, std=0.05)
+    norm = L.make_qk_norm(*((vec(1, 1.0, d), vec(2, 1.0, d)) if gains else ()), eps=1e-3)
+    layer = TransformerLayer(B, S, HID, heads, F, params=params, qk_norm=norm)
+    x, dy = (torch.randn(T, HID, generator=gen(k)).to(DEV) for k in (1, 2))
+    y, dx = layer.forward(x), layer.backward(dy)
+    assert layer.device_status() == 0
+    o, st = torch.empty(T, a, dtype=torch.bfloat16, device=DEV), status()
+    lse = torch.empty(B * heads * S, device=DEV)
+    ln1 = torch.nn.functional.layer_norm(x.double(), (HID,), params["ln1_g"].double(),
+                                         params["ln1_b"].double(), 1e-5)
+    qkv = (ln1.bfloat16().double() @ params["w_qkv"].double().T + params["b_qkv"].double()).bfloat16()
+    assert L.mc_qk_norm_forward(qkv, qkv, T, heads, heads, d, 3 * a, 3 * a, norm, status=st) == 0
+    assert L.mc_attention_forward(qkv, o, lse, B, S, heads, d, st, torch.cuda.current_stream()) == 0
+    check_status(st)
+    x1 = x.double() + o.double() @ params["w_o"].double().T + params["b_o"].double()
+    ln2 = torch.nn.functional.layer_norm(x1, (HID,), params["ln2_g"].double(),
+                                         params["ln2_b"].double(), 1e-5)
+    u = ln2 @ params["w_fc1"].double().T + params["b_fc1"].double()
+    want = x1 + torch.nn.functional.gelu(u, approximate="tanh") @ params["w_fc2"].double().T + \
+        params["b_fc2"].double()
+    assert_close("y", to_f64(y), want.cpu().numpy(), *TOL)
+    assert [n for n in NAMES if n in layer.grads] == (["q_norm_g", "k_norm_g"] if gains else [])
+    assert bool(torch.isfinite(dx).all())
+
+
 def test_layer_without_norms_keeps_its_bits():
     params = TransformerLayer.random_params(HID, H, F, seed=3, std=0.05)
     layer = TransformerLayer(B, S, HID, H, F, 2, params=params)
