@@ -53,10 +53,10 @@ constexpr int kXKeys = 256;  // keys per block
 constexpr int kXRing = 4;    // items in shared memory
 // Up to so many keys two CTAs per SM take the items (attention_cross_pair.cu): at
 // D = 128, 4 x 1037 queries of 64 heads, 333 keys 67 us against 94 of this kernel, 900
-// keys 136 against 144, 960 139 against 141, 1024 140 against 136; one query of 8 heads
+// keys 135 against 144, 960 138 against 141, 1024 139 against 136; one query of 8 heads
 // to ragged lengths up to 8192 (32 of them) 120 against 96.  At D = 64 always, where P
-// has columns of its own there: 333 keys 56 against 86, 8192 keys 586 against 655, one
-// query to 300 (300 sequences, 12 heads) 67 against 144.
+// has columns of its own there: 333 keys 52 against 86, 8192 keys 552 against 655, one
+// query to 300 (300 sequences, 12 heads) 63 against 144.
 constexpr int kXPairKeys = 960;
 // O is rescaled only when a row's maximum grows by more than this (log2
 // units): P stays below 2^8 and the final division by the sum, taken against

@@ -14,10 +14,10 @@
 // until its product is complete.
 //
 // What bounds it: S, softmax and product of a block are a chain of some 3,000 clocks at
-// D = 128, of which the two CTAs overlap two (4 x 1037 queries of 64 heads: 128 keys 38
-// us, 256 52 us, 512 81 us); the instructions of the softmax where S runs ahead (D =
-// 64: 4096 to 8192 keys 578 us; a part of the exponentials as polynomials, an eighth
-// 632).
+// D = 128, of which the two CTAs overlap two (4 x 1037 queries of 64 heads: 128 keys 35
+// us, 256 51 us, 512 80 us; two threads to a row, which then exchange maxima: 19%
+// slower); the instructions of the softmax where S runs ahead (D = 64: 4096 to 8192 keys
+// 552 us; a part of the exponentials as polynomials, an eighth of them, 10% slower).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,12 +45,14 @@ struct alignas(16) PairItem {
 template <int D>
 struct PairCfg {
   static constexpr int kChunks = D / 64;
-  static constexpr int kTile = 128 * D * 2;         // 128 rows of Q, K or V
-  static constexpr int kNQ = D == 64 ? 2 : 1;       // tiles of Q,
-  static constexpr int kNK = D == 64 ? 2 : 1;       // of K and of V
-  static constexpr int kUsed = (kNQ + 2 * kNK) * kTile +
+  static constexpr int kTile = 128 * D * 2;    // Q [128][D] bf16
+  static constexpr int kNQ = D == 64 ? 2 : 1;  // tiles of Q
+  // Tiles of 128 rows of K and V come through one ring, in the order of their use.
+  // (Five of the half size at D = 128, replaced as they are used: 10% slower.)
+  static constexpr int kSlots = D == 64 ? 5 : 2;
+  // The dynamic shared memory starts 1024-byte aligned (checked at run time).
+  static constexpr int kSmem = (kNQ + kSlots) * kTile +
                                kPairRing * static_cast<int>(sizeof(PairItem)) + 32 * 8 + kCrossSorted;
-  static constexpr int kSmem = kUsed + 1024;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
   static constexpr uint32_t kTmemCols = 256;
   static constexpr bool kOwnP = D == 64;
@@ -71,33 +73,32 @@ __global__ void __launch_bounds__(kPairThreads, 2)
                       const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ PairArgs F) {
   using C = PairCfg<D>;
-  constexpr int NQ = C::kNQ, NK = C::kNK;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  constexpr int NQ = C::kNQ, NS = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const CrossArgs& A = F.c;
   int* status = A.status;
-  uint8_t* sQ = smem;                     // [NQ]
-  uint8_t* sK = smem + NQ * C::kTile;     // [NK]
-  uint8_t* sV = sK + NK * C::kTile;       // [NK]
-  PairItem* items = reinterpret_cast<PairItem*>(sV + NK * C::kTile);
+  if (smem_u32(smem) & 1023u) {  // the 128-byte swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) record_error(status, MC_ERR_DEVICE_BOUNDS, kSiteCross);
+    return;
+  }
+  uint8_t* sQ = smem;                  // [NQ]
+  uint8_t* sR = smem + NQ * C::kTile;  // K and V
+  PairItem* items = reinterpret_cast<PairItem*>(sR + NS * C::kTile);
   uint64_t* bars = reinterpret_cast<uint64_t*>(items + kPairRing);
   uint64_t* q_full = bars + 0;     // [NQ]
   uint64_t* q_empty = bars + 2;    // [NQ] the item's last S
-  uint64_t* k_full = bars + 4;     // [NK]
-  uint64_t* k_empty = bars + 6;    // [NK] after S
-  uint64_t* v_full = bars + 8;     // [NK]
-  uint64_t* v_empty = bars + 10;   // [NK] after O += P V
-  uint64_t* s_full = bars + 12;    // S in TMEM
-  uint64_t* s_free = bars + 13;    // and in registers (4 warps)
-  uint64_t* p_full = bars + 14;    // P in TMEM (4 warps)
-  uint64_t* pv_done = bars + 15;   // O += P V complete
-  uint64_t* drain = bars + 16;
-  uint64_t* steal_bar = bars + 17;
-  uint64_t* it_full = bars + 18;   // [kPairRing]
-  uint64_t* it_empty = bars + 22;  // [kPairRing] read by the MMA thread and the softmax (5)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
-  void* response = bars + 28;  // 16 bytes, aligned as the items are
+  uint64_t* full = bars + 4;       // [NS]
+  uint64_t* empty = bars + 9;      // [NS] after S (K), after O += P V (V)
+  uint64_t* s_full = bars + 14;    // S in TMEM
+  uint64_t* s_free = bars + 15;    // and in registers (4 warps)
+  uint64_t* p_full = bars + 16;    // P in TMEM (4 warps)
+  uint64_t* pv_done = bars + 17;   // O += P V complete
+  uint64_t* drain = bars + 18;
+  uint64_t* steal_bar = bars + 19;
+  uint64_t* it_full = bars + 20;   // [kPairRing]
+  uint64_t* it_empty = bars + 24;  // [kPairRing] read by the MMA thread and the softmax (5)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
+  void* response = bars + 30;  // 16 bytes, aligned as the items are
   int8_t* order = reinterpret_cast<int8_t*>(bars + 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -106,11 +107,9 @@ __global__ void __launch_bounds__(kPairThreads, 2)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
-    for (int i = 0; i < NK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(s_free, 4);
@@ -153,8 +152,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
     if (warp == 0) {
       if (lane == 0) {
         // -------------------------------------------------------- producer
-        int g = 0, q_n = 0;  // blocks (K, V) and Q tiles issued
-        int v_n = 0;
+        int u = 0, q_n = 0;  // tiles of K and V, and of Q issued
         bool ok = true;
         const uint32_t q_bytes = static_cast<uint32_t>(A.G * A.pq * 128 * C::kChunks);
         OptItems steal(response, steal_bar, F.items, F.steal);
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         ok = announce(0, cur);
         for (int r = 0; ok && cur.blocks >= 0; ++r, cur = next) {
           if (cur.blocks == 0 && !(ok = go_on(r))) break;
-          for (int j = 0; j < cur.blocks; ++j, ++g) {
+          for (int j = 0; j < cur.blocks; ++j) {
             if (j == 0) {
               const int qb = q_n % NQ;
               if (!(ok = mbar_wait(&q_empty[qb], ((q_n / NQ) & 1) ^ 1u, status, kSiteCross))) break;
@@ -203,26 +201,15 @@ __global__ void __launch_bounds__(kPairThreads, 2)
                              cur.q0);
               ++q_n;
             }
-            const int st = g % NK;
-            const uint32_t phase = ((g / NK) & 1) ^ 1u;
-            if (!(ok = mbar_wait(&k_empty[st], phase, status, kSiteCross))) break;
-            mbar_arrive_expect_tx(&k_full[st], C::kTile);
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_load_2d(sK + st * C::kTile + c * 16384, &tm_k, &k_full[st], cur.hk * D + c * 64,
-                          cur.k0 + j * 128);
-            if (!(ok = mbar_wait(&v_empty[st], phase, status, kSiteCross))) {
-              ++g;
-              break;
+            for (int n = 0; n < 2; ++n, ++u) {  // K, then V
+              const int st = u % NS;
+              if (!(ok = mbar_wait(&empty[st], ((u / NS) & 1) ^ 1u, status, kSiteCross))) break;
+              mbar_arrive_expect_tx(&full[st], C::kTile);
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_2d(sR + st * C::kTile + c * 16384, n == 0 ? &tm_k : &tm_v, &full[st],
+                            cur.hk * D + c * 64, cur.k0 + j * 128);
             }
-            mbar_arrive_expect_tx(&v_full[st], C::kTile);
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_load_2d(sV + st * C::kTile + c * 16384, &tm_v, &v_full[st], cur.hk * D + c * 64,
-                          cur.k0 + j * 128);
-            ++v_n;
-            if (j == 0 && !(ok = go_on(r))) {
-              ++g;
-              break;
-            }
+            if (!ok || (j == 0 && !(ok = go_on(r)))) break;
           }
         }
         steal.finish(status);
@@ -230,10 +217,8 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         // Copies still in flight must land before the CTA exits.
         for (int i = q_n - 1; i >= 0 && i >= q_n - NQ; --i)
           mbar_wait(&q_full[i % NQ], (i / NQ) & 1, status, kSiteCross, 200000000ull, false);
-        for (int i = g - 1; i >= 0 && i >= g - NK; --i)
-          mbar_wait(&k_full[i % NK], (i / NK) & 1, status, kSiteCross, 200000000ull, false);
-        for (int i = v_n - 1; i >= 0 && i >= v_n - NK; --i)
-          mbar_wait(&v_full[i % NK], (i / NK) & 1, status, kSiteCross, 200000000ull, false);
+        for (int i = u - 1; i >= 0 && i >= u - NS; --i)
+          mbar_wait(&full[i % NS], (i / NS) & 1, status, kSiteCross, 200000000ull, false);
       }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
@@ -241,33 +226,33 @@ __global__ void __launch_bounds__(kPairThreads, 2)
       const bool leader = elect_one();
       // K-major Q and K (1024 B per 8 rows), MN-major V (64-wide d chunks 16 KB apart)
       const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), 16384, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_u32(sR), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_u32(sR), 16384, 1024);
       int g = 0, n_items = 0;  // blocks whose S is issued, items with blocks
-      int p_tail = 0;          // keys of the block whose O += P V is still to be issued
+      int p_keys = 0;          // of the block whose O += P V is still to be issued
       bool p_first = false;    // as the first one of its item
       bool ok = true;
       auto issue_pv = [&](int gp) -> bool {
-        const int st = gp % NK;
-        if (!mbar_wait_warp(&v_full[st], (gp / NK) & 1, status, kSiteCross)) return false;
+        const int u = 2 * gp + 1, st = u % NS;
+        if (!mbar_wait_warp(&full[st], (u / NS) & 1, status, kSiteCross)) return false;
         // steps of 16 keys; P is 0 for those behind the sequence, V may be anything there
-        const int steps = (p_tail + 15) >> 4;
-        if (p_tail < steps * 16)
-          cross_clear_tail<D>(sV + st * C::kTile, p_tail, lane, steps * 16);
-        const uint64_t vd = smem_desc_add(v_desc, st * C::kTile);
+        const int steps = (p_keys + 15) >> 4;
+        if (p_keys < steps * 16)
+          cross_clear_tail<D>(sR + st * C::kTile, p_keys, lane, steps * 16);
         if (!mbar_wait_warp(p_full, gp & 1, status, kSiteCross)) return false;
         tc_fence_after();
+        const uint64_t vd = smem_desc_add(v_desc, st * C::kTile);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             if (kk < steps)
               umma_bf16_ts(tO, tP + kk * 8, smem_desc_add(vd, kk * 2048), kIdescPV,
                            kk > 0 || !p_first ? 1u : 0u);
-          umma_commit(&v_empty[st]);
+          umma_commit(&empty[st]);
           umma_commit(pv_done);
         }
         __syncwarp();
-        p_tail = 0;
+        p_keys = 0;
         return true;
       };
       for (int r = 0; ok; ++r) {
@@ -280,11 +265,12 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         if (blocks < 0) break;
         const int qb = n_items % NQ;
         for (int j = 0; j < blocks; ++j, ++g) {
-          const int st = g % NK;
+          const int left = min(keys - j * 128, 128);
+          const int u = 2 * g, st = u % NS;
           if (j == 0 &&
               !(ok = mbar_wait_warp(&q_full[qb], (n_items / NQ) & 1, status, kSiteCross)))
             break;
-          if (!(ok = mbar_wait_warp(&k_full[st], (g / NK) & 1, status, kSiteCross))) break;
+          if (!(ok = mbar_wait_warp(&full[st], (u / NS) & 1, status, kSiteCross))) break;
           // S is in registers; where P lies over it, the products have read P
           if (g > 0 && !(ok = C::kOwnP
                                   ? mbar_wait_warp(s_free, (g - 1) & 1, status, kSiteCross)
@@ -292,26 +278,24 @@ __global__ void __launch_bounds__(kPairThreads, 2)
             break;
           tc_fence_after();
           // (as many columns as there are keys, in 16s)
-          const uint32_t idesc =
-              idesc_bf16_f32(128, (min(keys - j * 128, 128) + 15) & ~15, false, false);
+          const uint32_t idesc = idesc_bf16_f32(128, (left + 15) & ~15, false, false);
           const uint64_t qd = smem_desc_add(q_desc, qb * C::kTile);
           const uint64_t kd = smem_desc_add(k_desc, st * C::kTile);
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-              umma_bf16(tS, smem_desc_add(qd, off), smem_desc_add(kd, off), idesc,
-                        kk > 0 ? 1u : 0u);
+              umma_bf16(tS, smem_desc_add(qd, off), smem_desc_add(kd, off), idesc, kk > 0 ? 1u : 0u);
             }
             umma_commit(s_full);
-            umma_commit(&k_empty[st]);
+            umma_commit(&empty[st]);
             if (j == blocks - 1) umma_commit(&q_empty[qb]);
           }
           __syncwarp();
           if constexpr (C::kOwnP) {
-            if (p_tail > 0 && !(ok = issue_pv(g - 1))) break;
+            if (p_keys > 0 && !(ok = issue_pv(g - 1))) break;
           }
-          p_tail = min(keys - j * 128, 128);
+          p_keys = left;
           p_first = j == 0;
           if (!C::kOwnP || j == blocks - 1) {
             if (!(ok = issue_pv(g))) break;
@@ -364,7 +348,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         const int end = it.keys - j * 128;
         // Where S is held until the product, a last block does no more than it has
         // keys for (333 keys, D = 128: 67 us against 71; at D = 64, where S is free
-        // at once, the branch costs more than it saves: 8192 keys 616 us against 578).
+        // at once, the branch costs more than it saves: 8192 keys 6% more).
         float mx = -INFINITY;
         if (C::kOwnP || end >= 128) {
           if (C::kOwnP && end < 128) {
@@ -485,7 +469,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
                          (lane & 3) * 8
                    : nullptr;
       }
-#pragma unroll
+#pragma unroll 1  // (unrolled, 128 keys take 2 us more: instructions missed)
       for (int c = 0; c < D / 32; ++c) {
         float v[32] = {};
         if (it.blocks > 0) tmem_ld_32x32b_x32(tO + lane_off + c * 32, v);
