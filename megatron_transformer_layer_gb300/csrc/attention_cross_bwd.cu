@@ -5,7 +5,8 @@
 // dK and dV summed over the query heads that share a key head: those are rows
 // of the same blocks (attention_cross.cuh), so the products sum them.
 //
-//   delta: one pass over O and dO.
+//   delta: one pass over O and dO; where no sequence has more than 128 keys the dkdv
+//          kernel forms it instead.
 //   dkdv:  a block of 128 keys against its sequence's blocks of queries,
 //          accumulates dV and dK and writes each block pair's dz^T tile as bf16.
 //   dq:    a block of queries: the product of its tiles with K (bound by the
@@ -23,7 +24,7 @@
 // tcgen05 product has the type of the other one, dO's, Q's and K's.  dK and dQ
 // take the same rounded dz.  dz itself is formed in 32 bits from the unrounded P;
 // sums and accumulators are 32-bit and dQ, dK and dV are rounded once more when
-// stored.  delta is formed from the stored bf16 O.
+// stored.  delta is formed from the stored bf16 O, or (WHOLE) from P and dP.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -125,7 +126,8 @@ struct XKvCfg {
   // aligned (checked at run time).
   static constexpr int kQ = D == 64 ? 3 : 2, kdO = 2;
   static constexpr int kUsed = (2 + kQ + kdO) * kTile + static_cast<int>(kXTileBytes) +
-                               4 * 128 * 4 + kXKvRing * static_cast<int>(sizeof(XKvItem)) + 36 * 8 + kCrossSorted;
+                               4 * 128 * 4 + kXKvRing * static_cast<int>(sizeof(XKvItem)) + 40 * 8 +
+                               kCrossSorted;
   // one CTA per SM: it takes all 512 TMEM columns
   static constexpr int kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;
   static constexpr uint32_t kTmemCols = 512;
@@ -155,7 +157,7 @@ struct XKvCfg {
 // dV and dK from all shares, read in their order from the others' shared memory
 // (SPLIT; 2048 queries to 4096 keys, 16 heads on 2 key heads, both passes 141 us
 // against 262).
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool WHOLE>
 __global__ void __launch_bounds__(kXKvThreads, 1)
     cross_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -201,10 +203,12 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
   void* response = bars + 32;     // 16 bytes, aligned as the items are
   uint64_t* ds_full = bars + 34;  // the dz^T tile of block i is in sDs (16 warps)
   uint64_t* ds_free = bars + 35;  // its bulk store has read sDs
-  int8_t* order = reinterpret_cast<int8_t*>(bars + 36);
+  uint64_t* meet_bar = bars + 36;  // [4] per group: sums over the keys (4 warps)
+  int8_t* order = reinterpret_cast<int8_t*>(bars + 40);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(&meet_bar[i], 4);
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
     mbar_init(v_full, 1);
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         const int64_t at =
             (static_cast<int64_t>(hk) * A.G + my_head) * A.q_rows + q0 + qi;
         q_lse = B.lse[at];
-        q_delta = B.delta[at];
+        if constexpr (!WHOLE) q_delta = B.delta[at];
       }
     };
     bool have = false;  // loaded and not yet staged
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       have = false;
       if (grp != 0) return;
       sL[st * 128 + t] = q_in ? q_lse * kOptLog2e : INFINITY;
-      sD[st * 128 + t] = q_in ? q_delta : 0.f;
+      if constexpr (!WHOLE) sD[st * 128 + t] = q_in ? q_delta : 0.f;
       mbar_arrive_warp(&lse_ready[st], lane);
     };
     // waits for item r's announcement and loads its first block's queries
@@ -562,6 +566,44 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       const XKvItem& it = items[slot];
       have = it.count > 0;
       if (have && grp == 0) load_query(it.q0, it.queries, it.hk, it.first);
+    };
+    // WHOLE: every block holds all keys of its sequence, and delta is summed from the
+    // block itself, sum_j P dP in 32 bits.  (Formed from the stored bf16 O it is off by
+    // up to 2^-8 of O dO, which where few keys share the weight is as much as all of dP -
+    // delta: with one key it would leave dQ, which is 0, with nothing but that.)  Sums
+    // over a warp's 32 keys leave column `lane` to lane `lane`; then over the four warps
+    // of the group in a fixed order, through sD, which is free: the products of a block,
+    // and with them all of its readers, are behind the next block's dP^T.  4 x 1037
+    // queries to 128 keys, 64 heads of 128: 96 us against 112 with the pass over O and
+    // dO; 4096 queries of 16 heads to 100 keys of 2: 114 against 90.
+    [[maybe_unused]] int met = 0;
+    auto meet = [&]() -> bool {
+      mbar_arrive_warp(&meet_bar[grp], lane);
+      return mbar_wait_warp(&meet_bar[grp], met++ & 1, status, kSiteCross);
+    };
+    [[maybe_unused]] auto sum_delta = [&](const float (&p)[32], const float (&dp)[32]) -> bool {
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float a = p[e] * dp[e], b = p[e + 16] * dp[e + 16];
+        v[e] = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < o; ++e)
+          v[e] = (lane & o ? v[e + o] : v[e]) +
+                 __shfl_xor_sync(0xffffffffu, lane & o ? v[e] : v[e + o], o);
+      float *s0 = sD + grp * 32 + lane, *s1 = s0 + 128;
+      float col = v[0];
+      if (quarter == 1) *s0 = col;
+      if (quarter == 3) *s1 = col;
+      if (!meet()) return false;
+      if (quarter == 0) col += *s0;
+      if (quarter == 2) *s1 = col + *s1;
+      if (!meet()) return false;
+      if (quarter == 0) *s0 = col + *s1;
+      return meet();
     };
     // dV and dK of the item before, in TMEM until its last products are done,
     // or (keys that no query sees) zeros.
@@ -599,7 +641,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       const bool edge = it.real < 128, mine = t < it.real;
       for (int i = 0; i < count; ++i, ++g) {
         const float* l2 = sL + (g & 1) * 128 + grp * 32;
-        const float* dl = sD + (g & 1) * 128 + grp * 32;
+        const float* dl = sD + (WHOLE ? 0 : (g & 1) * 128) + grp * 32;
         if (!mbar_wait_warp(&lse_ready[g & 1], (g >> 1) & 1, status, kSiteCross) ||
             !mbar_wait_warp(s_full, g & 1, status, kSiteCross)) {
           ok = false;
@@ -655,6 +697,9 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           if (edge) {  // (V behind the sequence may be anything)
 #pragma unroll
             for (int e = 0; e < 32; ++e) dv[e] = mine ? dv[e] : 0.f;
+          }
+          if constexpr (WHOLE) {
+            if (!(ok = sum_delta(p, dv))) break;
           }
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
@@ -1054,19 +1099,22 @@ int launch_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const ui
   if (!cross_q_map(&tq, q, D, A, A.ld_q) || !cross_kv_map(&tk, k, D, A) ||
       !cross_kv_map(&tv, v, D, A) || !cross_q_map(&td, dout, D, A, A.ld_o))
     return MC_ERR_CUDA;
-  static PerDeviceInit init_kv, init_split, init_q;
-  auto kv = cross_dkdv_kernel<D, false>;
-  auto kv_split = cross_dkdv_kernel<D, true>;
+  static PerDeviceInit init_kv[2], init_split[2], init_q;
+  const int whole = A.nkb == 1 ? 1 : 0;
+  auto kv = whole ? cross_dkdv_kernel<D, false, true> : cross_dkdv_kernel<D, false, false>;
+  auto kv_split = whole ? cross_dkdv_kernel<D, true, true> : cross_dkdv_kernel<D, true, false>;
   auto dq = cross_dq_kernel<D>;
-  if (cross_smem(init_kv, kv, XKvCfg<D>::kSmem) != cudaSuccess ||
-      cross_smem(init_split, kv_split, XKvCfg<D>::kSmem) != cudaSuccess ||
+  if (cross_smem(init_kv[whole], kv, XKvCfg<D>::kSmem) != cudaSuccess ||
+      cross_smem(init_split[whole], kv_split, XKvCfg<D>::kSmem) != cudaSuccess ||
       cross_smem(init_q, dq, XDqCfg<D>::kSmem) != cudaSuccess)
     return MC_ERR_CUDA;
-  const int64_t per_block = kXDeltaThreads / (D / 8) * kXDeltaPasses;
-  const int64_t blocks = (static_cast<int64_t>(A.q_rows) * A.H + per_block - 1) / per_block;
-  launch_kernel(cross_delta_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kXDeltaThreads), 0,
-                st, 1, o, dout, delta, A.q_rows, A.H, A.ld_o);
-  if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
+  if (!whole) {
+    const int64_t per_block = kXDeltaThreads / (D / 8) * kXDeltaPasses;
+    const int64_t blocks = (static_cast<int64_t>(A.q_rows) * A.H + per_block - 1) / per_block;
+    launch_kernel(cross_delta_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kXDeltaThreads),
+                  0, st, 1, o, dout, delta, A.q_rows, A.H, A.ld_o);
+    if (cudaGetLastError() != cudaSuccess) return MC_ERR_CUDA;
+  }
   const int at_once = heads_at_once(A), sms = num_sms();
   B.sort = cross_sorts(A) ? 1 : 0;
   // (items of unequal sequences are taken over by the CTAs that are done, whatever

@@ -195,6 +195,29 @@ def test_a_sequence_longer_than_stated_is_reported():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sq,sk,heads,kv_heads", [(300, 1, 2, 2), (1, 1, 12, 12), (300, 2, 4, 2),
+                                                  (40, 3, 8, 8), (1500, 9, 2, 1), (130, 128, 3, 3)])
+def test_gradients_with_few_keys(d, sq, sk, heads, kv_heads):
+    """Where a sequence has few keys dP - delta cancels: what is left has to be as
+    exact as elsewhere, roundings to bf16 of dz and of dQ (each at most 2^-8 of the
+    value, so that together they stay below 2^-7 of the 2-norm), beside 2^-16 of the
+    terms' size (delta, P and lse in 32 bits).  With one key dQ is 0."""
+    n = 3
+    p = Problem(n, n * sq, n * sk, heads, kv_heads, d, q_lens=[sq, max(1, sq - 7), sq],
+                kv_lens=[sk, max(1, sk - 1), sk]).check_forward()
+    dq = to_f64(p.check_backward().dq_all)[:, : p.a]
+    ref, _, _ = O.backward(*map(p.clean, (p.q, p.k, p.v, p.dout)), p.q_seq, p.k_seq, heads, kv_heads,
+                           d, p.scale)
+    size = p.scale * np.linalg.norm(p.clean(p.k), axis=1).max() * \
+        np.linalg.norm(p.clean(p.v), axis=1).max() * np.abs(p.clean(p.dout)).max() * np.sqrt(d)
+    err = np.linalg.norm((dq - ref[0])[[i for f, _, r in p.q_seq for i in range(f, f + r)]])
+    rows = np.sqrt(sum(r for _, _, r in p.q_seq) * heads)
+    assert err <= 2.0 ** -7 * np.linalg.norm(ref[0]) + 2.0 ** -16 * size * rows
+    if sk == 1:
+        assert np.abs(dq[dq != 3.0]).max() <= 2.0 ** -16 * size
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("wide", [8, 24])
 def test_rows_of_other_widths(d, wide):
     """Strides that are multiples of 8 elements only."""
