@@ -639,6 +639,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       if (count < 0) break;
       const int q0 = it.q0, queries = it.queries, hk = it.hk, first = it.first;
       const bool edge = it.real < 128, mine = t < it.real;
+      const bool only = it.real == 1 && it.kb == 0;
       for (int i = 0; i < count; ++i, ++g) {
         const float* l2 = sL + (g & 1) * 128 + grp * 32;
         const float* dl = sD + (WHOLE ? 0 : (g & 1) * 128) + grp * 32;
@@ -674,6 +675,10 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         if (edge) {  // (keys behind the sequence)
 #pragma unroll
           for (int e = 0; e < 32; ++e) p[e] = mine ? p[e] : 0.f;
+          if (only) {  // the weight of a sequence's only key is 1, and dz = dP - dP
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[e] = rintf(p[e]);
+          }
         }
         if (pending) {
           if (!mbar_wait_warp(acc_done, (g - 1) & 1, status, kSiteCross)) {
@@ -697,6 +702,10 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           if (edge) {  // (V behind the sequence may be anything)
 #pragma unroll
             for (int e = 0; e < 32; ++e) dv[e] = mine ? dv[e] : 0.f;
+            if (!WHOLE && only) {  // (P = 0 leaves the others at 0)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) dv[e] = dl[e];
+            }
           }
           if constexpr (WHOLE) {
             if (!(ok = sum_delta(p, dv))) break;

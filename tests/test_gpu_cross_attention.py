@@ -214,7 +214,17 @@ def test_gradients_with_few_keys(d, sq, sk, heads, kv_heads):
     rows = np.sqrt(sum(r for _, _, r in p.q_seq) * heads)
     assert err <= 2.0 ** -7 * np.linalg.norm(ref[0]) + 2.0 ** -16 * size * rows
     if sk == 1:
-        assert np.abs(dq[dq != 3.0]).max() <= 2.0 ** -16 * size
+        assert (dq == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_key_beside_many(d):
+    """A sequence's only key has the weight 1: no gradient of its queries, in a call
+    whose other sequences have many keys too."""
+    p = Problem(3, 3 * 140, 3 * 300, 4, 2, d, kv_lens=[300, 1, 129]).check()
+    dq = to_f64(p.dq_all)[140:280, : p.a]
+    assert (dq == 0).all()
+    assert (to_f64(p.dkv_all)[300, : p.akv] == 0).all()
 
 
 @pytest.mark.parametrize("d", [64, 128])
