@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
     // over a warp's 32 keys leave column `lane` to lane `lane`; then over the four warps
     // of the group in a fixed order, through sD, which is free: the products of a block,
     // and with them all of its readers, are behind the next block's dP^T.  4 x 1037
-    // queries to 128 keys, 64 heads of 128: 96 us against 112 with the pass over O and
-    // dO; 4096 queries of 16 heads to 100 keys of 2: 114 against 90.
+    // queries to 128 keys, 64 heads of 128: 94 us against 112 with the pass over O and
+    // dO; 4096 queries of 16 heads to 100 keys of 2: 108 against 90.
     [[maybe_unused]] int met = 0;
     auto meet = [&]() -> bool {
       mbar_arrive_warp(&meet_bar[grp], lane);
@@ -595,15 +595,13 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           v[e] = (lane & o ? v[e + o] : v[e]) +
                  __shfl_xor_sync(0xffffffffu, lane & o ? v[e] : v[e + o], o);
       float *s0 = sD + grp * 32 + lane, *s1 = s0 + 128;
-      float col = v[0];
+      const float col = v[0];
       if (quarter == 1) *s0 = col;
       if (quarter == 3) *s1 = col;
       if (!meet()) return false;
-      if (quarter == 0) col += *s0;
+      if (quarter == 0) *s0 = col + *s0;
       if (quarter == 2) *s1 = col + *s1;
-      if (!meet()) return false;
-      if (quarter == 0) *s0 = col + *s1;
-      return meet();
+      return meet();  // (who reads adds the two)
     };
     // dV and dK of the item before, in TMEM until its last products are done,
     // or (keys that no query sees) zeros.
@@ -716,7 +714,11 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               const int at = gr * 16 + e;
-              const float4 dlv = *reinterpret_cast<const float4*>(dl + at);
+              float4 dlv = *reinterpret_cast<const float4*>(dl + at);
+              if constexpr (WHOLE) {
+                const float4 more = *reinterpret_cast<const float4*>(dl + 128 + at);
+                dlv.x += more.x, dlv.y += more.y, dlv.z += more.z, dlv.w += more.w;
+              }
               const float* dq = dv + gr * 16 + e;
               const float2 d0 = __fmul2_rn(make_float2(p[at], p[at + 1]),
                                            __fadd2_rn(make_float2(dq[0], dq[1]),
