@@ -754,9 +754,10 @@ size_t mc_attention_backward_cross_ws_bytes(const mc_cross_attention* cross);
 
 /* dq, dk, dv (bf16, rows as Q, K and V: ld_q, ld_kv) from dout (rows as O) and
  * the forward's o and lse.  dk and dv are summed over the query heads that
- * share a key head; padded rows get zeros.  `delta` is fp32 scratch [heads,
- * q_rows]; `ws` device memory of ws_bytes (16-byte aligned, less than
- * mc_attention_backward_cross_ws_bytes -> MC_ERR_WORKSPACE). */
+ * share a key head; padded rows get zeros.  How exact a sequence's gradients are
+ * depends on its own lengths, not on bounds, slots or the other sequences.  `delta`
+ * is fp32 scratch [heads, q_rows]; `ws` device memory of ws_bytes (16-byte aligned,
+ * less than mc_attention_backward_cross_ws_bytes -> MC_ERR_WORKSPACE). */
 int mc_attention_backward_cross(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                 const uint16_t* o, const float* lse, const uint16_t* dout,
                                 uint16_t* dq, uint16_t* dk, uint16_t* dv, float* delta,

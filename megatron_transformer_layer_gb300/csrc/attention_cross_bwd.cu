@@ -5,8 +5,8 @@
 // dK and dV summed over the query heads that share a key head: those are rows
 // of the same blocks (attention_cross.cuh), so the products sum them.
 //
-//   delta: one pass over O and dO; where no sequence has more than 128 keys the dkdv
-//          kernel forms it instead.
+//   delta: one pass over O and dO; the dkdv kernel forms that of sequences of up to 128
+//          keys itself (and there is no pass where the bound on the keys is 128 or less).
 //   dkdv:  a block of 128 keys against its sequence's blocks of queries,
 //          accumulates dV and dK and writes each block pair's dz^T tile as bf16.
 //   dq:    a block of queries: the product of its tiles with K (bound by the
@@ -24,7 +24,8 @@
 // tcgen05 product has the type of the other one, dO's, Q's and K's.  dK and dQ
 // take the same rounded dz.  dz itself is formed in 32 bits from the unrounded P;
 // sums and accumulators are 32-bit and dQ, dK and dV are rounded once more when
-// stored.  delta is formed from the stored bf16 O, or (WHOLE) from P and dP.
+// stored.  delta of a sequence of more than 128 keys is formed from the stored bf16 O, of
+// a shorter one from P and dP: its own length decides, not the call's bound or the others.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -108,7 +109,8 @@ struct alignas(16) XKvItem {
   int q0, queries;     // the sequence's first query row, and its real queries
   int n, hk, kb;
   int first;           // its first block of queries
-  int pad[2];
+  int whole;           // it holds all keys of its sequence
+  int pad;
 };
 constexpr int kXKvRing = 4;
 constexpr int kXKvThreads = 640;
@@ -271,6 +273,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
     it.k0 = kv.first + it.kb * 128;
     it.real = min(max(kv.real - it.kb * 128, 0), 128);
     it.slot = min(max(kv.slot - it.kb * 128, 0), 128);
+    it.whole = kv.real <= 128 ? 1 : 0;
     it.q0 = q.first;
     it.queries = q.real;
     it.count = it.real > 0 ? (q.real + A.pq - 1) / A.pq : 0;
@@ -553,6 +556,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       have = false;
       if (grp != 0) return;
       sL[st * 128 + t] = q_in ? q_lse * kOptLog2e : INFINITY;
+      // (what a whole item forms itself takes its place)
       if constexpr (!WHOLE) sD[st * 128 + t] = q_in ? q_delta : 0.f;
       mbar_arrive_warp(&lse_ready[st], lane);
     };
@@ -567,41 +571,45 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       have = it.count > 0;
       if (have && grp == 0) load_query(it.q0, it.queries, it.hk, it.first);
     };
-    // WHOLE: every block holds all keys of its sequence, and delta is summed from the
-    // block itself, sum_j P dP in 32 bits.  (Formed from the stored bf16 O it is off by
-    // up to 2^-8 of O dO, which where few keys share the weight is as much as all of dP -
+    // A block that holds all keys of its sequence (`whole`; WHOLE: the call has no other)
+    // forms delta itself, sum_j P dP in 32 bits.  (From the stored bf16 O it is off by up
+    // to 2^-8 of O dO, which where few keys share the weight is as much as all of dP -
     // delta: with one key it would leave dQ, which is 0, with nothing but that.)  Sums
     // over a warp's 32 keys leave column `lane` to lane `lane`; then over the four warps
-    // of the group in a fixed order, through sD, which is free: the products of a block,
-    // and with them all of its readers, are behind the next block's dP^T.  4 x 1037
-    // queries to 128 keys, 64 heads of 128: 94 us against 112 with the pass over O and
-    // dO; 4096 queries of 16 heads to 100 keys of 2: 108 against 90.
-    [[maybe_unused]] int met = 0;
-    auto meet = [&]() -> bool {
+    // of the group in a fixed order, through the places of sDs that this group's dz goes
+    // to (rows 0..7: a warp's 32 columns in two of them), once the store of the block
+    // before has read them, into sD.  dP^T is loaded again behind it: kept in registers,
+    // it costs the other items 1% more.  4 x 1037 queries to 128 keys, 64 heads of 128: 95
+    // us against 112 with the pass over O and dO; 4096 queries of 16 heads to 100 keys of
+    // 2: 107 against 90; one of four sequences of 1037 with 300 keys, the others with 40
+    // to 128: 182 against 163 with delta from O for all.
+    auto meet = [&](uint32_t phase) -> bool {  // (twice a block)
       mbar_arrive_warp(&meet_bar[grp], lane);
-      return mbar_wait_warp(&meet_bar[grp], met++ & 1, status, kSiteCross);
+      return mbar_wait_warp(&meet_bar[grp], phase, status, kSiteCross);
     };
-    [[maybe_unused]] auto sum_delta = [&](const float (&p)[32], const float (&dp)[32]) -> bool {
-      float v[16];
+    auto part = [&](int q) -> float* {
+      const int r = 2 * q + (lane >> 4), side = ((r >> 2) ^ grp) & 1;
+      return reinterpret_cast<float*>(sDs + (grp >> 1) * 16384 + r * 128 + side * 64) + (lane & 15);
+    };
+    auto sum_delta = [&](const float (&p)[32], bool mine, int g) -> bool {
+      float dp[32];
+      tmem_ld_32x32b_x32(tdP + my_cols, dp);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float a = p[e] * dp[e], b = p[e + 16] * dp[e + 16];
-        v[e] = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-        for (int e = 0; e < o; ++e)
-          v[e] = (lane & o ? v[e + o] : v[e]) +
-                 __shfl_xor_sync(0xffffffffu, lane & o ? v[e] : v[e + o], o);
-      float *s0 = sD + grp * 32 + lane, *s1 = s0 + 128;
-      const float col = v[0];
-      if (quarter == 1) *s0 = col;
-      if (quarter == 3) *s1 = col;
-      if (!meet()) return false;
-      if (quarter == 0) *s0 = col + *s0;
-      if (quarter == 2) *s1 = col + *s1;
-      return meet();  // (who reads adds the two)
+      for (int e = 0; e < 32; ++e) dp[e] = mine ? dp[e] : 0.f;
+      if (g > 0 && !mbar_wait_warp(ds_free, (g - 1) & 1, status, kSiteCross)) return false;
+      auto both = [&](float a, float b, int o) {
+        return (lane & o ? b : a) + __shfl_xor_sync(0xffffffffu, lane & o ? a : b, o);
+      };
+      // (depth first: few sums at a time are in registers)
+      auto sum16 = [&](int e) { return both(p[e] * dp[e], p[e + 16] * dp[e + 16], 16); };
+      auto sum8 = [&](int e) { return both(sum16(e), sum16(e + 8), 8); };
+      auto sum4 = [&](int e) { return both(sum8(e), sum8(e + 4), 4); };
+      auto sum2 = [&](int e) { return both(sum4(e), sum4(e + 2), 2); };
+      *part(quarter) = both(sum2(0), sum2(1), 1);
+      if (!meet(0)) return false;
+      if (quarter == 0)
+        sD[(g & 1) * 128 + grp * 32 + lane] = (*part(0) + *part(1)) + (*part(2) + *part(3));
+      return meet(1);
     };
     // dV and dK of the item before, in TMEM until its last products are done,
     // or (keys that no query sees) zeros.
@@ -637,10 +645,10 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
       if (count < 0) break;
       const int q0 = it.q0, queries = it.queries, hk = it.hk, first = it.first;
       const bool edge = it.real < 128, mine = t < it.real;
-      const bool only = it.real == 1 && it.kb == 0;
+      const bool whole = WHOLE || it.whole;
       for (int i = 0; i < count; ++i, ++g) {
         const float* l2 = sL + (g & 1) * 128 + grp * 32;
-        const float* dl = sD + (WHOLE ? 0 : (g & 1) * 128) + grp * 32;
+        const float* dl = sD + (g & 1) * 128 + grp * 32;
         if (!mbar_wait_warp(&lse_ready[g & 1], (g >> 1) & 1, status, kSiteCross) ||
             !mbar_wait_warp(s_full, g & 1, status, kSiteCross)) {
           ok = false;
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         if (edge) {  // (keys behind the sequence)
 #pragma unroll
           for (int e = 0; e < 32; ++e) p[e] = mine ? p[e] : 0.f;
-          if (only) {  // the weight of a sequence's only key is 1, and dz = dP - dP
+          if (whole && it.real == 1) {  // the weight of a sequence's only key is 1, and dz = dP - dP
 #pragma unroll
             for (int e = 0; e < 32; ++e) p[e] = rintf(p[e]);
           }
@@ -693,6 +701,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           break;
         }
         tc_fence_after();
+        if (whole && !(ok = sum_delta(p, mine, g))) break;
         uint32_t pp[16];  // dz
         {
           float dv[32];
@@ -700,13 +709,6 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
           if (edge) {  // (V behind the sequence may be anything)
 #pragma unroll
             for (int e = 0; e < 32; ++e) dv[e] = mine ? dv[e] : 0.f;
-            if (!WHOLE && only) {  // (P = 0 leaves the others at 0)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) dv[e] = dl[e];
-            }
-          }
-          if constexpr (WHOLE) {
-            if (!(ok = sum_delta(p, dv))) break;
           }
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
@@ -714,11 +716,7 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               const int at = gr * 16 + e;
-              float4 dlv = *reinterpret_cast<const float4*>(dl + at);
-              if constexpr (WHOLE) {
-                const float4 more = *reinterpret_cast<const float4*>(dl + 128 + at);
-                dlv.x += more.x, dlv.y += more.y, dlv.z += more.z, dlv.w += more.w;
-              }
+              const float4 dlv = *reinterpret_cast<const float4*>(dl + at);
               const float* dq = dv + gr * 16 + e;
               const float2 d0 = __fmul2_rn(make_float2(p[at], p[at + 1]),
                                            __fadd2_rn(make_float2(dq[0], dq[1]),
