@@ -72,6 +72,7 @@ class TransformerLayer:
         self.grads = {k: torch.zeros(v, dtype=torch.float32, device=self.device)
                       for k, v in shapes.items()}
         self._grads_c = L.make_grads(self.grads)
+        self._norm_grads = {}
         if qk_norm is not None:
             self._set_norm(qk_norm)
         self._x = None
@@ -101,14 +102,20 @@ class TransformerLayer:
         names = ("q_norm_g", "q_norm_b", "k_norm_g", "k_norm_b")
         d = self.shape.head_dim or self.hidden // self.shape.heads
         for name, x in zip(names, norm.tensors):
-            if x is not None and name not in self.grads:
-                self.grads[name] = torch.zeros(d, dtype=torch.float32, device=self.device)
-        gq, bq, gk, bk = (self.grads.get(n) if x is not None else None
-                          for n, x in zip(names, norm.tensors))
+            if x is None:
+                self.grads.pop(name, None)
+            elif name not in self.grads:
+                # (the same memory as before: a captured step may still write there)
+                if name not in self._norm_grads:
+                    self._norm_grads[name] = torch.empty(d, dtype=torch.float32, device=self.device)
+                self.grads[name] = self._norm_grads[name].zero_()
+        gq, bq, gk, bk = (self.grads.get(n) for n in names)
         self.qk_norm = L.make_layer_qk_norm(norm, L.make_qk_norm_grads(gq, gk, bq, bk))
 
     def set_qk_norm(self, norm):
-        """Other gains, shifts or eps (make_qk_norm) for a layer built with norms."""
+        """Other gains, shifts or eps (make_qk_norm) for a layer built with norms.
+        ``grads`` keeps the entries of those that the new norm has too, loses the
+        others, and gets zeros for new ones."""
         if self.qk_norm is None:
             raise ValueError("the layer was built without norms of Q and K: it keeps no room for them")
         if norm is None:
