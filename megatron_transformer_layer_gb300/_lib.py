@@ -554,10 +554,10 @@ def _rotary(rotary, shape):
     return ctypes.byref(rotary)
 
 
-def _is_bf16(x):
+def _is_bf16(x, what="rotary positions"):
     import torch
     if x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"rotary positions take bf16 or fp32, got {x.dtype}")
+        raise TypeError(f"{what} take bf16 or fp32, got {x.dtype}")
     return 1 if x.dtype == torch.bfloat16 else 0
 
 
@@ -626,6 +626,29 @@ def _turning(positions, inv_freq, spec, tokens):
             _array(inv_freq, "inv_freq", "float32", spec.rot_dim // 2), ctypes.byref(spec))
 
 
+def _token_rows(x, what, tokens, ld, width):
+    """Pointer of a tensor whose `tokens` rows of `width` elements lie ld apart: of
+    rows, of heads [tokens, heads, head_dim], or of any contiguous shape whose last
+    dimension rows are whole numbers of."""
+    try:
+        (n, w), (s0, s1) = x.shape, x.stride()
+        if n >= tokens and w >= width and s1 == 1 and (s0 == ld or tokens == 1) and x.is_cuda:
+            return x.data_ptr()
+    except ValueError:  # not two dimensions
+        pass
+    if not x.is_cuda:
+        raise ValueError(f"{what}: a tensor on the GPU expected, got one on {x.device}")
+    if x.dim() > 1 and x.stride(0) == ld and x.shape[0] >= max(tokens, 1):
+        covers = x[0].is_contiguous() and x[0].numel() >= width
+    else:
+        covers = x.dim() > 0 and x.is_contiguous() and x.numel() >= (tokens - 1) * ld + width and \
+            (x.dim() == 1 or tokens == 1 or (x.shape[-1] > 0 and ld % x.shape[-1] == 0))
+    if not covers:
+        raise ValueError(f"{what}: {tokens} rows of {width} elements, {ld} apart, expected, got shape "
+                         f"{tuple(x.shape)}, strides {x.stride()}")
+    return x.data_ptr()
+
+
 def mc_qk_norm_forward(x, out, tokens, q_heads, k_heads, head_dim, ld_in, ld_out, norm,
                        positions=None, inv_freq=None, spec=None, status=None, stream=None) -> int:
     """Norms (and, with a spec, rotary positions) over q_heads + k_heads heads at
@@ -633,7 +656,10 @@ def mc_qk_norm_forward(x, out, tokens, q_heads, k_heads, head_dim, ld_in, ld_out
     x itself)."""
     if out.dtype != x.dtype:
         raise TypeError(f"norms of queries and keys: {x.dtype} in, {out.dtype} out")
-    return lib().mc_qk_norm_forward(_ptr(x), _ptr(out), _is_bf16(x), tokens, q_heads, k_heads,
+    width = (q_heads + k_heads) * head_dim
+    return lib().mc_qk_norm_forward(_token_rows(x, "x", tokens, ld_in, width),
+                                    _token_rows(out, "out", tokens, ld_out, width),
+                                    _is_bf16(x, "norms of queries and keys"), tokens, q_heads, k_heads,
                                     head_dim, ld_in, ld_out,
                                     _norm_ref(norm, "norm", q_heads, k_heads, head_dim),
                                     *_turning(positions, inv_freq, spec, tokens), _ptr(status),
@@ -654,7 +680,11 @@ def mc_qk_norm_backward(x, dout, din, tokens, q_heads, k_heads, head_dim, ld_in,
         raise TypeError(f"norms of queries and keys: {x.dtype} in, {dout.dtype} and {din.dtype} "
                         "for its gradients")
     need = 0 if grads is None else mc_qk_norm_scratch_floats(tokens, q_heads, k_heads, head_dim)
-    return lib().mc_qk_norm_backward(_ptr(x), _ptr(dout), _ptr(din), _is_bf16(x), tokens, q_heads,
+    width = (q_heads + k_heads) * head_dim
+    return lib().mc_qk_norm_backward(_token_rows(x, "x", tokens, ld_in, width),
+                                     _token_rows(dout, "dout", tokens, ld_dout, width),
+                                     _token_rows(din, "din", tokens, ld_din, width),
+                                     _is_bf16(x, "norms of queries and keys"), tokens, q_heads,
                                      k_heads, head_dim, ld_in, ld_dout, ld_din,
                                      _norm_ref(norm, "norm", q_heads, k_heads, head_dim),
                                      *_turning(positions, inv_freq, spec, tokens),
