@@ -683,8 +683,9 @@ int mc_qk_norm_backward(const void* in, const void* dout, void* din, int32_t is_
  * attention may be NULL; qk_norm NULL is mc_layer_forward_opt / _backward_opt,
  * to the bit): after the QKV projection Q and K are normed, and turned by
  * `rotary`, in one pass.  The backward call writes the gradients that qk_norm->
- * grads asks for (adds them with MC_ACCUMULATE_GRADS); the forward call does not
- * read them.  Q and K as they come from the projection are kept in `saved`,
+ * grads asks for (adds them with MC_ACCUMULATE_GRADS); the forward call writes
+ * none, but both check the pointers: NULL or 4-byte aligned, in an inference
+ * program too.  Q and K as they come from the projection are kept in `saved`,
  * which grows by them: mc_layer_saved_bytes_norm, mc_layer_workspace_bytes_norm
  * (of qk_norm only whether it is NULL is read).  All shape flags combine with
  * it. */
