@@ -49,7 +49,7 @@ int check_cross(const mc_cross_attention* c) {
       !aligned(c->kv_lens, 4))
     return MC_ERR_ALIGN;
   if (!(c->scale == 0.f || (c->scale >= 0x1p-16f && c->scale <= 0x1p16f))) return MC_ERR_ARGUMENT;
-  // items are counted in 32 bits
+  // items, and twice of them (the launches' shares), are counted in 32 bits
   const int64_t pq = 128 / (c->heads / c->kv_heads);
   auto most = [&](const int32_t* off, int64_t rows, int64_t bound) {
     return !off ? rows / c->sequences : bound > 0 && bound < rows ? bound : rows;
@@ -57,7 +57,7 @@ int check_cross(const mc_cross_attention* c) {
   const int64_t nqb = (most(c->q_offsets, c->q_rows, c->max_q) + pq - 1) / pq,
                 nkb = (most(c->kv_offsets, c->kv_rows, c->max_kv) + 127) / 128;
   const int64_t longest = nqb > nkb ? nqb : nkb;
-  if (longest * c->sequences > (1ll << 30) / c->kv_heads) return MC_ERR_UNSUPPORTED;
+  if (longest * c->sequences * c->kv_heads >= (1ll << 30)) return MC_ERR_UNSUPPORTED;
   return MC_OK;
 }
 
