@@ -727,9 +727,11 @@ int mc_layer_backward_norm(const mc_layer_shape* shape, const mc_layer_weights* 
  * h / (heads / kv_heads); its rows are ld_q elements apart in Q, ld_o in O, and
  * those of K and V ld_kv.  K and V of a packed projection K | V: v = k +
  * kv_heads head_dim, ld_kv = 2 kv_heads head_dim.  max_q and max_kv bound the
- * rows of a sequence (0: not known) where offsets are given; a sequence with
- * more is reported as MC_ERR_DEVICE_BOUNDS, and then no result of the call is
- * valid.  Outputs overlap neither one another nor an input. */
+ * rows of a sequence where offsets are given; a sequence with more is reported
+ * as MC_ERR_DEVICE_BOUNDS, and then no result of the call is valid.  0: not known,
+ * for few rows only: every sequence then counts as long as all rows together, in
+ * the items that the launches walk, nearly all of them empty, and in the backward
+ * pass's workspace (sequences times the product of all blocks).  Outputs overlap neither one another nor an input. */
 typedef struct mc_cross_attention {
   int32_t sequences;
   int32_t heads, kv_heads; /* kv_heads divides heads, by at most 128 */

@@ -121,7 +121,6 @@ class mc_layer_qk_norm(ctypes.Structure):  # noqa: N801
 
 
 class mc_cross_attention(ctypes.Structure):  # noqa: N801
-    lengths = (1 << 62,) * 4  # of the four arrays (make_cross_attention)
     _fields_ = [("sequences", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("q_rows", ctypes.c_int32), ("kv_rows", ctypes.c_int32),
@@ -745,7 +744,9 @@ def make_cross_attention(sequences, q_rows, kv_rows, heads, kv_heads, head_dim, 
                          ld_kv=None, ld_o=None, q_offsets=None, q_lens=None, kv_offsets=None,
                          kv_lens=None, max_q=0, max_kv=0, scale=0.0):
     """Row strides default to the heads' own width.  Offsets int32 [sequences +
-    1], lengths int32 [sequences].  Keeps a reference to the tensors."""
+    1], lengths int32 [sequences].  With offsets state max_q and max_kv, the most
+    rows of a sequence: without them each counts as long as all rows together, in
+    the backward pass's workspace too.  Keeps a reference to the tensors."""
     arrays = (q_offsets, q_lens, kv_offsets, kv_lens)
     names = ("q_offsets", "q_lens", "kv_offsets", "kv_lens")
     out = mc_cross_attention(
