@@ -652,7 +652,8 @@ typedef struct mc_qk_norm {
  * a cross attention lie in rows of their own).  Rows, types, positions and
  * in-place use as mc_rotary_forward; spec NULL: nothing turns, positions and
  * inv_freq are not read.  Sums are 32-bit: the squares of a head must not
- * overflow there. */
+ * overflow there.  What a head with an infinity or a NaN becomes is not defined;
+ * no other head is touched by it (its type's gradients of gain and shift are). */
 int mc_qk_norm_forward(const void* in, void* out, int32_t is_bf16, int64_t tokens,
                        int32_t q_heads, int32_t k_heads, int32_t head_dim, int64_t ld_in,
                        int64_t ld_out, const mc_qk_norm* norm, const int32_t* positions,
@@ -731,7 +732,8 @@ int mc_layer_backward_norm(const mc_layer_shape* shape, const mc_layer_weights* 
  * as MC_ERR_DEVICE_BOUNDS, and then no result of the call is valid.  0: not known,
  * for few rows only: every sequence then counts as long as all rows together, in
  * the items that the launches walk, nearly all of them empty, and in the backward
- * pass's workspace (sequences times the product of all blocks).  Outputs overlap neither one another nor an input. */
+ * pass's workspace (32 sequences of 512 queries and keys, 8 heads of 128: 237 us
+ * forward against 45, 17 GB against 0.13).  Outputs overlap neither one another nor an input. */
 typedef struct mc_cross_attention {
   int32_t sequences;
   int32_t heads, kv_heads; /* kv_heads divides heads, by at most 128 */
