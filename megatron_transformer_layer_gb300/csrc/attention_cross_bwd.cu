@@ -14,9 +14,11 @@
 //          again).
 // Key heads are taken in groups whose tiles fit the workspace.
 //
-// 4096 queries to 8192 keys, 16 heads of 128: delta 10 us, dkdv 490 (4,500 clocks a pair of
-// blocks, of which its four products take 2,048: the chain of S^T, P, dP and dz is
-// longer than they are), dq 180 (6 TB/s).  Nine packed sequences of up to 700 queries
+// 4096 queries to 8192 keys, 16 heads of 128: delta 10 us, dkdv 490-500 (4,500 clocks a
+// pair of blocks; its four products are 2,048 at the tensor pipe's rate, and some 3,100
+// with their operands of 128 x 128 out of shared memory, which the loads and the tile's
+// way out share, about 320 KB a pair: what is beyond is the chain of S^T, P, dP and dz),
+// dq 180 (6 TB/s); heads of 64: 533 us in all, floor 176.  Nine packed sequences of up to 700 queries
 // of 64 heads and 900 keys of 8: 25 (5.4 TB/s), 229 and 78 us; the tiles are 340 of
 // dkdv's 570 MB and most of dq's.
 //

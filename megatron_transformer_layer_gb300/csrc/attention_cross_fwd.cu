@@ -27,14 +27,14 @@
 // that, sums and statistics are 32-bit, and O is rounded once more when stored.
 //
 // Bound by the tensor cores and by what their products wait for: 4096 queries to 8192
-// keys, 64 heads of 128, 750-800 us = 1.37-1.47 PFLOP/s, 3,400-3,600 clocks a block of
-// which the products take 2,048; loading S, the exchange of maxima and the write of P
-// stand between the softmax of one block and the next.  Not kept there: a maximum that
-// lags a block behind (768 us), warps of their own for the store of O (784), K in three
-// halves and two tiles of Q (790), two CTAs per SM (840), a part of the exponentials as
-// polynomials on the multiply-add units (an eighth 768, three 849: those are busier than
-// the exponential unit).  32 x 1 query to lengths up to 8192 (8 key heads, 4.2 MB an item):
-// 5.9-6.1 TB/s; equal lengths 6.8, a copy's rate.
+// keys, 64 heads of 128, 750 us on the same inputs again, 800 on others each time =
+// 1.47 and 1.37 PFLOP/s, 3,400-3,600 clocks a block of which the products take 2,048;
+// loading S, the exchange of maxima and the write of P stand between the softmax of one
+// block and the next.  Not kept there: a maximum that lags a block behind (768 us), warps
+// of their own for the store of O (784), K in three halves and two tiles of Q (790), two
+// CTAs per SM (840), a part of the exponentials as polynomials on the multiply-add units
+// (an eighth 768, three 849).  32 x 1 query to lengths up to 8192 (8 key heads, 4.2 MB an
+// item): 5.9-6.1 TB/s; equal lengths 6.8, a copy's rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,12 +51,17 @@ constexpr int kXFwdThreads = 384;
 constexpr int kXRegsIo = 72, kXRegsSoftmax = 216;
 constexpr int kXKeys = 256;  // keys per block
 constexpr int kXRing = 4;    // items in shared memory
-// Up to so many keys two CTAs per SM take the items (attention_cross_pair.cu): at
-// D = 128, 4 x 1037 queries of 64 heads, 333 keys 67 us against 94 of this kernel, 900
-// keys 135 against 144, 960 138 against 141, 1024 139 against 136; one query of 8 heads
-// to ragged lengths up to 8192 (32 of them) 120 against 96.  At D = 64 always, where P
-// has columns of its own there: 333 keys 52 against 86, 8192 keys 552 against 655, one
-// query to 300 (300 sequences, 12 heads) 63 against 144.
+// Up to so many keys two CTAs per SM take the items (attention_cross_pair.cu).  At
+// D = 128 (equal lengths, the same inputs again), 4 x 1037 queries of 64 heads: 128 keys
+// 36 us against 80 of this kernel, 256 51 against 68, 333 68 against 95, 512 81 against
+// 91, 900 135 against 145, 960 139 against 142, 1024 139 against 136.  (A block of 256
+// keys that is not full is selected and exponentiated in full here, so that 128 keys
+// take longer than 256.)  One query of each of 32 sequences, 64 heads on 8 key heads:
+// 300 keys 12 against 17, 960 25 against 27, ragged lengths up to 8192 120 against 96.
+// Where no heads share the keys or items are fewer than SMs one query is slower: 30
+// sequences, 900 keys, 32 heads 84 against 74; 12 sequences, 8 heads 18 against 15.  At
+// D = 64 always, where P has columns of its own there: 333 keys 52 against 86, 8192 keys
+// 552 against 655, one query to 300 (300 sequences, 12 heads) 63 against 144.
 constexpr int kXPairKeys = 960;
 // O is rescaled only when a row's maximum grows by more than this (log2
 // units): P stays below 2^8 and the final division by the sum, taken against

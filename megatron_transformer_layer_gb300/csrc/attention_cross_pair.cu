@@ -14,10 +14,13 @@
 // until its product is complete.
 //
 // What bounds it: S, softmax and product of a block are a chain of some 3,000 clocks at
-// D = 128, of which the two CTAs overlap two (4 x 1037 queries of 64 heads: 128 keys 35
-// us, 256 51 us, 512 80 us; two threads to a row, which then exchange maxima: 19%
-// slower); the instructions of the softmax where S runs ahead (D = 64: 4096 to 8192 keys
-// 552 us; a part of the exponentials as polynomials, an eighth of them, 10% slower).
+// D = 128, of which the two CTAs overlap two (4 x 1037 queries of 64 heads, the same
+// inputs again: 128 keys 36 us, 256 51 us, 512 81 us; two threads to a row, which then
+// exchange maxima: 19% slower).  At D = 64, where S runs ahead, no unit is full: 4096
+// queries to 8192 keys, 16 heads, issue 46% of the slots, the tensor pipe is active 39%
+// of the time, the exponentials' pipe 39%, multiply-adds 23%; what is left are waits
+// between a row's softmax and the products (64 heads: 552-568 us, floor 282; a part of
+// the exponentials as polynomials, an eighth of them, was 10% slower).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -145,8 +145,11 @@ __device__ __forceinline__ RotVec<T, VEC> pack(const P* f) {
 // of a head turned in adjacent pairs, 50.4 us = 3.3 TB/s at 330: a warp has some 35 turns
 // there, each a chain of two sums over the lanes, four warps to a scheduler, which
 // issues 42% of the time.  Two turns side by side in a warp were slower (57 against 53 us:
-// more registers), more warps of fewer registers too (60).  Backward 86 us = 4.7 TB/s for the first shape; 18 us for 2036 tokens of
-// 24 heads of 64, of which the sums of the gradients over blocks take 7.
+// more registers), more warps of fewer registers too (60).  Backward 86 us = 4.7 TB/s for
+// the first shape; 18 us for 2036 tokens of 24 heads of 64, of which the sums of the
+// gradients over blocks take 7.  fp32, the first shape: 99 us = 5.4 TB/s, backward 137 =
+// 5.9.  Vectors of two elements or one (no ring, each load waited for): bf16 164 and 241
+// us, fp32 172 and 249, backward bf16 340 and 388.
 template <typename T, int VEC, bool ADJACENT, bool BACK, bool SHIFT>
 __global__ void __launch_bounds__(NormCfg<BACK>::kWarps * 32, NormCfg<BACK>::kBlocks)
     qk_norm_kernel(const T* in, const T* dout, T* out, const int32_t* __restrict__ positions,
