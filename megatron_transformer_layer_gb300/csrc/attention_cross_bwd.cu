@@ -625,8 +625,9 @@ __global__ void __launch_bounds__(kXKvThreads, 1)
         const float sc = w == 0 ? 1.f : A.scale;
         uint16_t* base = (w == 0 ? B.dv : B.dk) +
                          (static_cast<int64_t>(k0) + quarter * 32) * A.ld_kv + hk * D;
-        const bool in_range =
-            MC_DCHECK(k0 + slot <= A.kv_rows && hk < A.KV, status, kSiteCross);
+        // (a block behind its sequence has no rows, and may start behind all rows)
+        const bool in_range = MC_DCHECK(slot == 0 || (k0 + slot <= A.kv_rows && hk < A.KV),
+                                        status, kSiteCross);
         float v[32] = {};
         if (from_tmem) {
           tmem_ld_32x32b_x32((w == 0 ? tdV : tdK) + lane_off + c * 32, v);

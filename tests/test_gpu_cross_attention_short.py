@@ -1,5 +1,9 @@
 """Gradients of sequences with few keys: as exact, and the same to the bit, whatever
 other sequences the call has and whatever bounds or slots it states for them."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +12,7 @@ import oracle.cross_attention as O
 from megatron_transformer_layer_gb300 import _lib as L
 
 from gpu_util import DEV, check_status, status, to_f64
+from test_gpu_attention_opt_debug import TESTS, digest
 from test_gpu_cross_attention import Problem
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +103,45 @@ def test_bounds_do_not_change_bits():
     for bounds in (dict(max_q=sq, max_kv=129), dict(max_q=4 * sq), {}):
         again = backward(p, (0, 4 * sq), (0, off[-1]), **bounds, **rows)
         assert all(torch.equal(x, y) for x, y in zip(first, again)), bounds
+
+
+# a cluster shares the queries of a key block (few key blocks, many queries), of which
+# some hold all keys of their sequence and some do not
+SHARED = [(2, 1500, 300, 2, 1, 128, [300, 9]), (3, 1100, 200, 4, 1, 64, [128, 200, 2]),
+          (1, 4000, 131, 2, 2, 64, [3]), (4, 700, 260, 3, 1, 128, [1, 129, 0, 128])]
+
+
+def shared(n, sq, sk, heads, kv_heads, d, lens):
+    return Problem(n, n * sq, n * sk, heads, kv_heads, d, kv_lens=lens,
+                   q_lens=[sq - 7 * i for i in range(n)])
+
+
+@pytest.mark.parametrize("case", SHARED)
+def test_shares_of_queries(case):
+    p = shared(*case).check()
+    first = p.dq_all.clone(), p.dkv_all.clone()
+    for _ in range(3):
+        p.backward()
+        assert torch.equal(p.dq_all, first[0]) and torch.equal(p.dkv_all, first[1])
+
+
+def results():
+    """Digests of the gradients (a call's status is checked) in this build."""
+    out = []
+    for p in [shared(*c) for c in SHARED] + list(problems(128, 6, 2, 33)):
+        p.forward()
+        p.backward()
+        out.append(digest(p.o_all, p.lse, p.dq_all, p.dkv_all))
+    return out
+
+
+def test_debug_build_is_clean_and_matches_release():
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "from megatron_transformer_layer_gb300 import _lib as L\n"
+            "assert L.LIB_PATH.endswith('_debug.so')\n"
+            "from test_gpu_cross_attention_short import results\n"
+            "for r in results(): print(r)\n") % (os.path.dirname(TESTS), TESTS)
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=600,
+                         env=dict(os.environ, MC_LAYER_DEBUG="1"))
+    assert out.returncode == 0, out.stderr[-2000:]
+    assert out.stdout.split() == results()
