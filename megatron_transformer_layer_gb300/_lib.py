@@ -117,6 +117,7 @@ class mc_qk_norm_grads(ctypes.Structure):  # noqa: N801
 
 
 class mc_layer_qk_norm(ctypes.Structure):  # noqa: N801
+    parts = (None, None)  # norm and gradients with their lengths (make_layer_qk_norm)
     _fields_ = [("norm", mc_qk_norm), ("grads", mc_qk_norm_grads)]
 
 

@@ -18,9 +18,9 @@
 // pair of blocks; its four products are 2,048 at the tensor pipe's rate, and some 3,100
 // with their operands of 128 x 128 out of shared memory, which the loads and the tile's
 // way out share, about 320 KB a pair: what is beyond is the chain of S^T, P, dP and dz),
-// dq 180 (6 TB/s); heads of 64: 533 us in all, floor 176.  Nine packed sequences of up to 700 queries
-// of 64 heads and 900 keys of 8: 25 (5.4 TB/s), 229 and 78 us; the tiles are 340 of
-// dkdv's 570 MB and most of dq's.
+// dq 180 (6 TB/s); heads of 64: 533 us in all, floor 176.  Nine packed sequences of up to
+// 700 queries of 64 heads and 900 keys of 8: 25 (5.4 TB/s), 229-235 and 78 us; the tiles
+// are 340 of dkdv's 570 MB and most of dq's.
 //
 // P and dz are rounded to bf16, each by at most 2^-8 of itself: an operand of a
 // tcgen05 product has the type of the other one, dO's, Q's and K's.  dK and dQ

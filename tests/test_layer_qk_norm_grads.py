@@ -29,6 +29,14 @@ def test_entries_follow_the_norm(monkeypatch):
     assert offered(layer) == list(NAMES)
 
 
+def test_a_structure_of_bare_pointers():
+    """Filled field by field, as a C program would: the library's own checks come first."""
+    n = L.mc_layer_qk_norm(L.mc_qk_norm(P, None, P, None, 0.0, 0))
+    sh = L.make_shape(1, 64, 768, 12, 2304)
+    rc = L.mc_layer_forward_norm(sh, L.mc_layer_weights(*[P] * 12), n, None, None, P, P, P, P, 1 << 40)
+    assert rc == L.MC_ERR_ARGUMENT  # (eps)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_no_gradient_of_an_earlier_norm(accumulate):
